@@ -55,6 +55,13 @@ from ._binding import (  # noqa: F401
     version,
 )
 
+from ._scored import (  # noqa: E402,F401
+    attn_jvp_bwd_scored,
+    attn_jvp_fwd_scored,
+    attn_jvp_fwd_scored_stats,
+    bwd_scored_workspace_bytes,
+    key_bounds,
+)
 from .autograd import AttnJvpFunction, attn_jvp_autograd  # noqa: E402,F401
 
 __all__ = [
@@ -67,4 +74,6 @@ __all__ = [
     "load_library", "selftest_wait_timeout", "set_bwd_pairs", "set_persistent_key_tiles", "DEFAULT_BWD_PAIRS",
     "DEFAULT_PERSISTENT_KEY_TILES",
     "set_wait_bound_ns", "strerror", "version", "AttnJvpError",
+    "attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored", "bwd_scored_workspace_bytes",
+    "key_bounds",
 ]

@@ -38,7 +38,8 @@ EXPORTED = (
     "attn_jvp_strerror", "attn_jvp_last_cuda_error", "attn_jvp_check_device_status",
     "attn_jvp_set_wait_bound_ns", "attn_jvp_set_persistent_key_tiles", "attn_jvp_set_bwd_pairs",
     "attn_jvp_selftest_wait_timeout",
-    "attn_jvp_version",
+    "attn_jvp_version", "attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored",
+    "attn_jvp_bwd_scored_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -121,6 +122,14 @@ def load_library(path: str = LIB_PATH):
         lib.attn_jvp_set_bwd_pairs.restype = ctypes.c_int
         lib.attn_jvp_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
         lib.attn_jvp_selftest_wait_timeout.restype = ctypes.c_int
+        lib.attn_jvp_fwd_scored.argtypes = [vp] * 12 + [i64] * 6 + [f32, f32, vp]
+        lib.attn_jvp_fwd_scored.restype = ctypes.c_int
+        lib.attn_jvp_fwd_scored_stats.argtypes = [vp] * 13 + [i64] * 6 + [f32, f32, vp]
+        lib.attn_jvp_fwd_scored_stats.restype = ctypes.c_int
+        lib.attn_jvp_bwd_scored.argtypes = [vp] * 21 + [i64] * 6 + [f32, f32, vp, ctypes.c_uint64, vp]
+        lib.attn_jvp_bwd_scored.restype = ctypes.c_int
+        lib.attn_jvp_bwd_scored_workspace_bytes.argtypes = [i64] * 5
+        lib.attn_jvp_bwd_scored_workspace_bytes.restype = ctypes.c_uint64
         lib.attn_jvp_version.argtypes = []
         lib.attn_jvp_version.restype = ctypes.c_int
         _lib = lib

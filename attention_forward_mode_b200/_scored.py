@@ -1,0 +1,188 @@
+"""ctypes binding of the score-modified attention + JVP: a tanh cap, a bias by
+distance, an interval of visible keys per query row, and shared key heads
+(``attn_jvp_fwd_scored``, ``attn_jvp_fwd_scored_stats``, ``attn_jvp_bwd_scored``),
+and ``key_bounds``, which writes the usual masks as such intervals.
+Argument marshalling only, as in ``_binding``."""
+from __future__ import annotations
+
+import torch
+
+from ._binding import GRAD_NAMES, _check, _ptr, load_library
+
+__all__ = ["attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored", "bwd_scored_workspace_bytes",
+           "key_bounds"]
+
+
+def _tensor(name, x, shape, dtype, device=None):
+    """x is a contiguous CUDA tensor of this shape and type (on this device)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype or tuple(x.shape) != tuple(shape) \
+            or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+    if device is not None and x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    return x
+
+
+def _launch_stream(stream, device) -> int:
+    """Handle of ``stream``, by default torch's current stream of ``device``."""
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _sizes(q, k, v, tq, tk, tv):
+    for name, x in (("q", q), ("k", k)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 4:
+            raise ValueError(f"{name} must be a CUDA [B, H, L, d] tensor")
+    B, H, Lq, d = q.shape
+    Hkv, Lk = k.shape[1], k.shape[2]
+    if H and (Hkv < 1 or H % Hkv):
+        raise ValueError(f"query heads ({H}) must be a multiple of the key heads ({Hkv})")
+    for name, x, shape in (("q", q, q.shape), ("tq", tq, q.shape), ("k", k, (B, Hkv, Lk, d)),
+                           ("v", v, (B, Hkv, Lk, d)), ("tk", tk, (B, Hkv, Lk, d)), ("tv", tv, (B, Hkv, Lk, d))):
+        _tensor(name, x, shape, torch.bfloat16, q.device)
+    return B, H, Hkv, Lq, Lk, d
+
+
+def _score_args(slopes, key_begin, key_end, softcap, scale, sizes, device):
+    B, H, _, Lq, _, d = sizes
+    if slopes is not None:
+        _tensor("slopes", slopes, (H,), torch.float32, device)
+    bounds = []
+    for name, x in (("key_begin", key_begin), ("key_end", key_end)):
+        if x is not None:
+            if isinstance(x, torch.Tensor) and x.dim() == 1:  # the same for every sequence of the batch
+                _tensor(name, x, (Lq,), torch.int32, device)
+                x = x.expand(B, Lq).contiguous()
+            _tensor(name, x, (B, Lq), torch.int32, device)
+        bounds.append(x)
+    return slopes, bounds[0], bounds[1], float(softcap or 0.0), float(d ** -0.5 if scale is None else scale)
+
+
+def _fwd(entry, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end, o, to, lse, mu, stream, want_lse,
+         want_mu):
+    sizes = _sizes(q, k, v, tq, tk, tv)
+    B, H, _, Lq, _, _ = sizes
+    dev = q.device
+    slopes, key_begin, key_end, softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
+    o = torch.empty_like(q) if o is None else _tensor("o", o, q.shape, torch.bfloat16, dev)
+    to = torch.empty_like(q) if to is None else _tensor("to", to, q.shape, torch.bfloat16, dev)
+    stat = lambda name, x, want: (_tensor(name, x, (B, H, Lq), torch.float32, dev) if x is not None  # noqa: E731
+                                  else torch.empty((B, H, Lq), device=dev) if want else None)
+    lse, mu = stat("lse", lse, want_lse), stat("mu", mu, want_mu)
+    rows = (_ptr(o), _ptr(to), _ptr(lse)) + ((_ptr(mu),) if want_mu else ())
+    with torch.cuda.device(dev):
+        rc = getattr(load_library(), entry)(_ptr(q), _ptr(k), _ptr(v), _ptr(tq), _ptr(tk), _ptr(tv), *rows,
+                                            _ptr(slopes), _ptr(key_begin), _ptr(key_end), *sizes, scale, softcap,
+                                            _launch_stream(stream, dev))
+    _check(rc, entry)
+    return o, to, lse, mu
+
+
+def attn_jvp_fwd_scored(q, k, v, tq, tk, tv, scale=None, softcap=0.0, slopes=None, key_begin=None, key_end=None,
+                        o=None, to=None, lse=None, stream=None, want_lse=True):
+    """O, tO, lse of attention whose scores are capped (``softcap`` c > 0:
+    c tanh(z / c)), biased by distance (``slopes``, fp32 [H]:
+    -slope |i + Lk - Lq - j|) and limited to the keys ``key_begin[b, i]`` <= j <
+    ``key_end[b, i]`` of query row i (int32 [B, Lq], or [Lq] for every sequence;
+    ``key_bounds`` makes them).  q, tq bf16 [B, H, Lq, 128]; k, v, tk, tv
+    [B, Hkv, Lk, 128] with H a multiple of Hkv.  Rows that see nothing give
+    zeros and lse = -inf.  Asynchronous on ``stream`` (default: the current
+    stream of the tensors' device)."""
+    return _fwd("attn_jvp_fwd_scored", q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end, o, to, lse,
+                None, stream, want_lse, False)[:3]
+
+
+def attn_jvp_fwd_scored_stats(q, k, v, tq, tk, tv, scale=None, softcap=0.0, slopes=None, key_begin=None, key_end=None,
+                              o=None, to=None, lse=None, mu=None, stream=None):
+    """``attn_jvp_fwd_scored`` that also returns mu, for ``attn_jvp_bwd_scored``.
+    Returns (o, to, lse, mu)."""
+    return _fwd("attn_jvp_fwd_scored_stats", q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end, o, to,
+                lse, mu, stream, True, True)
+
+
+def bwd_scored_workspace_bytes(B: int, H: int, Hkv: int, Lq: int, Lk: int) -> int:
+    """Device workspace with which ``attn_jvp_bwd_scored`` may split its key
+    side on the current device."""
+    return int(load_library().attn_jvp_bwd_scored_workspace_bytes(int(B), int(H), int(Hkv), int(Lq), int(Lk)))
+
+
+def attn_jvp_bwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout, scale=None, softcap=0.0, slopes=None,
+                        key_begin=None, key_end=None, grads=None, workspace=None, stream=None):
+    """Gradients of <dout, O> + <dtout, tO> of ``attn_jvp_fwd_scored`` with
+    respect to q, k, v, tq, tk, tv (slopes and cap are constants); o, to, lse,
+    mu from ``attn_jvp_fwd_scored_stats`` with the same options.  ``grads``: an
+    optional dict of preallocated outputs; ``workspace``: a CUDA uint8 tensor
+    of ``bwd_scored_workspace_bytes`` bytes (allocated per call when omitted).
+    Returns a dict dq, dk, dv, dtq, dtk, dtv shaped like the inputs."""
+    sizes = _sizes(q, k, v, tq, tk, tv)
+    B, H, _, Lq, _, _ = sizes
+    dev = q.device
+    slopes, key_begin, key_end, softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
+    for name, x in (("o", o), ("to", to), ("dout", dout), ("dtout", dtout)):
+        _tensor(name, x, q.shape, torch.bfloat16, dev)
+    for name, x in (("lse", lse), ("mu", mu)):
+        _tensor(name, x, (B, H, Lq), torch.float32, dev)
+    grads = dict(grads or {})
+    for name in GRAD_NAMES:
+        like = q if name in ("dq", "dtq") else k
+        if grads.get(name) is None:
+            grads[name] = torch.empty_like(like)
+        _tensor(name, grads[name], like.shape, torch.bfloat16, dev)
+    with torch.cuda.device(dev):
+        handle = _launch_stream(stream, dev)
+        if workspace is None:
+            workspace = torch.empty(max(1, bwd_scored_workspace_bytes(*sizes[:5])), dtype=torch.uint8, device=dev)
+        _tensor("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+        rc = load_library().attn_jvp_bwd_scored(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(tq), _ptr(tk), _ptr(tv), _ptr(o), _ptr(to), _ptr(lse), _ptr(mu),
+            _ptr(dout), _ptr(dtout), *(_ptr(grads[n]) for n in GRAD_NAMES), _ptr(slopes), _ptr(key_begin),
+            _ptr(key_end), *sizes, scale, softcap, _ptr(workspace), workspace.numel(), handle)
+    _check(rc, "attn_jvp_bwd_scored")
+    return grads
+
+
+def key_bounds(Lq: int, Lk: int | None = None, *, causal: bool = False, prefix: int = 0, frame: int = 0,
+               window: int = 0, documents=None, device="cuda"):
+    """(key_begin, key_end), int32 [Lq], of the usual masks.  Query row i stands
+    at key position p = i + Lk - Lq.
+
+    ``documents``: offsets of documents along the keys (a list or tensor,
+    ascending): a row sees its own document only, and nothing before the first
+    or behind the last offset.  Inside its document (else the whole sequence),
+    ``causal`` hides the keys behind p except the document's first ``prefix``
+    ones, ``frame`` (> 0) those behind the end of p's frame of that many keys,
+    and ``window`` (> 0) all but the last ``window`` keys up to p.
+    """
+    Lk = Lq if Lk is None else Lk
+    if Lq < 0 or Lk < 1 or prefix < 0 or frame < 0 or window < 0 or (causal and frame):
+        raise ValueError("sizes must not be negative, and a mask is causal by keys or by frames")
+    if prefix and not causal:
+        raise ValueError("prefix belongs to the causal mask")
+    p = torch.arange(Lq, device=device, dtype=torch.int64) + (Lk - Lq)
+    begin, end = torch.zeros_like(p), torch.full_like(p, Lk)
+    inside = (p >= 0) | torch.tensor(not (causal or frame), device=device)
+    if documents is not None:
+        cu = torch.as_tensor(documents, device=device, dtype=torch.int64)
+        if cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError("documents are at least two offsets")
+        at = torch.searchsorted(cu, p, right=True) - 1  # the last offset that is not behind p
+        inside = (at >= 0) & (at < cu.numel() - 1)
+        at = at.clamp(0, cu.numel() - 2)
+        begin, end = cu[at], cu[at + 1].clamp(max=Lk)
+    first = begin
+    if causal:
+        end = torch.minimum(end, torch.maximum(p + 1, first + prefix))
+    if frame:
+        end = torch.minimum(end, first + (torch.div(p - first, frame, rounding_mode="floor") + 1) * frame)
+    if window:
+        begin = torch.maximum(first, p - window + 1)
+    if causal and documents is None and prefix:
+        inside = torch.ones_like(inside)
+    zero = torch.zeros_like(p)
+    begin, end = torch.where(inside, begin, zero), torch.where(inside, end, zero)
+    return begin.to(torch.int32), end.to(torch.int32)

@@ -1,6 +1,6 @@
 """Build the CUDA library in-tree: ``attention_forward_mode_b200/libattnjvp.so``.
 
-One nvcc invocation for sm_100a (B200) with line info; the C ABI symbols are
+One nvcc invocation for sm_100a (B200) with line info, the sources compiled side by side; the C ABI symbols are
 the only exported ones.  Usage: ``python -m attention_forward_mode_b200.build``.
 """
 from __future__ import annotations
@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libattnjvp.so")
-SOURCES = [os.path.join(HERE, "csrc", "api.cu")]
+SOURCES = [os.path.join(HERE, "csrc", n) for n in ("api.cu", "scored.cu")]
 DEPS = sorted(glob.glob(os.path.join(HERE, "csrc", "*")) + [os.path.join(ROOT, "include", "attn_jvp.h")])
 
 
@@ -27,7 +27,7 @@ def nvcc_path() -> str:
 
 def command(out: str = LIB, extra=()) -> list[str]:
     return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-            "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "-I" + os.path.join(ROOT, "include"),
+            "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared", "--threads", str(len(SOURCES)), "-I" + os.path.join(ROOT, "include"),
             *extra, "-o", out, *SOURCES]
 
 

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "attn_jvp.h"
+#include "host_common.h"
 #include "jvp_bwd_sm100.cuh"
 #include "jvp_f32.cuh"
 #include "jvp_sm100.cuh"
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kVersion = 100;  // 0.1.0
 constexpr uint64_t kDefaultBoundNs = 2000000000ull;
-constexpr int kMaxDevices = 64;
+using ajvp::host::kMaxDevices;
 
 thread_local int t_last_cuda_error = 0;
 std::atomic<uint64_t> g_bound_ns{kDefaultBoundNs};
@@ -624,6 +625,22 @@ int64_t fwd_host_heads_per_chunk(int64_t BH, int64_t Lq, int64_t Lk, int64_t d, 
 
 }  // namespace
 
+namespace ajvp {
+namespace host {
+int fail(cudaError_t e) { return fail_cuda(e); }
+int device(int *dev) { return device_setup(dev); }
+int sm_count(int dev) { return g_dev[dev].sm_count; }
+int encoder() { return get_encoder(); }
+uint64_t wait_bound_ns() { return g_bound_ns.load(); }
+int encode(CUtensorMap *m, const void *ptr, int64_t d, int64_t L, int64_t BH, uint32_t box_rows) {
+    return encode_3d(m, ptr, d, L, BH, box_rows);
+}
+int64_t key_split(int64_t BH, int64_t Lq, int64_t Lk, int sm_count) { return bwd_key_split(BH, Lq, Lk, sm_count); }
+uint64_t stats_bytes(int64_t BH, int64_t Lq) { return bwd_stats_bytes(BH, Lq); }
+uint64_t partial_bytes(int64_t BH, int64_t Lk, int64_t parts) { return bwd_partial_bytes(BH, Lk, parts); }
+}  // namespace host
+}  // namespace ajvp
+
 extern "C" {
 
 int attn_jvp_fwd(const void *q, const void *k, const void *v, const void *tq, const void *tk, const void *tv,
@@ -1041,8 +1058,10 @@ int attn_jvp_check_device_status(void *stream) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(ajvp::g_status_word, &zero, sizeof(int));
         if (e != cudaSuccess) return fail_cuda(e);
-        return (word & 2) ? AJVP_ERR_DEVICE_LAYOUT : AJVP_ERR_TIMEOUT;
     }
+    e = ajvp::host::scored_status(&word);  // the other translation unit's word
+    if (e != cudaSuccess) return fail_cuda(e);
+    if (word != 0) return (word & 2) ? AJVP_ERR_DEVICE_LAYOUT : AJVP_ERR_TIMEOUT;
     return AJVP_OK;
 }
 

@@ -59,6 +59,7 @@
 #include <type_traits>
 
 #include "ptx_sm100.cuh"
+#include "score_sm100.cuh"
 
 namespace ajvp {
 namespace bwd {
@@ -94,16 +95,24 @@ enum : int {
 };
 constexpr uint32_t OFF_TMEM_SLOT = 8 * N_BARS;
 constexpr uint32_t OFF_ABORT = OFF_TMEM_SLOT + 4;
+constexpr uint32_t OFF_SCRATCH = OFF_ABORT + 4;  // scored: eight ints
 constexpr uint32_t NB_EPI = 1;
 
 // Masks (MASK bits): 1 causal -- key j is visible to query i iff
 // j <= i + (Lk - Lq) of its sequence, bottom-right aligned; 2 packed -- the
 // tensors are [H][total][128] and sequence b owns row-side rows
 // cu_row[b] .. cu_row[b+1]-1 and streamed rows cu_col[b] .. cu_col[b+1]-1.
-// 4 split (unmasked key-side variants only) -- the streamed range is cut into
-// n_split consecutive parts, one per CTA, each writing its fp32 partial sums
+// 4 split (unmasked and scored key-side variants) -- the streamed range is cut
+// into n_split consecutive parts, one per CTA, each writing its fp32 partial sums
 // to partial[split][B*H][Lrow][2][128] (unscaled); bwd_split_reduce_kernel adds
 // them up in split order, so the result stays deterministic.
+// MASK_SCORED (score_sm100.cuh) -- the score modifications, an interval of
+// visible keys per query row, and shared key heads: BH is then the number of
+// row-side (batch, head) slabs, and a key-side CTA streams the queries of every
+// head of its group one after the other into the same accumulators.  The cap's
+// chain rule turns (S_bar, dS_bar) into the gradients of the raw scores,
+//     z_bar = f' S_bar + f'' dz dS_bar,  dz_bar = f' dS_bar,   f'' = -(2 / c) tanh f',
+// with u = f' dz in place of dz in the formulas above.
 constexpr int MASK_CAUSAL = 1, MASK_PACKED = 2, MASK_SPLIT = 4;
 
 struct Params {
@@ -123,10 +132,11 @@ struct Params {
     float scale_log2;     // s * log2(e)
     float out_scale[2];   // factor applied to each accumulator at the end (s or 1)
     unsigned long long bound_ns;
+    Score score;  // MASK_SCORED
 };
 
 // {lse log2(e), mu, a, D} per query row; one warp per row, 4 features per lane.
-__global__ void __launch_bounds__(256) bwd_rowstats_kernel(const __nv_bfloat16 *__restrict__ o,
+static __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const __nv_bfloat16 *__restrict__ o,
                                                            const __nv_bfloat16 *__restrict__ to,
                                                            const __nv_bfloat16 *__restrict__ dout,
                                                            const __nv_bfloat16 *__restrict__ dtout,
@@ -167,7 +177,7 @@ __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const __nv_bfloat16 *
 // Sum of the split parts' fp32 partial sums, in part order, times the
 // accumulator's output scale, rounded to bf16: out[a][row][:] for the
 // rows x 2 accumulators of one key-side variant.  One thread per 4 columns.
-__global__ void __launch_bounds__(256) bwd_split_reduce_kernel(const float4 *__restrict__ partial, int n_split,
+static __global__ void __launch_bounds__(256) bwd_split_reduce_kernel(const float4 *__restrict__ partial, int n_split,
                                                                long long rows, __nv_bfloat16 *__restrict__ out0,
                                                                __nv_bfloat16 *__restrict__ out1, float s0, float s1) {
     const long long n4 = rows * 2 * (HD / 4);  // float4s of one part
@@ -363,7 +373,7 @@ struct Var {
     __device__ static uint32_t long_off(int s) { return SM_L + (uint32_t)s * L_BYTES; }
     static constexpr uint32_t SMEM_BYTES = SM_BAR + 256;  // the base is 1024-byte aligned (checked)
     static_assert(SMEM_BYTES <= 232448, "exceeds the opt-in shared memory of one CTA");
-    static_assert(8 * N_BARS + 8 <= 256, "barrier area");
+    static_assert(OFF_SCRATCH + 32 <= 256, "barrier area");
     // tensor memory: two accumulators, then the score buffer(s)
     static constexpr uint32_t BUF0 = 256u;
     static constexpr uint32_t BUF_COLS = kSingle ? 256u : 128u;
@@ -400,7 +410,11 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
     using C = Var<VAR, kPair>;
     constexpr bool kCausal = (MASK & MASK_CAUSAL) != 0, kPacked = (MASK & MASK_PACKED) != 0;
     constexpr bool kSplitK = (MASK & MASK_SPLIT) != 0;
-    static_assert(!kSplitK || (MASK == MASK_SPLIT && VAR != V_Q), "the split is for the unmasked key side");
+    constexpr bool kScored = (MASK & MASK_SCORED) != 0, kCap = (MASK & MASK_CAP) != 0, kBias = (MASK & MASK_BIAS) != 0;
+    static_assert(!kSplitK || ((MASK == MASK_SPLIT || kScored) && VAR != V_Q),
+                  "the split is for the unmasked and scored key sides");
+    static_assert(!kScored || (!kCausal && !kPacked), "the scored form is dense");
+    static_assert(kScored || (!kCap && !kBias), "caps and biases belong to the scored form");
     static_assert(!kPair || MASK == 0, "pairs are built for the unmasked kernels");
     extern __shared__ __align__(1024) uint8_t bwd_smem[];
     const uint32_t base = smem_u32(bwd_smem);
@@ -451,7 +465,33 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
     const int yr_load = (kPair && !rows_live) ? 0 : yr;
     // streamed tiles jt0 .. jt0 + nt - 1 (local index j = 0 .. nt - 1)
     int jt0 = 0, nt = (Lcol_s + BN - 1) / BN;
-    if (kSplitK) {
+    // scored: the batch index, the first streamed slab (a key-side CTA's group has
+    // `group` of them), and the tiles ntv of one slab that some row of the tile sees;
+    // streamed tile t is tile jt0 + u % ntv of slab bh_c + u / ntv, u = u0 + t
+    int sb = 0, bh_c = bh, ntv = 1, u0 = 0;
+    if constexpr (kScored) {
+        int2 seen;
+        int slabs = 1;
+        if (VAR == V_Q) {
+            sb = bh / p.score.H;
+            bh_c = sb * p.score.Hkv + (bh - sb * p.score.H) / p.score.group;
+            seen = tile_key_range(p.score, sb, r0, Lrow_s, Lcol_s,
+                                  reinterpret_cast<int *>(gbase + C::SM_BAR + OFF_SCRATCH));
+        } else {
+            sb = bh / p.score.Hkv;
+            bh_c = sb * p.score.H + (bh - sb * p.score.Hkv) * p.score.group;
+            slabs = p.score.group;
+            seen = p.score.qrange ? p.score.qrange[(size_t)sb * p.n_rtiles + rt] : make_int2(0, Lcol_s);
+        }
+        jt0 = seen.x / BN;
+        ntv = seen.y > 0 ? (seen.y + BN - 1) / BN - jt0 : 0;
+        nt = ntv * slabs;
+        if (kSplitK) {
+            const int chunk = (nt + p.n_split - 1) / p.n_split;
+            u0 = min(sp * chunk, nt);
+            nt = min(chunk, nt - u0);
+        }
+    } else if (kSplitK) {
         const int chunk = (nt + p.n_split - 1) / p.n_split;
         jt0 = sp * chunk;
         nt = max(0, min(chunk, nt - jt0));
@@ -560,14 +600,19 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 }
             }
             // a stage [x c0 | y c0 | x c1 | y c1] of two streamed tensors, rows y..y+63
-            auto load_pair = [&](uint32_t st, const CUtensorMap *mx, const CUtensorMap *my, uint32_t fb, int y) {
-                tma_load_3d(st, mx, fb, 0, y, bh);
-                tma_load_3d(st + CHUNK_C, my, fb, 0, y, bh);
-                tma_load_3d(st + 2 * CHUNK_C, mx, fb, 64, y, bh);
-                tma_load_3d(st + 3 * CHUNK_C, my, fb, 64, y, bh);
+            auto load_pair = [&](uint32_t st, const CUtensorMap *mx, const CUtensorMap *my, uint32_t fb, int y, int z) {
+                tma_load_3d(st, mx, fb, 0, y, z);
+                tma_load_3d(st + CHUNK_C, my, fb, 0, y, z);
+                tma_load_3d(st + 2 * CHUNK_C, mx, fb, 64, y, z);
+                tma_load_3d(st + 3 * CHUNK_C, my, fb, 64, y, z);
             };
             for (int t = 0; t < nt && ok; ++t) {
-                const int y = yc0 + (jt0 + t) * BN;  // tensor row of the streamed tile
+                int y = yc0 + (jt0 + t) * BN, z = bh;  // tensor row and slab of the streamed tile
+                if constexpr (kScored) {
+                    const int u = u0 + t, slab = u / ntv;
+                    y = (jt0 + u - slab * ntv) * BN;
+                    z = bh_c + slab;
+                }
                 if (lp) {  // long ring, stage t % kLS: free once the G2 products of tile t - kLS are complete
                     const int s = t % C::kLS;
                     if (t >= C::kLS &&
@@ -592,15 +637,15 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                     } else if (VAR == V_V) {
                         // only G2 reads it, as one N = 256 operand [x | y]: [x c0 | x c1 | y c0 | y c1]
                         const uint32_t st = base + C::long_off(s);
-                        tma_load_3d(st, &p.tm_l[0], fb, 0, y, bh);
-                        tma_load_3d(st + CHUNK_C, &p.tm_l[0], fb, 64, y, bh);
-                        tma_load_3d(st + 2 * CHUNK_C, &p.tm_l[1], fb, 0, y, bh);
-                        tma_load_3d(st + 3 * CHUNK_C, &p.tm_l[1], fb, 64, y, bh);
+                        tma_load_3d(st, &p.tm_l[0], fb, 0, y, z);
+                        tma_load_3d(st + CHUNK_C, &p.tm_l[0], fb, 64, y, z);
+                        tma_load_3d(st + 2 * CHUNK_C, &p.tm_l[1], fb, 0, y, z);
+                        tma_load_3d(st + 3 * CHUNK_C, &p.tm_l[1], fb, 64, y, z);
                     } else {
-                        load_pair(base + C::long_off(s), &p.tm_l[0], &p.tm_l[1], fb, y);
+                        load_pair(base + C::long_off(s), &p.tm_l[0], &p.tm_l[1], fb, y, z);
                     }
                     if (kWithStats)  // padded by BN rows past the last head: never out of bounds
-                        bulk_load(base + C::SM_ST + s * STATS_TILE, p.stats + (size_t)bh * p.Lq + y, STATS_TILE, fb);
+                        bulk_load(base + C::SM_ST + s * STATS_TILE, p.stats + (size_t)z * p.Lq + y, STATS_TILE, fb);
                     l_last[s] = t;
                 } else {  // short ring, stage t % kSS: free once G1 of tile t - kSS is complete
                     // (V_Q, V_K: one stage, freed by the [Z|W] products' own completion barrier)
@@ -623,7 +668,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                         load(st + C::P_B2 + C::B2_CH, &p.tm_s32, fi, 64, y + 32 * (int)crank);
                     } else {
                         mbar_arrive_expect_tx(fb, 4 * CHUNK_C);
-                        load_pair(st, &p.tm_s[0], &p.tm_s[1], fb, y);
+                        load_pair(st, &p.tm_s[0], &p.tm_s[1], fb, y, z);
                     }
                     s_last[ss] = t;
                     if (C::kStatsRing) {
@@ -635,7 +680,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                         }
                         const uint32_t sb = BAR(B_ST_FULL + (t & 1));
                         mbar_arrive_expect_tx(sb, STATS_TILE);  // padded by BN rows: never out of bounds
-                        bulk_load(base + C::SM_ST + (t & 1) * STATS_TILE, p.stats + (size_t)bh * p.Lq + y, STATS_TILE, sb);
+                        bulk_load(base + C::SM_ST + (t & 1) * STATS_TILE, p.stats + (size_t)z * p.Lq + y, STATS_TILE, sb);
                         st_last = t;
                     }
                 }
@@ -834,9 +879,33 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 warp_arrive_after_tc(BAR(bar));
             }
         };
+        // scored: the row-side item's visible keys (V_Q), its slope (log2 units; key side:
+        // the streamed slab's) and its place on the streamed axis, where the distance of
+        // query i to key j, |i + Lk - Lq - j|, is |rpos - streamed item| for both sides
+        int2 rb = make_int2(0, 0);
+        float slope2 = 0.f;
+        const int rpos = r0 + row + (VAR == V_Q ? koff : -koff);
+        if constexpr (kScored && VAR == V_Q) {
+            rb = row_bounds(p.score, sb, r0 + row, Lrow_s, Lcol_s);
+            if (kBias) slope2 = p.score.slopes[bh - sb * p.score.H] * 1.4426950408889634f;
+        }
+        // scored: log2-unit scores of two columns less lse2 (ls), the cap's tanh and derivative;
+        // dist: distance of the row-side item to column c
+        auto score2 = [&](float2 x, float2 ls, float dist, float2 &t, float2 &df) -> float2 {
+            float2 y;
+            if constexpr (kCap) {
+                cap2(x, p.score.cap_in, t, df);
+                y = __ffma2_rn(t, make_float2(p.score.cap_out, p.score.cap_out), make_float2(-ls.x, -ls.y));
+            } else {
+                y = __ffma2_rn(x, c2, make_float2(-ls.x, -ls.y));
+            }
+            if constexpr (kBias)
+                y = __ffma2_rn(make_float2(-slope2, -slope2), make_float2(fabsf(dist), fabsf(dist - 1.f)), y);
+            return y;
+        };
         // one pair of columns (c, c + 1 of this group): x scores, y score tangent,
         // z A, w B -> r1, r2 (see the variant table)
-        auto pair = [&](int c, int lo, int hi, bool masked, uint32_t st_base, uint32_t xa, uint32_t xb, uint32_t ya,
+        auto pair = [&](int c, int lo, int hi, uint32_t vis, float dist, bool masked, uint32_t st_base, uint32_t xa, uint32_t xb, uint32_t ya,
                         uint32_t yb, uint32_t za, uint32_t zb, uint32_t wa, uint32_t wb, float2 &r1, float2 &r2) {
             float4 sa = rs, sb = rs;  // statistics of columns c and c + 1
             if (C::kColStats) {
@@ -844,11 +913,17 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 sb = ld_shared_f4(st_base + 16u * (c + 1));
             }
             const float2 x = make_float2(__uint_as_float(xa), __uint_as_float(xb));
-            const float2 t = __ffma2_rn(x, c2, make_float2(-sa.x, -sb.x));
+            [[maybe_unused]] float2 th = make_float2(0.f, 0.f), df = make_float2(1.f, 1.f);
+            float2 t;
+            if constexpr (kScored)
+                t = score2(x, make_float2(sa.x, sb.x), dist - (float)c, th, df);
+            else
+                t = __ffma2_rn(x, c2, make_float2(-sa.x, -sb.x));
             const float2 pp = make_float2(ex2_approx(t.x), ex2_approx(t.y));
             if (VAR == V_V) {
-                // u - mu = s Y - mu in one packed FMA
-                const float2 umu = __ffma2_rn(make_float2(__uint_as_float(ya), __uint_as_float(yb)), s2,
+                // u - mu = s Y - mu in one packed FMA (capped: u = s Y f')
+                const float2 fs = kCap ? __fmul2_rn(df, s2) : s2;
+                const float2 umu = __ffma2_rn(make_float2(__uint_as_float(ya), __uint_as_float(yb)), fs,
                                               make_float2(-sa.y, -sb.y));
                 r1 = pp;                     // P
                 r2 = __fmul2_rn(pp, umu);    // P (u - mu)
@@ -866,13 +941,23 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
             }
             // columns past the end of the tensor, or hidden by the causal mask
             if (masked) {
-                if (c >= hi || c < lo) r1.x = r2.x = 0.f;
-                if (c + 1 >= hi || c + 1 < lo) r1.y = r2.y = 0.f;
+                if (kScored ? !((vis >> c) & 1u) : (c >= hi || c < lo)) r1.x = r2.x = 0.f;
+                if (kScored ? !((vis >> (c + 1)) & 1u) : (c + 1 >= hi || c + 1 < lo)) r1.y = r2.y = 0.f;
             }
         };
 
         for (int j = 0; j < nt; ++j) {
             const int b = j % C::kNB, s = j % C::kLS;
+            int tile = jt0 + j;
+            int2 cb = make_int2(0, 0);  // scored key side: the visible keys of this lane's streamed query
+            if constexpr (kScored) {
+                const int u = u0 + j, slab = u / ntv;
+                tile = jt0 + u - slab * ntv;
+                if (VAR != V_Q) {
+                    cb = row_bounds(p.score, sb, tile * BN + (int)col0 + lane, Lcol_s, Lrow_s);
+                    if (kBias) slope2 = p.score.slopes[bh_c - sb * p.score.H + slab] * 1.4426950408889634f;
+                }
+            }
             // V_Q, V_K: Z and W first (complete well before X and Y)
             const int g1bar = C::kSingle ? (int)B_ZW_DONE : (int)B_G1_DONE + b;
             if (!failed) failed = !ew_wait(BAR(g1bar), (j / C::kNB) & 1, abort_flag, bound);
@@ -884,8 +969,30 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
             if (failed) continue;
             tc_fence_after();
             // this group's columns lo .. hi - 1 are inside the tensor and visible
-            const int y0 = (jt0 + j) * BN + (int)col0;  // the group's first streamed item
+            const int y0 = tile * BN + (int)col0;  // the group's first streamed item
             int lo = 0, hi = Lcol_s - y0;
+            // scored: does every row of this warp see all 32 columns (one choice per warp),
+            // and if not, which columns this row sees
+            bool full = false;
+            uint32_t vis = 0xffffffffu;
+            const float dist = (float)(rpos - y0);
+            if constexpr (kScored) {
+                if (VAR == V_Q) {
+                    full = __all_sync(0xffffffffu, rb.x <= y0 && rb.y >= y0 + 32);
+                    if (!full) vis = bit_range(rb.x - y0, rb.y - y0);
+                } else {
+                    const int k0 = r0 + wl * 32;
+                    full = __all_sync(0xffffffffu, cb.x <= k0 && cb.y >= k0 + 32);
+                    if (!full) {
+                        vis = 0u;
+#pragma unroll 8
+                        for (int c = 0; c < 32; ++c) {
+                            const int lo_c = __shfl_sync(0xffffffffu, cb.x, c), hi_c = __shfl_sync(0xffffffffu, cb.y, c);
+                            vis |= (k0 + lane >= lo_c && k0 + lane < hi_c ? 1u : 0u) << c;
+                        }
+                    }
+                }
+            }
             if (kCausal) {
                 if (VAR == V_Q)
                     hi = min(hi, r0 + row + koff - y0 + 1);  // keys <= query + (Lk - Lq)
@@ -954,16 +1061,36 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                             const float2 ls =
                                 C::kColStats ? make_float2(stf[4 * c], stf[4 * c + 4]) : make_float2(rs.x, rs.x);
                             const float2 x = make_float2(__uint_as_float(xr[i]), __uint_as_float(xr[i + 1]));
-                            const float2 tt = __ffma2_rn(x, c2, make_float2(-ls.x, -ls.y));
+                            [[maybe_unused]] float2 th = make_float2(0.f, 0.f), df = make_float2(1.f, 1.f);
+                            float2 tt;
+                            if constexpr (kScored)
+                                tt = score2(x, ls, dist - (float)c, th, df);
+                            else
+                                tt = __ffma2_rn(x, c2, make_float2(-ls.x, -ls.y));
                             const float2 pp = make_float2(ex2_approx(tt.x), ex2_approx(tt.y));
                             const float2 u =
                                 __fmul2_rn(make_float2(__uint_as_float(yr[i]), __uint_as_float(yr[i + 1])), s2);
                             const float2 zz = make_float2(za[c], za[c + 1]);
-                            const float2 pb = __ffma2_rn(u, zz, make_float2(wz[c], wz[c + 1]));
-                            float2 r1 = __fmul2_rn(pp, pb), r2 = __fmul2_rn(pp, zz);
-                            if (kMasked) {  // columns past the end of the tensor, or hidden by the causal mask
-                                if (c >= hi || c < lo) r1.x = r2.x = 0.f;
-                                if (c + 1 >= hi || c + 1 < lo) r1.y = r2.y = 0.f;
+                            float2 r1, r2;
+                            if constexpr (kCap) {
+                                // (u here is dz): dz_bar = P f' za,
+                                // z_bar = P f' ((f' - (2 / c) tanh) dz za + wz)
+                                const float2 pf = __fmul2_rn(pp, df);
+                                const float2 f2 =
+                                    __ffma2_rn(th, make_float2(-p.score.cap_second, -p.score.cap_second), df);
+                                const float2 pb =
+                                    __ffma2_rn(__fmul2_rn(u, zz), f2, make_float2(wz[c], wz[c + 1]));
+                                r1 = __fmul2_rn(pf, pb);
+                                r2 = __fmul2_rn(pf, zz);
+                            } else {
+                                const float2 pb = __ffma2_rn(u, zz, make_float2(wz[c], wz[c + 1]));
+                                r1 = __fmul2_rn(pp, pb);
+                                r2 = __fmul2_rn(pp, zz);
+                            }
+                            if (kMasked) {  // columns past the end of the tensor, or hidden by the mask
+                                if (kScored ? !((vis >> c) & 1u) : (c >= hi || c < lo)) r1.x = r2.x = 0.f;
+                                if (kScored ? !((vis >> (c + 1)) & 1u) : (c + 1 >= hi || c + 1 < lo))
+                                    r1.y = r2.y = 0.f;
                             }
                             h1[i / 2] = pack_bf16x2(r1.x, r1.y);
                             h2[i / 2] = pack_bf16x2(r2.x, r2.y);
@@ -974,7 +1101,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 };
                 // the choice must be the same for the whole warp: the copies hold
                 // warp-collective tensor-memory loads and stores
-                if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32))
+                if (kScored ? full : __all_sync(0xffffffffu, lo <= 0 && hi >= 32))
                     e_halves(std::false_type{});
                 else
                     e_halves(std::true_type{});
@@ -985,11 +1112,11 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 tmem_wait_ld();
                 // the per-column mask only for tiles that reach past the end or cross the
                 // causal diagonal (most tiles see all their columns); one choice per warp
-                if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
+                if (kScored ? full : __all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float2 r1, r2;
-                        pair(i, lo, hi, false, st_base, xr[i], xr[i + 1], yr[i], yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
+                        pair(i, lo, hi, vis, dist, false, st_base, xr[i], xr[i + 1], yr[i], yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
                         e1[i / 2] = pack_bf16x2(r1.x, r1.y);
                         e2[i / 2] = pack_bf16x2(r2.x, r2.y);
                     }
@@ -997,7 +1124,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float2 r1, r2;
-                        pair(i, lo, hi, true, st_base, xr[i], xr[i + 1], yr[i], yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
+                        pair(i, lo, hi, vis, dist, true, st_base, xr[i], xr[i + 1], yr[i], yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
                         e1[i / 2] = pack_bf16x2(r1.x, r1.y);
                         e2[i / 2] = pack_bf16x2(r2.x, r2.y);
                     }

@@ -58,6 +58,7 @@
 #pragma once
 
 #include "ptx_sm100.cuh"
+#include "score_sm100.cuh"
 
 namespace ajvp {
 namespace sm100 {
@@ -119,6 +120,8 @@ enum : int {
 static_assert(STAGES == 2, "the K-side ring reuses the two S/dS' buffer barriers");
 constexpr uint32_t OFF_TMEM_SLOT = 8 * N_BARS;     // u32
 constexpr uint32_t OFF_ABORT = OFF_TMEM_SLOT + 4;  // int
+constexpr uint32_t OFF_SCRATCH = OFF_ABORT + 4;    // scored: eight ints
+static_assert(OFF_SCRATCH + 32 <= 256, "barrier area");
 
 constexpr uint32_t TM_O = 0, TM_T = 128, TM_BUF = 256;
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units: P entries stay <= 256
@@ -146,6 +149,7 @@ struct Params {
     float scale;           // s
     float scale_log2;      // s * log2(e)
     unsigned long long bound_ns;
+    Score score;  // MASK_SCORED
 };
 
 // Coalesced store of one warp's 32 rows x 32 bf16 columns (lane = row, w = its
@@ -174,7 +178,9 @@ __device__ __forceinline__ void store_rows_32x32(uint32_t slot, const uint32_t (
 // iff j <= i + (Lk - Lq), bottom-right aligned; 2 packed -- the tensors are
 // [H][total][128] and sequence b owns rows cu_q[b] .. cu_q[b+1]-1 (queries)
 // and cu_k[b] .. cu_k[b+1]-1 (keys).  Rows with no visible key give zeros and
-// lse = -inf.
+// lse = -inf.  MASK_SCORED (score_sm100.cuh): the score modifications, shared
+// key heads, and an interval of visible keys per query row; a CTA streams the
+// key tiles between its rows' smallest and largest visible key.
 constexpr int MASK_CAUSAL = 1, MASK_PACKED = 2;
 
 // kSplit = false: bf16 P and P.*s dS' operands, bf16 outputs.
@@ -194,6 +200,9 @@ template <bool kSplit, int MASK = 0, bool kPersist = false>
 __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_constant__ Params p) {
     static_assert(!kPersist || (!kSplit && MASK == 0), "the persistent form is the unmasked bf16 kernel");
     constexpr bool kCausal = (MASK & MASK_CAUSAL) != 0, kPacked = (MASK & MASK_PACKED) != 0;
+    constexpr bool kScored = (MASK & MASK_SCORED) != 0, kCap = (MASK & MASK_CAP) != 0, kBias = (MASK & MASK_BIAS) != 0;
+    static_assert(!kScored || (!kSplit && !kCausal && !kPacked), "the scored form is a dense bf16 kernel");
+    static_assert(kScored || (!kCap && !kBias), "caps and biases belong to the scored form");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -264,9 +273,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         Lq_s = a1 - a0;
         yk0 = k0;
         Lk_s = k1 - k0;
-    } else if (kCausal) {
+    } else if (kCausal || (kScored && p.score.end != nullptr)) {
+        // heavy (late) query tiles first (scored: so they are under prefix and frame-causal masks)
         bh = blockIdx.x % p.BH;
-        qt = p.n_qtiles - 1 - blockIdx.x / p.BH;  // heavy (late) query tiles first
+        qt = p.n_qtiles - 1 - blockIdx.x / p.BH;
     } else {
         qt = blockIdx.x % p.n_qtiles;
         bh = blockIdx.x / p.n_qtiles;
@@ -277,7 +287,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
     const int koff = Lk_s - Lq_s;        // causal offset of the diagonal
     int kend = Lk_s;                     // keys any row of this tile may see
     if (kCausal) kend = max(0, min(Lk_s, q0 + BR + koff));
-    const int nk = (kend + BC - 1) / BC;
+    int kbase = 0;    // scored: the first streamed key, a multiple of the tile
+    int bh_kv = bh;   // outer index of the key-side tensors
+    if constexpr (kScored) {
+        const int b = bh / p.score.H;
+        bh_kv = b * p.score.Hkv + (bh - b * p.score.H) / p.score.group;
+        const int2 seen = tile_key_range(p.score, b, q0, Lq_s, Lk_s,
+                                         reinterpret_cast<int *>(gbase + kBar + OFF_SCRATCH));
+        kend = seen.y;
+        kbase = seen.x / BC * BC;
+        yk0 = kbase;
+    }
+    const int nk = (kend - kbase + BC - 1) / BC;
     if (MASK != 0 && nk == 0) {
         // no row of the tile sees a key: zeros and lse = -inf, no pipeline at all
         for (int r = threadIdx.x; r < BR && q0 + r < Lq_s; r += blockDim.x) {
@@ -387,10 +408,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         const int y = yk0 + t * BC;
                         mbar_arrive_expect_tx(fb, KT_STAGE);
                         // chunk c: K rows then tK rows, so [K | tK] is one N = 128 operand
-                        tma_load_3d(st, &p.tm_k, fb, 0, y, bh_n);
-                        tma_load_3d(st + CHUNK_K, &p.tm_tk, fb, 0, y, bh_n);
-                        tma_load_3d(st + 2 * CHUNK_K, &p.tm_k, fb, 64, y, bh_n);
-                        tma_load_3d(st + 3 * CHUNK_K, &p.tm_tk, fb, 64, y, bh_n);
+                        tma_load_3d(st, &p.tm_k, fb, 0, y, kScored ? bh_kv : bh_n);
+                        tma_load_3d(st + CHUNK_K, &p.tm_tk, fb, 0, y, kScored ? bh_kv : bh_n);
+                        tma_load_3d(st + 2 * CHUNK_K, &p.tm_k, fb, 64, y, kScored ? bh_kv : bh_n);
+                        tma_load_3d(st + 3 * CHUNK_K, &p.tm_tk, fb, 64, y, kScored ? bh_kv : bh_n);
                         kt_last[s] = G;
                     }
                     if (t >= 1) {
@@ -414,10 +435,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         const int y = yk0 + (t - 1) * BC;
                         mbar_arrive_expect_tx(fb, VT_STAGE);
                         // [V c0 | V c1 | tV c0 | tV c1]: N-chunks 64 columns apart (LBO)
-                        tma_load_3d(st, &p.tm_v, fb, 0, y, bh_n);
-                        tma_load_3d(st + CHUNK_K, &p.tm_v, fb, 64, y, bh_n);
-                        tma_load_3d(st + 2 * CHUNK_K, &p.tm_tv, fb, 0, y, bh_n);
-                        tma_load_3d(st + 3 * CHUNK_K, &p.tm_tv, fb, 64, y, bh_n);
+                        tma_load_3d(st, &p.tm_v, fb, 0, y, kScored ? bh_kv : bh_n);
+                        tma_load_3d(st + CHUNK_K, &p.tm_v, fb, 64, y, kScored ? bh_kv : bh_n);
+                        tma_load_3d(st + 2 * CHUNK_K, &p.tm_tv, fb, 0, y, kScored ? bh_kv : bh_n);
+                        tma_load_3d(st + 3 * CHUNK_K, &p.tm_tv, fb, 64, y, kScored ? bh_kv : bh_n);
                         vt_last[s] = i;
                     }
                 }
@@ -562,7 +583,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         const float c = p.scale_log2;
         const float2 c2 = make_float2(c, c);
         const float2 s2 = make_float2(p.scale, p.scale);
-        const bool up = c >= 0.f;  // row max of c*S is c * max(S) (min(S) for c < 0)
+        // row max of c*S is c * max(S) (min(S) for c < 0); the scored form's row holds modified scores
+        const bool up = kScored || c >= 0.f;
         const float sentinel = up ? -INFINITY : INFINITY;
         float *xch = reinterpret_cast<float *>(gbase + kXch);
         bool failed = false;
@@ -581,6 +603,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             };
             // keys this row sees (a prefix of the sequence's keys; may be <= 0 when causal)
             const int kcount = kCausal ? min(Lk_s, q0_n + row + koff + 1) : Lk_s;
+            int2 seen = make_int2(0, 0);  // scored: this row's keys, relative to kbase
+            float slope2 = 0.f, dist0 = 0.f;  // bias: slope in log2 units; distance to the first streamed key
+            if constexpr (kScored) {
+                const int sb = bh / p.score.H;
+                seen = row_bounds(p.score, sb, q0 + row, Lq_s, Lk_s);
+                seen.x -= kbase;
+                seen.y -= kbase;
+                if (kBias) {
+                    slope2 = p.score.slopes[bh - sb * p.score.H] * 1.4426950408889634f;
+                    dist0 = (float)(q0 + row + koff - kbase - (int)col0);
+                }
+            }
 
             for (int j = 0; j < nk; ++j) {
                 const int G = G0 + j;  // CTA-wide tile index
@@ -589,13 +623,46 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 if (!failed) failed = !mbar_wait_warp(BAR(B_SD_FULL + b), (G >> 1) & 1, abort_flag, bound);
                 uint32_t xs[32], xd[32];
                 const int valid = kcount - j * BC - (int)col0;  // visible keys of this group (may be <= 0)
+                const int lo = seen.x - j * BC - (int)col0, hi = seen.y - j * BC - (int)col0;  // (scored)
                 float part = sentinel;
                 if (!failed) {
                     tc_fence_after();
                     tmem_ld32(t_s + col0, xs);
                     tmem_ld32(t_s + 64 + col0, xd);
                     tmem_wait_ld();
-                    if (valid < 32) {
+                    if constexpr (kScored) {
+                        // scores in log2 units: c x, or cap_out tanh, less the bias; the score tangent
+                        // takes the cap's derivative here
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 x = make_float2(__uint_as_float(xs[i]), __uint_as_float(xs[i + 1]));
+                            float2 y;
+                            if constexpr (kCap) {
+                                float2 t, df;
+                                cap2(x, p.score.cap_in, t, df);
+                                y = __fmul2_rn(t, make_float2(p.score.cap_out, p.score.cap_out));
+                                const float2 d =
+                                    __fmul2_rn(make_float2(__uint_as_float(xd[i]), __uint_as_float(xd[i + 1])), df);
+                                xd[i] = __float_as_uint(d.x);
+                                xd[i + 1] = __float_as_uint(d.y);
+                            } else {
+                                y = __fmul2_rn(x, c2);
+                            }
+                            if constexpr (kBias) {
+                                const float e = dist0 - (float)(j * BC);
+                                y = __ffma2_rn(make_float2(-slope2, -slope2),
+                                               make_float2(fabsf(e - (float)i), fabsf(e - (float)(i + 1))), y);
+                            }
+                            xs[i] = __float_as_uint(y.x);
+                            xs[i + 1] = __float_as_uint(y.y);
+                        }
+                        if (lo > 0 || hi < 32) {
+                            const uint32_t vis = bit_range(lo, hi);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((vis >> i) & 1u)) xs[i] = __float_as_uint(-INFINITY);
+                        }
+                    } else if (valid < 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (i >= valid) xs[i] = __float_as_uint(sentinel);
@@ -632,7 +699,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                     break;
                 }
                 const float other = xch[(b * 2 + (grp ^ 1)) * 128 + row];
-                const float m_tile = (up ? fmaxf(part, other) : fminf(part, other)) * c;
+                const float m_tile = kScored ? fmaxf(part, other) : (up ? fmaxf(part, other) : fminf(part, other)) * c;
                 if (j == 0) {
                     m_ref = m_tile;
                 } else {
@@ -718,16 +785,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                     }
                 }
                 if (failed) continue;  // the next tile's barrier carries the failure to everyone
-                const float2 nm2 = make_float2(-m_ref, -m_ref);
+                // (scored: hidden keys hold -infinity, which gives 0 against any finite reference)
+                const float nm = kScored && m_ref == -INFINITY ? 0.f : -m_ref;
+                const float2 nm2 = make_float2(nm, nm);
                 float pv[32];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 y =
-                        __ffma2_rn(make_float2(__uint_as_float(xs[2 * i]), __uint_as_float(xs[2 * i + 1])), c2, nm2);
+                    const float2 x = make_float2(__uint_as_float(xs[2 * i]), __uint_as_float(xs[2 * i + 1]));
+                    const float2 y = kScored ? __fadd2_rn(x, nm2) : __ffma2_rn(x, c2, nm2);
                     pv[2 * i] = ex2_approx(y.x);
                     pv[2 * i + 1] = ex2_approx(y.y);
                 }
-                if (valid < 32) {
+                if (!kScored && valid < 32) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (i >= valid) pv[i] = 0.f;

@@ -12,8 +12,8 @@
 
 namespace ajvp {
 
-// Device status word: bit 0 = some bounded wait gave up.
-__device__ int g_status_word;
+// Device status word: bit 0 = some bounded wait gave up (one per translation unit).
+static __device__ int g_status_word;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

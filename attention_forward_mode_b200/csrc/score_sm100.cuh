@@ -1,0 +1,120 @@
+// score_sm100.cuh -- score modifications shared by the forward and backward
+// tensor-core kernels: a tanh cap, a bias by distance, an interval of visible
+// keys per query row, and key heads shared by groups of query heads.
+//
+// With z = s Q K^T and dz = s (tQ K^T + Q tK^T) the modified scores are
+//     S_ij = c tanh(z_ij / c) - slope_h |i + Lk - Lq - j|,   dS_ij = (1 - tanh^2(z_ij / c)) dz_ij
+// and query row i of sequence b sees the keys begin[b][i] <= j < end[b][i].
+// An interval per row is enough for prefix, document, frame-causal, causal
+// and sliding-window masks, costs two integers per row whatever the mask, and
+// gives every tile the range of the other side's tiles that it has to visit.
+#pragma once
+
+#include <climits>
+
+#include "ptx_sm100.cuh"
+
+namespace ajvp {
+
+// MASK bits of the scored kernels (beside those of the kernels' own)
+constexpr int MASK_SCORED = 8, MASK_CAP = 16, MASK_BIAS = 32;
+
+struct Score {
+    const int *begin, *end;  // [B][Lq] visible keys of each query row, or NULL: 0 / Lk
+    const float *slopes;     // [H] distance slopes (MASK_BIAS)
+    const int2 *qrange;      // backward: [B][n_rtiles] first and end query row that sees a key of the 128-key tile
+                             // (NULL: every row)
+    float cap_in;            // 2 s log2(e) / c: tanh(z / c) = 1 - 2 / (1 + 2^(cap_in x)) of a raw score x = z / s
+    float cap_out;           // c log2(e): the capped score in log2 units is cap_out tanh
+    float cap_second;        // 2 / c
+    int H, Hkv, group;       // query heads, key heads, query heads per key head
+};
+
+// the visible keys of one query row, inside [0, Lk]; rows past the end see none
+__device__ __forceinline__ int2 row_bounds(const Score &sc, int b, int row, int Lq, int Lk) {
+    if (row >= Lq) return make_int2(0, 0);
+    const size_t i = (size_t)b * (size_t)Lq + (size_t)row;
+    const int lo = sc.begin ? max(sc.begin[i], 0) : 0;
+    const int hi = sc.end ? min(sc.end[i], Lk) : Lk;
+    return make_int2(lo, hi);
+}
+
+// The smallest interval that holds the visible keys of rows row0 .. row0 + 127
+// (0, 0 if none sees any); every thread of the CTA calls it.  scratch: eight
+// ints of shared memory.
+__device__ __forceinline__ int2 tile_key_range(const Score &sc, int b, int row0, int Lq, int Lk, int *scratch) {
+    if (!sc.begin && !sc.end) return make_int2(0, Lk);
+    int *const s_lo = scratch, *const s_hi = scratch + 4;
+    const int warp = threadIdx.x >> 5;
+    if (warp < 4) {
+        const int2 r = row_bounds(sc, b, row0 + (int)threadIdx.x, Lq, Lk);
+        const bool any = r.x < r.y;
+        const int lo = __reduce_min_sync(0xffffffffu, any ? r.x : INT_MAX);
+        const int hi = __reduce_max_sync(0xffffffffu, any ? r.y : 0);
+        if ((threadIdx.x & 31) == 0) {
+            s_lo[warp] = lo;
+            s_hi[warp] = hi;
+        }
+    }
+    __syncthreads();
+    const int lo = min(min(s_lo[0], s_lo[1]), min(s_lo[2], s_lo[3]));
+    const int hi = max(max(s_hi[0], s_hi[1]), max(s_hi[2], s_hi[3]));
+    return hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// bits i of a 32-wide tile with lo <= i < hi
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+    const uint32_t below_hi = hi <= 0 ? 0u : (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u);
+    const uint32_t below_lo = lo <= 0 ? 0u : (lo >= 32 ? 0xffffffffu : (1u << lo) - 1u);
+    return below_hi & ~below_lo;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh(z / c) of two raw scores, and 1 - tanh^2.  With e = exp(2 z / c) and
+// r = 1 / (1 + e): tanh = 1 - 2 r and 1 - tanh^2 = 4 r (1 - r).  The error is
+// a few 2^-24 absolute (the scores need absolute accuracy: c tanh enters an
+// exponential), e = infinity gives r = 0.
+__device__ __forceinline__ void cap2(float2 x, float cap_in, float2 &t, float2 &df) {
+    const float2 y = __fmul2_rn(x, make_float2(cap_in, cap_in));
+    const float2 r = make_float2(rcp_approx(1.f + ex2_approx(y.x)), rcp_approx(1.f + ex2_approx(y.y)));
+    t = __ffma2_rn(r, make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
+    const float2 r4 = __fmul2_rn(r, make_float2(4.f, 4.f));
+    df = __ffma2_rn(r4, make_float2(-r.x, -r.y), r4);
+}
+
+// [B][n_ktiles] query rows (first, end) that see a key of each 128-key tile,
+// for the key-side kernels; one block per tile.
+static __global__ void __launch_bounds__(256) query_range_kernel(Score sc, int Lq, int Lk, int2 *out) {
+    const int k0 = (int)blockIdx.x * 128, b = (int)blockIdx.y;
+    const int k1 = min(k0 + 128, Lk);
+    int first = INT_MAX, end = 0;
+    for (int q = (int)threadIdx.x; q < Lq; q += 256) {
+        const int2 r = row_bounds(sc, b, q, Lq, Lk);
+        if (max(r.x, k0) < min(r.y, k1)) {
+            first = min(first, q);
+            end = q + 1;
+        }
+    }
+    __shared__ int s_first[8], s_end[8];
+    first = __reduce_min_sync(0xffffffffu, first);
+    end = __reduce_max_sync(0xffffffffu, end);
+    if ((threadIdx.x & 31) == 0) {
+        s_first[threadIdx.x >> 5] = first;
+        s_end[threadIdx.x >> 5] = end;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) {
+            first = min(first, s_first[w]);
+            end = max(end, s_end[w]);
+        }
+        out[(size_t)b * gridDim.x + blockIdx.x] = end > 0 ? make_int2(first, end) : make_int2(0, 0);
+    }
+}
+
+}  // namespace ajvp

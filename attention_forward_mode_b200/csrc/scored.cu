@@ -1,0 +1,356 @@
+// scored.cu -- host side of the score-modified attention + JVP (tanh cap,
+// distance bias, an interval of visible keys per query row, shared key heads):
+// attn_jvp_fwd_scored, attn_jvp_fwd_scored_stats, attn_jvp_bwd_scored.
+// Argument checks, tensor maps, launches; no device memory is allocated here.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <initializer_list>
+#include <mutex>
+
+#include "attn_jvp.h"
+#include "host_common.h"
+#include "jvp_bwd_sm100.cuh"
+#include "jvp_sm100.cuh"
+
+using namespace ajvp;
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// positions are exact in fp32, which the distance bias computes in
+constexpr int64_t kMaxLen = int64_t(1) << 24;
+
+struct Setup {
+    std::once_flag once;
+    cudaError_t error = cudaSuccess;
+};
+Setup g_setup[host::kMaxDevices];
+
+template <int MASK>
+cudaError_t set_fwd() {
+    return cudaFuncSetAttribute(sm100::attn_jvp_fwd_kernel<false, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sm100::SMEM_BYTES);
+}
+template <int VAR, int MASK>
+cudaError_t set_bwd() {
+    return cudaFuncSetAttribute(bwd::attn_jvp_bwd_kernel<VAR, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)bwd::Var<VAR>::SMEM_BYTES);
+}
+template <int MASK>
+cudaError_t set_mask() {
+    cudaError_t e = set_fwd<MASK>();
+    if (e == cudaSuccess) e = set_bwd<bwd::V_Q, MASK>();
+    if (e == cudaSuccess) e = set_bwd<bwd::V_K, MASK>();
+    if (e == cudaSuccess) e = set_bwd<bwd::V_V, MASK>();
+    if (e == cudaSuccess) e = set_bwd<bwd::V_K, MASK | bwd::MASK_SPLIT>();
+    if (e == cudaSuccess) e = set_bwd<bwd::V_V, MASK | bwd::MASK_SPLIT>();
+    return e;
+}
+
+int setup(int *dev) {
+    int rc = host::device(dev);
+    if (rc != AJVP_OK) return rc;
+    Setup &s = g_setup[*dev];
+    std::call_once(s.once, [&]() {
+        s.error = set_mask<MASK_SCORED>();
+        if (s.error == cudaSuccess) s.error = set_mask<MASK_SCORED | MASK_CAP>();
+        if (s.error == cudaSuccess) s.error = set_mask<MASK_SCORED | MASK_BIAS>();
+        if (s.error == cudaSuccess) s.error = set_mask<MASK_SCORED | MASK_CAP | MASK_BIAS>();
+    });
+    return s.error == cudaSuccess ? AJVP_OK : host::fail(s.error);
+}
+
+struct Sizes {
+    int64_t B, H, Hkv, Lq, Lk, d;
+};
+
+int check_sizes(const Sizes &z, float scale, float softcap) {
+    if (z.B < 0 || z.H < 0 || z.Hkv < 0 || z.Lq < 0 || z.Lk < 1 || z.d < 1) return AJVP_ERR_INVALID_ARG;
+    if (z.H > 0 && (z.Hkv < 1 || z.H % z.Hkv != 0)) return AJVP_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return AJVP_ERR_INVALID_ARG;
+    if (softcap > 0.f && (!std::isfinite(2.f * scale * kLog2e / softcap) || !std::isfinite(2.f / softcap) ||
+                          !std::isfinite(softcap * kLog2e)))
+        return AJVP_ERR_INVALID_ARG;
+    return AJVP_OK;
+}
+
+int check_large(const Sizes &z) {
+    if (z.Lq >= kMaxLen || z.Lk >= kMaxLen || z.B >= (int64_t(1) << 31) || z.H >= (int64_t(1) << 31) ||
+        z.B * z.H >= (int64_t(1) << 31))
+        return AJVP_ERR_TOO_LARGE;
+    if ((z.Lq + 127) / 128 * z.B * z.H >= (int64_t(1) << 31) || (z.Lk + 127) / 128 * z.B * z.H >= (int64_t(1) << 31))
+        return AJVP_ERR_TOO_LARGE;
+    return AJVP_OK;
+}
+
+Score make_score(const Sizes &z, float scale, float softcap, const float *slopes, const int32_t *begin,
+                 const int32_t *end) {
+    Score s;
+    std::memset(&s, 0, sizeof(s));
+    s.begin = begin;
+    s.end = end;
+    s.slopes = slopes;
+    if (softcap > 0.f) {
+        s.cap_in = 2.f * scale * kLog2e / softcap;
+        s.cap_out = softcap * kLog2e;
+        s.cap_second = 2.f / softcap;
+    }
+    s.H = (int)z.H;
+    s.Hkv = (int)z.Hkv;
+    s.group = (int)(z.H / z.Hkv);
+    return s;
+}
+
+int mask_bits(float softcap, const float *slopes) {
+    return MASK_SCORED | (softcap > 0.f ? MASK_CAP : 0) | (slopes ? MASK_BIAS : 0);
+}
+
+// f(std::integral_constant<int, MASK>) for the run-time mask
+template <class F>
+int with_mask(int mask, F f) {
+    switch (mask) {
+        case MASK_SCORED: return f(std::integral_constant<int, MASK_SCORED>());
+        case MASK_SCORED | MASK_CAP: return f(std::integral_constant<int, MASK_SCORED | MASK_CAP>());
+        case MASK_SCORED | MASK_BIAS: return f(std::integral_constant<int, MASK_SCORED | MASK_BIAS>());
+        default: return f(std::integral_constant<int, MASK_SCORED | MASK_CAP | MASK_BIAS>());
+    }
+}
+
+int fwd_scored(const void *q, const void *k, const void *v, const void *tq, const void *tk, const void *tv, void *o,
+               void *to, float *lse, float *mu, const float *slopes, const int32_t *key_begin, const int32_t *key_end,
+               const Sizes &z, float scale, float softcap, void *stream) {
+    int rc = check_sizes(z, scale, softcap);
+    if (rc != AJVP_OK) return rc;
+    if (z.B == 0 || z.H == 0 || z.Lq == 0) return AJVP_OK;
+    if (!q || !k || !v || !tq || !tk || !tv || !o || !to) return AJVP_ERR_INVALID_ARG;
+    if ((rc = check_large(z)) != AJVP_OK) return rc;
+    if (z.d != sm100::HD) return AJVP_ERR_UNSUPPORTED_DIM;
+    for (const void *p : {q, k, v, tq, tk, tv, (const void *)o, (const void *)to, (const void *)lse, (const void *)mu})
+        if (!host::aligned(p, 16)) return AJVP_ERR_MISALIGNED;
+    for (const void *p : {(const void *)slopes, (const void *)key_begin, (const void *)key_end})
+        if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
+    int dev = 0;
+    if ((rc = setup(&dev)) != AJVP_OK) return rc;
+    if ((rc = host::encoder()) != AJVP_OK) return rc;
+
+    const int64_t BH = z.B * z.H, BHk = z.B * z.Hkv;
+    sm100::Params p;
+    std::memset(&p, 0, sizeof(p));
+    if ((rc = host::encode(&p.tm_q, q, z.d, z.Lq, BH, 128)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_tq, tq, z.d, z.Lq, BH, 128)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_k, k, z.d, z.Lk, BHk, 64)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_tk, tk, z.d, z.Lk, BHk, 64)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_v, v, z.d, z.Lk, BHk, 64)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_tv, tv, z.d, z.Lk, BHk, 64)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_o, o, z.d, z.Lq, BH, 128)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_to, to, z.d, z.Lq, BH, 128)) != AJVP_OK) return rc;
+    p.lse = lse;
+    p.mu = mu;
+    p.o_bf = static_cast<__nv_bfloat16 *>(o);
+    p.to_bf = static_cast<__nv_bfloat16 *>(to);
+    p.BH = (int)BH;
+    p.Lq = (int)z.Lq;
+    p.Lk = (int)z.Lk;
+    p.n_qtiles = (int)((z.Lq + sm100::BR - 1) / sm100::BR);
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.bound_ns = host::wait_bound_ns();
+    p.score = make_score(z, scale, softcap, slopes, key_begin, key_end);
+    return with_mask(mask_bits(softcap, slopes), [&](auto mask) {
+        sm100::attn_jvp_fwd_kernel<false, decltype(mask)::value>
+            <<<(unsigned)(p.n_qtiles * BH), sm100::NTHREADS, sm100::SMEM_BYTES, (cudaStream_t)stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? AJVP_OK : host::fail(e);
+    });
+}
+
+uint64_t range_bytes(int64_t B, int64_t Lk) {
+    return ((uint64_t)B * (uint64_t)((Lk + 127) / 128) * sizeof(int2) + 255u) / 256u * 256u;
+}
+
+// parts of a key-side CTA's streamed queries (the tiles of every head of its group)
+int64_t split_parts(const Sizes &z, int sm_count) {
+    const int64_t tiles = (z.Lq + bwd::BN - 1) / bwd::BN * (z.H / z.Hkv);
+    return host::key_split(z.B * z.Hkv, tiles * bwd::BN, z.Lk, sm_count);
+}
+
+// One backward variant over `rows` row-side slabs: r resident, l the long and
+// s the short streamed pair, out scaled by sc; n_split > 1 writes partial sums
+// to `partial` and reduces them.
+template <int VAR, int MASK>
+int launch_one(std::initializer_list<const void *> r, std::initializer_list<const void *> l,
+               std::initializer_list<const void *> s, void *out0, void *out1, float sc, const Score &score,
+               const void *stats, int64_t BHrow, int64_t BHcol, int64_t Lrow, int64_t Lcol, int64_t Lq, float scale,
+               int64_t n_split, float *partial, cudaStream_t stream) {
+    using namespace ajvp::bwd;
+    Params p;
+    std::memset(&p, 0, sizeof(p));
+    int rc, i = 0;
+    for (const void *x : r)
+        if ((rc = host::encode(&p.tm_r[i++], x, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
+    i = 0;
+    for (const void *x : l)
+        if ((rc = host::encode(&p.tm_l[i++], x, HD, Lcol, BHcol, 64)) != AJVP_OK) return rc;
+    i = 0;
+    for (const void *x : s)
+        if ((rc = host::encode(&p.tm_s[i++], x, HD, Lcol, BHcol, 64)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_out[0], out0, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p.tm_out[1], out1, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
+    p.out_scale[0] = p.out_scale[1] = sc;
+    p.BH = (int)BHrow;
+    p.n_split = (int)n_split;
+    p.partial = partial;
+    p.stats = static_cast<const float4 *>(stats);
+    p.Lrow = (int)Lrow;
+    p.Lcol = (int)Lcol;
+    p.Lq = (int)Lq;
+    p.n_rtiles = (int)((Lrow + BM - 1) / BM);
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.bound_ns = host::wait_bound_ns();
+    p.score = score;
+    const int64_t n_cta = (int64_t)p.n_rtiles * BHrow * n_split;
+    if (n_cta >= (int64_t(1) << 31)) return AJVP_ERR_TOO_LARGE;
+    attn_jvp_bwd_kernel<VAR, MASK><<<(unsigned)n_cta, NTHREADS, Var<VAR>::SMEM_BYTES, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host::fail(e);
+    if constexpr ((MASK & MASK_SPLIT) != 0) {
+        const long long rows = (long long)(BHrow * Lrow), n4 = rows * 2 * (HD / 4);
+        bwd_split_reduce_kernel<<<(unsigned)std::min<long long>((n4 + 255) / 256, 148LL * 16), 256, 0, stream>>>(
+            reinterpret_cast<const float4 *>(partial), (int)n_split, rows, static_cast<__nv_bfloat16 *>(out0),
+            static_cast<__nv_bfloat16 *>(out1), sc, sc);
+        if ((e = cudaGetLastError()) != cudaSuccess) return host::fail(e);
+    }
+    return AJVP_OK;
+}
+
+}  // namespace
+
+namespace ajvp {
+namespace host {
+cudaError_t scored_status(int *word) {
+    int w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&w, g_status_word, sizeof(int));
+    if (e != cudaSuccess || w == 0) return e;
+    *word |= w;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int));
+}
+}  // namespace host
+}  // namespace ajvp
+
+extern "C" {
+
+int attn_jvp_fwd_scored(const void *q, const void *k, const void *v, const void *tq, const void *tk, const void *tv,
+                        void *o, void *to, float *lse, const float *slopes, const int32_t *key_begin,
+                        const int32_t *key_end, int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk, int64_t d,
+                        float scale, float softcap, void *stream) {
+    return fwd_scored(q, k, v, tq, tk, tv, o, to, lse, nullptr, slopes, key_begin, key_end, {B, H, Hkv, Lq, Lk, d},
+                      scale, softcap, stream);
+}
+
+int attn_jvp_fwd_scored_stats(const void *q, const void *k, const void *v, const void *tq, const void *tk,
+                              const void *tv, void *o, void *to, float *lse, float *mu, const float *slopes,
+                              const int32_t *key_begin, const int32_t *key_end, int64_t B, int64_t H, int64_t Hkv,
+                              int64_t Lq, int64_t Lk, int64_t d, float scale, float softcap, void *stream) {
+    if (B > 0 && H > 0 && Lq > 0 && (!lse || !mu)) return AJVP_ERR_INVALID_ARG;
+    return fwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, slopes, key_begin, key_end, {B, H, Hkv, Lq, Lk, d}, scale,
+                      softcap, stream);
+}
+
+uint64_t attn_jvp_bwd_scored_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk) {
+    const Sizes z{B, H, Hkv, Lq, Lk, bwd::HD};
+    if (check_sizes(z, 1.f, 0.f) != AJVP_OK || H == 0 || check_large(z) != AJVP_OK) return 0;
+    const uint64_t least = host::stats_bytes(B * H, Lq) + range_bytes(B, Lk);
+    int dev = 0;
+    if (host::device(&dev) != AJVP_OK) return least;  // no usable device: the minimum
+    return least + 2u * host::partial_bytes(B * Hkv, Lk, split_parts(z, host::sm_count(dev)));
+}
+
+int attn_jvp_bwd_scored(const void *q, const void *k, const void *v, const void *tq, const void *tk, const void *tv,
+                        const void *o, const void *to, const float *lse, const float *mu, const void *dout,
+                        const void *dtout, void *dq, void *dk, void *dv, void *dtq, void *dtk, void *dtv,
+                        const float *slopes, const int32_t *key_begin, const int32_t *key_end, int64_t B, int64_t H,
+                        int64_t Hkv, int64_t Lq, int64_t Lk, int64_t d, float scale, float softcap, void *workspace,
+                        uint64_t workspace_bytes, void *stream) {
+    const Sizes z{B, H, Hkv, Lq, Lk, d};
+    int rc = check_sizes(z, scale, softcap);
+    if (rc != AJVP_OK) return rc;
+    if (B == 0 || H == 0) return AJVP_OK;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if ((rc = check_large(z)) != AJVP_OK) return rc;
+    if (d != bwd::HD) return AJVP_ERR_UNSUPPORTED_DIM;
+    if (Lq == 0) {  // no query rows: the key-side gradients are zero
+        void *zero[4] = {dk, dv, dtk, dtv};
+        for (void *p : zero)
+            if (!p) return AJVP_ERR_INVALID_ARG;
+        for (void *p : zero) {
+            const cudaError_t e = cudaMemsetAsync(p, 0, (size_t)(B * Hkv * Lk * d) * 2u, st);
+            if (e != cudaSuccess) return host::fail(e);
+        }
+        return AJVP_OK;
+    }
+    for (const void *p : {q, k, v, tq, tk, tv, o, to, (const void *)lse, (const void *)mu, dout, dtout,
+                          (const void *)dq, (const void *)dk, (const void *)dv, (const void *)dtq, (const void *)dtk,
+                          (const void *)dtv}) {
+        if (!p) return AJVP_ERR_INVALID_ARG;
+        if (!host::aligned(p, 16)) return AJVP_ERR_MISALIGNED;
+    }
+    for (const void *p : {(const void *)slopes, (const void *)key_begin, (const void *)key_end})
+        if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
+    const int64_t BH = B * H, BHk = B * Hkv;
+    const uint64_t stats = host::stats_bytes(BH, Lq), ranges = range_bytes(B, Lk);
+    if (!workspace || !host::aligned(workspace, 256) || workspace_bytes < stats + ranges) return AJVP_ERR_WORKSPACE;
+    int dev = 0;
+    if ((rc = setup(&dev)) != AJVP_OK) return rc;
+    if ((rc = host::encoder()) != AJVP_OK) return rc;
+    // cut the streamed queries of the key side into parts when its key tiles alone
+    // cannot fill the GPU and the workspace holds the partial sums
+    int64_t parts = split_parts(z, host::sm_count(dev));
+    const uint64_t part_bytes = host::partial_bytes(BHk, Lk, parts);
+    if (workspace_bytes < stats + ranges + 2u * part_bytes) parts = 1;
+    uint8_t *const ws = static_cast<uint8_t *>(workspace);
+    float *const partial_k = reinterpret_cast<float *>(ws + stats + ranges);
+    float *const partial_v = reinterpret_cast<float *>(ws + stats + ranges + part_bytes);
+
+    const long long rows = (long long)(BH * Lq);
+    bwd::bwd_rowstats_kernel<<<(unsigned)std::min<long long>((rows + 7) / 8, 148LL * 16), 256, 0, st>>>(
+        static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(to),
+        static_cast<const __nv_bfloat16 *>(dout), static_cast<const __nv_bfloat16 *>(dtout), lse, mu,
+        static_cast<float4 *>(workspace), rows);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host::fail(e);
+    Score score = make_score(z, scale, softcap, slopes, key_begin, key_end);
+    if (key_begin || key_end) {
+        int2 *const out = reinterpret_cast<int2 *>(ws + stats);
+        query_range_kernel<<<dim3((unsigned)((Lk + 127) / 128), (unsigned)B), 256, 0, st>>>(score, (int)Lq, (int)Lk,
+                                                                                            out);
+        if ((e = cudaGetLastError()) != cudaSuccess) return host::fail(e);
+        score.qrange = out;
+    }
+    return with_mask(mask_bits(softcap, slopes), [&](auto mask) -> int {
+        constexpr int M = decltype(mask)::value, MS = M | bwd::MASK_SPLIT;
+        int r = launch_one<bwd::V_Q, M>({q, tq, dtout, dout}, {k, tk}, {v, tv}, dq, dtq, scale, score, workspace, BH,
+                                        BHk, Lq, Lk, Lq, scale, 1, nullptr, st);
+        if (r != AJVP_OK) return r;
+        if (parts > 1) {
+            r = launch_one<bwd::V_K, MS>({k, tk, v, tv}, {q, tq}, {dtout, dout}, dk, dtk, scale, score, workspace, BHk,
+                                         BH, Lk, Lq, Lq, scale, parts, partial_k, st);
+            if (r != AJVP_OK) return r;
+            return launch_one<bwd::V_V, MS>({k, tk}, {dout, dtout}, {q, tq}, dv, dtv, 1.f, score, workspace, BHk, BH,
+                                            Lk, Lq, Lq, scale, parts, partial_v, st);
+        }
+        r = launch_one<bwd::V_K, M>({k, tk, v, tv}, {q, tq}, {dtout, dout}, dk, dtk, scale, score, workspace, BHk, BH,
+                                    Lk, Lq, Lq, scale, 1, nullptr, st);
+        if (r != AJVP_OK) return r;
+        return launch_one<bwd::V_V, M>({k, tk}, {dout, dtout}, {q, tq}, dv, dtv, 1.f, score, workspace, BHk, BH, Lk,
+                                       Lq, Lq, scale, 1, nullptr, st);
+    });
+}
+
+}  // extern "C"

@@ -379,6 +379,96 @@ AJVP_API uint64_t attn_jvp_bwd_workspace_bytes_split(int64_t B, int64_t H, int64
 AJVP_API int64_t attn_jvp_bwd_key_split_parts(int64_t B, int64_t H, int64_t Lq, int64_t Lk, int64_t sm_count);
 
 /*
+ * attn_jvp_fwd_scored -- attn_jvp_fwd with modified scores: a tanh cap, a
+ * bias by distance, an interval of visible keys per query row, and key heads
+ * shared by groups of query heads.  For batch b, query head h (its key head
+ * h / (H / Hkv)), with z = s Q K^T and dz = s (tQ K^T + Q tK^T):
+ *
+ *   S_ij  = c tanh(z_ij / c) - slope_h |i + Lk - Lq - j|    (c = softcap)
+ *   dS_ij = (1 - tanh^2(z_ij / c)) dz_ij
+ *   P     = softmax of S_i. over key_begin[b][i] <= j < key_end[b][i]
+ *   O = P V,  tO = (P .* (dS - mu)) V + P tV,  mu = rowsum(P .* dS)
+ *
+ *   q, tq, o, to   : __nv_bfloat16 [B][H][Lq][d]
+ *   k, v, tk, tv   : __nv_bfloat16 [B][Hkv][Lk][d], H a multiple of Hkv
+ *   lse            : float [B][H][Lq] (natural log of the sum of exp S), or NULL
+ *   slopes         : DEVICE float [H], or NULL (no bias)
+ *   key_begin/_end : DEVICE int32 [B][Lq], or NULL (0 / Lk); values are clamped
+ *                    to [0, Lk]; a row with begin >= end sees nothing and gets
+ *                    O = tO = 0, lse = -infinity
+ *   softcap        : c > 0, or 0 for none
+ *
+ * An interval per row expresses prefix masks (end = max(prefix, i + 1)),
+ * document masks (the document's first key and end), frame-causal masks (the
+ * end of the row's frame), causal and sliding-window masks, and their
+ * combinations.  Rows need not be ordered: a CTA visits the keys between its
+ * rows' smallest and largest visible one, so ordered bounds skip the most.
+ * The pages describe none of these; each is the definition above.
+ *
+ * Supported: d == 128, Lq, Lk < 2^24; 2 s log2(e) / c finite; tensors and
+ * lse 16-byte, slopes and bounds 4-byte aligned; other rules and errors as
+ * attn_jvp_fwd (AJVP_ERR_INVALID_ARG also for H not a multiple of Hkv and for
+ * a negative or non-finite softcap).  Values of keys that a row does not see
+ * must be finite where they share a 64-key tile with keys that it sees.
+ */
+AJVP_API int attn_jvp_fwd_scored(const void *q, const void *k, const void *v,
+                        const void *tq, const void *tk, const void *tv,
+                        void *o, void *to, float *lse,
+                        const float *slopes, const int32_t *key_begin, const int32_t *key_end,
+                        int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk, int64_t d,
+                        float scale, float softcap, void *stream);
+
+/*
+ * attn_jvp_fwd_scored_stats -- attn_jvp_fwd_scored that also saves mu (float
+ * [B][H][Lq]; 0 for rows that see nothing), the statistics
+ * attn_jvp_bwd_scored needs beside lse.  lse and mu are required.
+ */
+AJVP_API int attn_jvp_fwd_scored_stats(const void *q, const void *k, const void *v,
+                        const void *tq, const void *tk, const void *tv,
+                        void *o, void *to, float *lse, float *mu,
+                        const float *slopes, const int32_t *key_begin, const int32_t *key_end,
+                        int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk, int64_t d,
+                        float scale, float softcap, void *stream);
+
+/*
+ * attn_jvp_bwd_scored -- backward pass of attn_jvp_fwd_scored: the gradients
+ * of L = sum <dout, O> + sum <dtout, tO> with respect to q, k, v, tq, tk, tv
+ * (the slopes and the cap are constants).
+ *
+ *   q, tq, o, to, dout, dtout, dq, dtq : __nv_bfloat16 [B][H][Lq][d]
+ *   k, v, tk, tv, dk, dv, dtk, dtv     : __nv_bfloat16 [B][Hkv][Lk][d]; a shared
+ *                         key head's gradient sums its group's, in fp32
+ *   lse, mu             : float [B][H][Lq] (attn_jvp_fwd_scored_stats)
+ *   slopes, key_begin, key_end, softcap : as the forward
+ *   workspace           : DEVICE memory, 256-byte aligned.  With
+ *                         attn_jvp_bwd_scored_workspace_bytes(...) bytes the
+ *                         key side may split its streamed queries over several
+ *                         CTAs (fp32 partial sums added up in order, so that
+ *                         results stay deterministic); the row statistics and
+ *                         query ranges alone, 16 (B H Lq + 64) and
+ *                         8 B ceil(Lk / 128) bytes, each rounded up to a
+ *                         multiple of 256, run it unsplit.
+ *
+ * Five kernels on `stream` (four without bounds, two more when the key side is
+ * split), no atomics.  Gradients of rows that see no key and of keys that no
+ * row sees are zero; Lq == 0 writes zeros to dk, dv, dtk, dtv.  Other rules
+ * and errors as attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
+ */
+AJVP_API int attn_jvp_bwd_scored(const void *q, const void *k, const void *v,
+                 const void *tq, const void *tk, const void *tv,
+                 const void *o, const void *to, const float *lse, const float *mu,
+                 const void *dout, const void *dtout,
+                 void *dq, void *dk, void *dv, void *dtq, void *dtk, void *dtv,
+                 const float *slopes, const int32_t *key_begin, const int32_t *key_end,
+                 int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk, int64_t d,
+                 float scale, float softcap, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Device workspace, in bytes, with which attn_jvp_bwd_scored may split its key
+ * side on the current device (0 for invalid sizes; without a usable device the
+ * least it accepts). */
+AJVP_API uint64_t attn_jvp_bwd_scored_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk);
+
+/*
  * attn_jvp_bwd_host -- attn_jvp_bwd on HOST buffers: every tensor argument
  * (the twelve inputs, lse and mu included, and the six gradients) is host
  * memory in the layouts of attn_jvp_bwd; pinned memory gives overlapped
