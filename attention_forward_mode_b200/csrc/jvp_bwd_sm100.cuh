@@ -606,12 +606,20 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 tma_load_3d(st + 2 * CHUNK_C, mx, fb, 64, y, z);
                 tma_load_3d(st + 3 * CHUNK_C, my, fb, 64, y, z);
             };
+            int tv = u0, zv = bh_c;  // scored: place in the slab's visible tiles, and slab, of the next tile
+            if (kScored && nt > 0) {
+                zv += u0 / ntv;
+                tv = u0 % ntv;
+            }
             for (int t = 0; t < nt && ok; ++t) {
                 int y = yc0 + (jt0 + t) * BN, z = bh;  // tensor row and slab of the streamed tile
                 if constexpr (kScored) {
-                    const int u = u0 + t, slab = u / ntv;
-                    y = (jt0 + u - slab * ntv) * BN;
-                    z = bh_c + slab;
+                    y = (jt0 + tv) * BN;
+                    z = zv;
+                    if (++tv == ntv) {
+                        tv = 0;
+                        ++zv;
+                    }
                 }
                 if (lp) {  // long ring, stage t % kLS: free once the G2 products of tile t - kLS are complete
                     const int s = t % C::kLS;
@@ -891,10 +899,10 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
         }
         // scored: log2-unit scores of two columns less lse2 (ls), the cap's tanh and derivative;
         // dist: distance of the row-side item to column c
-        auto score2 = [&](float2 x, float2 ls, float dist, float2 &t, float2 &df) -> float2 {
+        auto score2 = [&](auto small, float2 x, float2 ls, float dist, float2 &t, float2 &df) -> float2 {
             float2 y;
             if constexpr (kCap) {
-                cap2(x, p.score.cap_in, t, df);
+                cap2<decltype(small)::value>(p.score, x, t, df);
                 y = __ffma2_rn(t, make_float2(p.score.cap_out, p.score.cap_out), make_float2(-ls.x, -ls.y));
             } else {
                 y = __ffma2_rn(x, c2, make_float2(-ls.x, -ls.y));
@@ -905,7 +913,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
         };
         // one pair of columns (c, c + 1 of this group): x scores, y score tangent,
         // z A, w B -> r1, r2 (see the variant table)
-        auto pair = [&](int c, int lo, int hi, uint32_t vis, float dist, bool masked, uint32_t st_base, uint32_t xa, uint32_t xb, uint32_t ya,
+        auto pair = [&](auto small, int c, int lo, int hi, uint32_t vis, float dist, bool masked, uint32_t st_base, uint32_t xa, uint32_t xb, uint32_t ya,
                         uint32_t yb, uint32_t za, uint32_t zb, uint32_t wa, uint32_t wb, float2 &r1, float2 &r2) {
             float4 sa = rs, sb = rs;  // statistics of columns c and c + 1
             if (C::kColStats) {
@@ -916,7 +924,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
             [[maybe_unused]] float2 th = make_float2(0.f, 0.f), df = make_float2(1.f, 1.f);
             float2 t;
             if constexpr (kScored)
-                t = score2(x, make_float2(sa.x, sb.x), dist - (float)c, th, df);
+                t = score2(small, x, make_float2(sa.x, sb.x), dist - (float)c, th, df);
             else
                 t = __ffma2_rn(x, c2, make_float2(-sa.x, -sb.x));
             const float2 pp = make_float2(ex2_approx(t.x), ex2_approx(t.y));
@@ -946,16 +954,24 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
             }
         };
 
+        int tv = u0, hv = bh_c - sb * p.score.H;  // scored: place in the slab's visible tiles, and head, of the next tile
+        if (kScored && nt > 0) {
+            hv += u0 / ntv;
+            tv = u0 % ntv;
+        }
         for (int j = 0; j < nt; ++j) {
             const int b = j % C::kNB, s = j % C::kLS;
             int tile = jt0 + j;
             int2 cb = make_int2(0, 0);  // scored key side: the visible keys of this lane's streamed query
             if constexpr (kScored) {
-                const int u = u0 + j, slab = u / ntv;
-                tile = jt0 + u - slab * ntv;
+                tile = jt0 + tv;
                 if (VAR != V_Q) {
                     cb = row_bounds(p.score, sb, tile * BN + (int)col0 + lane, Lcol_s, Lrow_s);
-                    if (kBias) slope2 = p.score.slopes[bh_c - sb * p.score.H + slab] * 1.4426950408889634f;
+                    if (kBias) slope2 = p.score.slopes[hv] * 1.4426950408889634f;
+                }
+                if (++tv == ntv) {
+                    tv = 0;
+                    ++hv;
                 }
             }
             // V_Q, V_K: Z and W first (complete well before X and Y)
@@ -1053,6 +1069,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                         tmem_ld16(tb + col0 + C::X + 16u * hh, xr);
                         tmem_ld16(tb + col0 + C::Y + 16u * hh, yr);
                         tmem_wait_ld();
+                        auto columns = [&](auto small) {
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const int c = 16 * hh + i;
@@ -1064,7 +1081,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                             [[maybe_unused]] float2 th = make_float2(0.f, 0.f), df = make_float2(1.f, 1.f);
                             float2 tt;
                             if constexpr (kScored)
-                                tt = score2(x, ls, dist - (float)c, th, df);
+                                tt = score2(small, x, ls, dist - (float)c, th, df);
                             else
                                 tt = __ffma2_rn(x, c2, make_float2(-ls.x, -ls.y));
                             const float2 pp = make_float2(ex2_approx(tt.x), ex2_approx(tt.y));
@@ -1095,6 +1112,13 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                             h1[i / 2] = pack_bf16x2(r1.x, r1.y);
                             h2[i / 2] = pack_bf16x2(r2.x, r2.y);
                         }
+                        };
+                        bool small = false;  // (capped: every score of the warp in the polynomial's range)
+                        if constexpr (kCap) small = cap_all_small(p.score, xr);
+                        if (kCap && small)
+                            columns(std::true_type{});
+                        else
+                            columns(std::false_type{});
                         tmem_st8(tb + col0 + C::E1 + 8u * hh, h1);
                         tmem_st8(tb + col0 + C::E2 + 8u * hh, h2);
                     }
@@ -1112,22 +1136,28 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
                 tmem_wait_ld();
                 // the per-column mask only for tiles that reach past the end or cross the
                 // causal diagonal (most tiles see all their columns); one choice per warp
-                if (kScored ? full : __all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
+                auto columns = [&](auto masked_c, auto small) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float2 r1, r2;
-                        pair(i, lo, hi, vis, dist, false, st_base, xr[i], xr[i + 1], yr[i], yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
+                        pair(small, i, lo, hi, vis, dist, decltype(masked_c)::value, st_base, xr[i], xr[i + 1], yr[i],
+                             yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
                         e1[i / 2] = pack_bf16x2(r1.x, r1.y);
                         e2[i / 2] = pack_bf16x2(r2.x, r2.y);
                     }
+                };
+                bool small = false;  // (capped: every score of the warp in the polynomial's range)
+                if constexpr (kCap) small = cap_all_small(p.score, xr);
+                const bool clear = kScored ? full : __all_sync(0xffffffffu, lo <= 0 && hi >= 32);
+                if (kCap && small) {
+                    if (clear)
+                        columns(std::false_type{}, std::true_type{});
+                    else
+                        columns(std::true_type{}, std::true_type{});
+                } else if (clear) {
+                    columns(std::false_type{}, std::false_type{});
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float2 r1, r2;
-                        pair(i, lo, hi, vis, dist, true, st_base, xr[i], xr[i + 1], yr[i], yr[i + 1], 0u, 0u, 0u, 0u, r1, r2);
-                        e1[i / 2] = pack_bf16x2(r1.x, r1.y);
-                        e2[i / 2] = pack_bf16x2(r2.x, r2.y);
-                    }
+                    columns(std::true_type{}, std::false_type{});
                 }
             }
             // over this group's own columns of X and Y (the previous tile's G2, which read

@@ -57,6 +57,8 @@
 // epilogue to have read O / T (B_OT_FREE).
 #pragma once
 
+#include <type_traits>
+
 #include "ptx_sm100.cuh"
 #include "score_sm100.cuh"
 
@@ -202,7 +204,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
     constexpr bool kCausal = (MASK & MASK_CAUSAL) != 0, kPacked = (MASK & MASK_PACKED) != 0;
     constexpr bool kScored = (MASK & MASK_SCORED) != 0, kCap = (MASK & MASK_CAP) != 0, kBias = (MASK & MASK_BIAS) != 0;
     static_assert(!kScored || (!kSplit && !kCausal && !kPacked), "the scored form is a dense bf16 kernel");
+    constexpr bool kFixed = (MASK & MASK_FIXED) != 0;
     static_assert(kScored || (!kCap && !kBias), "caps and biases belong to the scored form");
+    static_assert(!kFixed || kCap, "a fixed reference needs bounded scores");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -299,6 +303,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         yk0 = kbase;
     }
     const int nk = (kend - kbase + BC - 1) / BC;
+    // the t-th key tile that the CTA visits.  Biased scores: from the tile at the last row's
+    // position down to the first, then the tiles behind it, so that the largest bias comes
+    // first and the reference hardly ever rises (visited in order, steep slopes would
+    // rescale the accumulators at every tile: 1051 instead of 921 us per call at 12 heads of
+    // 8190 keys)
+    const int diag = min(max((q0 + BR - 1 + koff - kbase) / BC, 0), nk - 1);
+    auto key_tile = [&](int t) -> int { return kBias && !kFixed && t <= diag ? diag - t : t; };
     if (MASK != 0 && nk == 0) {
         // no row of the tile sees a key: zeros and lse = -inf, no pipeline at all
         for (int r = threadIdx.x; r < BR && q0 + r < Lq_s; r += blockDim.x) {
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         }
                         const uint32_t st = base + SM_KT + s * KT_STAGE;
                         const uint32_t fb = BAR(B_KT_FULL + s);
-                        const int y = yk0 + t * BC;
+                        const int y = yk0 + key_tile(t) * BC;
                         mbar_arrive_expect_tx(fb, KT_STAGE);
                         // chunk c: K rows then tK rows, so [K | tK] is one N = 128 operand
                         tma_load_3d(st, &p.tm_k, fb, 0, y, kScored ? bh_kv : bh_n);
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         }
                         const uint32_t st = base + SM_VT + s * VT_STAGE;
                         const uint32_t fb = BAR(B_VT_FULL + s);
-                        const int y = yk0 + (t - 1) * BC;
+                        const int y = yk0 + key_tile(t - 1) * BC;
                         mbar_arrive_expect_tx(fb, VT_STAGE);
                         // [V c0 | V c1 | tV c0 | tV c1]: N-chunks 64 columns apart (LBO)
                         tma_load_3d(st, &p.tm_v, fb, 0, y, kScored ? bh_kv : bh_n);
@@ -580,11 +591,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         const int row = wl * 32 + lane;
         const uint32_t lane_off = (uint32_t)(wl * 32) << 16;
         const uint32_t col0 = 32u * (uint32_t)grp;
-        const float c = p.scale_log2;
+        // log2-unit scores are c times the row's values: raw scores, or the cap's tanh
+        const float c = kCap ? p.score.cap_out : p.scale_log2;
         const float2 c2 = make_float2(c, c);
         const float2 s2 = make_float2(p.scale, p.scale);
-        // row max of c*S is c * max(S) (min(S) for c < 0); the scored form's row holds modified scores
-        const bool up = kScored || c >= 0.f;
+        // bias: does the maximum take raw scores and biases separately (else the values
+        // become the log2-unit scores before it)
+        float slope2 = 0.f;  // slope in log2 units
+        if constexpr (kBias) slope2 = p.score.slopes[bh % p.score.H] * 1.4426950408889634f;
+        const bool raw_max = kBias && !kCap && fabsf(slope2) * (float)(BC - 1) <= STEEP_LOG2;
+        // row max of c*S is c * max(S) (min(S) for c < 0)
+        const bool up = (kBias && !raw_max) || c >= 0.f;
         const float sentinel = up ? -INFINITY : INFINITY;
         float *xch = reinterpret_cast<float *>(gbase + kXch);
         bool failed = false;
@@ -604,16 +621,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             // keys this row sees (a prefix of the sequence's keys; may be <= 0 when causal)
             const int kcount = kCausal ? min(Lk_s, q0_n + row + koff + 1) : Lk_s;
             int2 seen = make_int2(0, 0);  // scored: this row's keys, relative to kbase
-            float slope2 = 0.f, dist0 = 0.f;  // bias: slope in log2 units; distance to the first streamed key
+            float dist0 = 0.f;            // bias: distance to this group's first streamed key
             if constexpr (kScored) {
                 const int sb = bh / p.score.H;
                 seen = row_bounds(p.score, sb, q0 + row, Lq_s, Lk_s);
                 seen.x -= kbase;
                 seen.y -= kbase;
-                if (kBias) {
-                    slope2 = p.score.slopes[bh - sb * p.score.H] * 1.4426950408889634f;
-                    dist0 = (float)(q0 + row + koff - kbase - (int)col0);
-                }
+                if (kBias) dist0 = (float)(q0 + row + koff - kbase - (int)col0);
+                if (kFixed) m_ref = kBias ? largest_bias(slope2, q0 + row + koff - kbase, seen.x, seen.y) : 0.f;
             }
 
             for (int j = 0; j < nk; ++j) {
@@ -622,8 +637,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 const uint32_t t_s = tbase + lane_off + TM_BUF + 128u * b;
                 if (!failed) failed = !mbar_wait_warp(BAR(B_SD_FULL + b), (G >> 1) & 1, abort_flag, bound);
                 uint32_t xs[32], xd[32];
-                const int valid = kcount - j * BC - (int)col0;  // visible keys of this group (may be <= 0)
-                const int lo = seen.x - j * BC - (int)col0, hi = seen.y - j * BC - (int)col0;  // (scored)
+                const int jk = key_tile(j) * BC;  // the tile's first key, relative to kbase
+                const int valid = kcount - jk - (int)col0;  // visible keys of this group (may be <= 0)
+                const int lo = seen.x - jk - (int)col0, hi = seen.y - jk - (int)col0;  // (scored)
                 float part = sentinel;
                 if (!failed) {
                     tc_fence_after();
@@ -631,36 +647,54 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                     tmem_ld32(t_s + 64 + col0, xd);
                     tmem_wait_ld();
                     if constexpr (kScored) {
-                        // scores in log2 units: c x, or cap_out tanh, less the bias; the score tangent
-                        // takes the cap's derivative here
+                        if constexpr (kCap) {  // tanh, and the score tangent times its derivative
+                            auto cap = [&](auto small) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 x = make_float2(__uint_as_float(xs[i]), __uint_as_float(xs[i + 1]));
-                            float2 y;
-                            if constexpr (kCap) {
-                                float2 t, df;
-                                cap2(x, p.score.cap_in, t, df);
-                                y = __fmul2_rn(t, make_float2(p.score.cap_out, p.score.cap_out));
-                                const float2 d =
-                                    __fmul2_rn(make_float2(__uint_as_float(xd[i]), __uint_as_float(xd[i + 1])), df);
-                                xd[i] = __float_as_uint(d.x);
-                                xd[i + 1] = __float_as_uint(d.y);
+                                for (int i = 0; i < 32; i += 2) {
+                                    float2 t, df;
+                                    cap2<decltype(small)::value>(
+                                        p.score, make_float2(__uint_as_float(xs[i]), __uint_as_float(xs[i + 1])), t, df);
+                                    const float2 d =
+                                        __fmul2_rn(make_float2(__uint_as_float(xd[i]), __uint_as_float(xd[i + 1])), df);
+                                    xs[i] = __float_as_uint(t.x);
+                                    xs[i + 1] = __float_as_uint(t.y);
+                                    xd[i] = __float_as_uint(d.x);
+                                    xd[i + 1] = __float_as_uint(d.y);
+                                }
+                            };
+                            if (cap_all_small(p.score, xs))
+                                cap(std::true_type{});
+                            else
+                                cap(std::false_type{});
+                        }
+                        if (kBias && !raw_max) {  // log2-unit scores c x - slope |e - i|
+                            const float e = dist0 - (float)jk;
+                            // tiles off the diagonal: |e - i| = side (e - i), linear in i
+                            const bool before = __all_sync(0xffffffffu, e >= 31.f);
+                            if (before || __all_sync(0xffffffffu, e <= 0.f)) {
+                                const float inc = before ? slope2 : -slope2, b0 = -inc * e;
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    const float2 bias = __ffma2_rn(make_float2(inc, inc),
+                                                                   make_float2((float)i, (float)(i + 1)),
+                                                                   make_float2(b0, b0));
+                                    const float2 y = __ffma2_rn(
+                                        make_float2(__uint_as_float(xs[i]), __uint_as_float(xs[i + 1])), c2, bias);
+                                    xs[i] = __float_as_uint(y.x);
+                                    xs[i + 1] = __float_as_uint(y.y);
+                                }
                             } else {
-                                y = __fmul2_rn(x, c2);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    xs[i] = __float_as_uint(
+                                        fmaf(__uint_as_float(xs[i]), c, -slope2 * fabsf(e - (float)i)));
                             }
-                            if constexpr (kBias) {
-                                const float e = dist0 - (float)(j * BC);
-                                y = __ffma2_rn(make_float2(-slope2, -slope2),
-                                               make_float2(fabsf(e - (float)i), fabsf(e - (float)(i + 1))), y);
-                            }
-                            xs[i] = __float_as_uint(y.x);
-                            xs[i + 1] = __float_as_uint(y.y);
                         }
                         if (lo > 0 || hi < 32) {
                             const uint32_t vis = bit_range(lo, hi);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!((vis >> i) & 1u)) xs[i] = __float_as_uint(-INFINITY);
+                                if (!((vis >> i) & 1u)) xs[i] = __float_as_uint(sentinel);
                         }
                     } else if (valid < 32) {
 #pragma unroll
@@ -670,7 +704,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                     float m4[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(xs[k]);
-                    if (up) {
+                    if (kFixed) {
+                    } else if (up) {
 #pragma unroll
                         for (int i = 4; i < 28; i += 8)
 #pragma unroll
@@ -689,18 +724,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         for (int k = 0; k < 4; ++k) m4[k] = fminf(m4[k], __uint_as_float(xs[28 + k]));
                         part = fminf(fmin3(m4[0], m4[1], m4[2]), m4[3]);
                     }
-                    xch[(b * 2 + grp) * 128 + row] = part;
+                    if (!kFixed) xch[(b * 2 + grp) * 128 + row] = part;
                 }
                 // both groups' partial maxima are in shared memory; every softmax
                 // thread reaches this barrier each tile, and a failure anywhere
                 // ends the loop for all of them together
-                if (named_bar_or(NB_TILE, SOFTMAX_THREADS, failed)) {
+                if (!kFixed && named_bar_or(NB_TILE, SOFTMAX_THREADS, failed)) {
                     failed = true;
                     break;
                 }
-                const float other = xch[(b * 2 + (grp ^ 1)) * 128 + row];
-                const float m_tile = kScored ? fmaxf(part, other) : (up ? fmaxf(part, other) : fminf(part, other)) * c;
-                if (j == 0) {
+                const float other = kFixed ? 0.f : xch[(b * 2 + (grp ^ 1)) * 128 + row];
+                float m_tile = (kBias && !raw_max) ? fmaxf(part, other) : (up ? fmaxf(part, other) : fminf(part, other)) * c;
+                if (kBias && raw_max)  // (-infinity: the row sees no key of the tile)
+                    m_tile += largest_bias(slope2, q0 + row + koff - kbase, jk, jk + BC);
+                if (kFixed) {
+                } else if (j == 0) {
                     m_ref = m_tile;
                 } else {
                     const bool need = m_tile > m_ref + RESCALE_THRESHOLD;
@@ -784,15 +822,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         }
                     }
                 }
-                if (failed) continue;  // the next tile's barrier carries the failure to everyone
-                // (scored: hidden keys hold -infinity, which gives 0 against any finite reference)
+                if (failed) continue;  // the next tile's barrier (the epilogue's, kFixed) carries the failure to everyone
+                // (scored: hidden keys hold a score of -infinity, which gives 0 against any finite reference)
                 const float nm = kScored && m_ref == -INFINITY ? 0.f : -m_ref;
                 const float2 nm2 = make_float2(nm, nm);
                 float pv[32];
+                if (kBias && raw_max) {
+                    // c x - slope |e - i| - m; off the diagonal |e - i| is linear in i
+                    const float e = dist0 - (float)jk;
+                    const bool before = __all_sync(0xffffffffu, e >= 31.f);
+                    if (before || __all_sync(0xffffffffu, e <= 0.f)) {
+                        const float inc = before ? slope2 : -slope2, b0 = fmaf(-inc, e, nm);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 bias = __ffma2_rn(make_float2(inc, inc), make_float2((float)i, (float)(i + 1)),
+                                                           make_float2(b0, b0));
+                            const float2 y = __ffma2_rn(
+                                make_float2(__uint_as_float(xs[i]), __uint_as_float(xs[i + 1])), c2, bias);
+                            pv[i] = ex2_approx(y.x);
+                            pv[i + 1] = ex2_approx(y.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            pv[i] = ex2_approx(fmaf(__uint_as_float(xs[i]), c, fmaf(-slope2, fabsf(e - (float)i), nm)));
+                    }
+                } else
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 x = make_float2(__uint_as_float(xs[2 * i]), __uint_as_float(xs[2 * i + 1]));
-                    const float2 y = kScored ? __fadd2_rn(x, nm2) : __ffma2_rn(x, c2, nm2);
+                    const float2 y = kBias ? __fadd2_rn(x, nm2) : __ffma2_rn(x, c2, nm2);
                     pv[2 * i] = ex2_approx(y.x);
                     pv[2 * i + 1] = ex2_approx(y.y);
                 }

@@ -18,6 +18,14 @@ namespace ajvp {
 
 // MASK bits of the scored kernels (beside those of the kernels' own)
 constexpr int MASK_SCORED = 8, MASK_CAP = 16, MASK_BIAS = 32;
+// Forward, capped scores whose log2-unit cap is at most FIXED_CAP: |c log2(e) tanh| <= FIXED_CAP
+// bounds every score before its bias, so each row keeps one reference for all
+// its keys (the largest bias among them) in place of a running maximum: weights
+// lie within 2^-80 .. 2^80 of it before the bias, inside the range of fp32 and
+// bf16 with room for sums of 2^24 keys.  No maxima, no exchange of them between
+// the softmax groups, no rescaling.
+constexpr int MASK_FIXED = 64;
+constexpr float FIXED_CAP = 80.f;
 
 struct Score {
     const int *begin, *end;  // [B][Lq] visible keys of each query row, or NULL: 0 / Lk
@@ -25,6 +33,7 @@ struct Score {
     const int2 *qrange;      // backward: [B][n_rtiles] first and end query row that sees a key of the 128-key tile
                              // (NULL: every row)
     float cap_in;            // 2 s log2(e) / c: tanh(z / c) = 1 - 2 / (1 + 2^(cap_in x)) of a raw score x = z / s
+    float cap_w;             // s / c: z / c = cap_w x
     float cap_out;           // c log2(e): the capped score in log2 units is cap_out tanh
     float cap_second;        // 2 / c
     int H, Hkv, group;       // query heads, key heads, query heads per key head
@@ -62,6 +71,23 @@ __device__ __forceinline__ int2 tile_key_range(const Score &sc, int b, int row0,
     return hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
+// Forward, biased scores without a cap: the running reference takes the largest
+// raw score of a tile's 64 keys and, separately, their largest bias.  Their sum
+// is above every score of the tile by at most 63 |slope| log2(e) more than it
+// need be, so up to this many log2 units the row's largest weight stays a normal
+// number 2^24 times above the smallest; steeper slopes form each score before the
+// maximum (one more packed operation and a dependence per score ahead of the
+// exchange of the maxima).
+constexpr float STEEP_LOG2 = 100.f;
+
+// the largest bias -slope2 |pos - j| over the keys lo <= j < hi (0 without keys)
+__device__ __forceinline__ float largest_bias(float slope2, int pos, int lo, int hi) {
+    if (lo >= hi) return 0.f;
+    const float near = (float)max(max(lo - pos, pos - (hi - 1)), 0);
+    const float far = (float)max(abs(pos - lo), abs(pos - (hi - 1)));
+    return fmaxf(-slope2 * near, -slope2 * far);
+}
+
 // bits i of a 32-wide tile with lo <= i < hi
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     const uint32_t below_hi = hi <= 0 ? 0u : (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u);
@@ -85,6 +111,43 @@ __device__ __forceinline__ void cap2(float2 x, float cap_in, float2 &t, float2 &
     t = __ffma2_rn(r, make_float2(-2.f, -2.f), make_float2(1.f, 1.f));
     const float2 r4 = __fmul2_rn(r, make_float2(4.f, 4.f));
     df = __ffma2_rn(r4, make_float2(-r.x, -r.y), r4);
+}
+
+// The same where |z / c| <= CAP_SMALL, without the special-function unit (two
+// of whose operations per score are what bounds the elementwise warps): with
+// w = z / c, tanh w = w P(w^2), P the polynomial of degree 4 that minimises the
+// largest error on [-CAP_SMALL, CAP_SMALL] (fitted by the Remez exchange, 3e-8
+// absolute).  A warp takes it when every score that it holds is that small;
+// scores under a cap that shapes only their tail are.
+constexpr float CAP_SMALL = 0.625f;
+__device__ __forceinline__ void cap2_small(float2 x, float cap_w, float2 &t, float2 &df) {
+    const float2 w = __fmul2_rn(x, make_float2(cap_w, cap_w));
+    const float2 v = __fmul2_rn(w, w);
+    float2 r = __ffma2_rn(v, make_float2(0.014530068f, 0.014530068f), make_float2(-0.051362868f, -0.051362868f));
+    r = __ffma2_rn(r, v, make_float2(0.13291031f, 0.13291031f));
+    r = __ffma2_rn(r, v, make_float2(-0.33330483f, -0.33330483f));
+    r = __ffma2_rn(r, v, make_float2(0.99999946f, 0.99999946f));
+    t = __fmul2_rn(r, w);
+    df = __ffma2_rn(t, make_float2(-t.x, -t.y), make_float2(1.f, 1.f));
+}
+template <bool kSmall>
+__device__ __forceinline__ void cap2(const Score &sc, float2 x, float2 &t, float2 &df) {
+    if constexpr (kSmall)
+        cap2_small(x, sc.cap_w, t, df);
+    else
+        cap2(x, sc.cap_in, t, df);
+}
+
+// every score that the warp holds is inside the polynomial's range (false for NaN)
+template <int N>
+__device__ __forceinline__ bool cap_all_small(const Score &sc, const uint32_t (&x)[N]) {
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        m[0] = fmax3(m[0], fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
+        m[1] = fmax3(m[1], fabsf(__uint_as_float(x[i + 2])), fabsf(__uint_as_float(x[i + 3])));
+    }
+    return __all_sync(0xffffffffu, fmaxf(m[0], m[1]) * fabsf(sc.cap_w) <= CAP_SMALL);
 }
 
 // [B][n_ktiles] query rows (first, end) that see a key of each 128-key tile,

@@ -61,6 +61,8 @@ int setup(int *dev) {
         if (s.error == cudaSuccess) s.error = set_mask<MASK_SCORED | MASK_CAP>();
         if (s.error == cudaSuccess) s.error = set_mask<MASK_SCORED | MASK_BIAS>();
         if (s.error == cudaSuccess) s.error = set_mask<MASK_SCORED | MASK_CAP | MASK_BIAS>();
+        if (s.error == cudaSuccess) s.error = set_fwd<MASK_SCORED | MASK_CAP | MASK_FIXED>();
+        if (s.error == cudaSuccess) s.error = set_fwd<MASK_SCORED | MASK_CAP | MASK_BIAS | MASK_FIXED>();
     });
     return s.error == cudaSuccess ? AJVP_OK : host::fail(s.error);
 }
@@ -97,6 +99,7 @@ Score make_score(const Sizes &z, float scale, float softcap, const float *slopes
     s.slopes = slopes;
     if (softcap > 0.f) {
         s.cap_in = 2.f * scale * kLog2e / softcap;
+        s.cap_w = scale / softcap;
         s.cap_out = softcap * kLog2e;
         s.cap_second = 2.f / softcap;
     }
@@ -158,12 +161,19 @@ int fwd_scored(const void *q, const void *k, const void *v, const void *tq, cons
     p.Lk = (int)z.Lk;
     p.n_qtiles = (int)((z.Lq + sm100::BR - 1) / sm100::BR);
     p.scale = scale;
-    p.scale_log2 = scale * kLog2e;
+    // hidden keys hold +-infinity in units of 1 / scale_log2, which must not be zero
+    p.scale_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;
     p.bound_ns = host::wait_bound_ns();
     p.score = make_score(z, scale, softcap, slopes, key_begin, key_end);
     return with_mask(mask_bits(softcap, slopes), [&](auto mask) {
-        sm100::attn_jvp_fwd_kernel<false, decltype(mask)::value>
-            <<<(unsigned)(p.n_qtiles * BH), sm100::NTHREADS, sm100::SMEM_BYTES, (cudaStream_t)stream>>>(p);
+        constexpr int M = decltype(mask)::value;
+        const dim3 grid((unsigned)(p.n_qtiles * BH));
+        if ((M & MASK_CAP) != 0 && p.score.cap_out <= FIXED_CAP)
+            sm100::attn_jvp_fwd_kernel<false, (M & MASK_CAP) != 0 ? M | MASK_FIXED : M>
+                <<<grid, sm100::NTHREADS, sm100::SMEM_BYTES, (cudaStream_t)stream>>>(p);
+        else
+            sm100::attn_jvp_fwd_kernel<false, M>
+                <<<grid, sm100::NTHREADS, sm100::SMEM_BYTES, (cudaStream_t)stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? AJVP_OK : host::fail(e);
     });
