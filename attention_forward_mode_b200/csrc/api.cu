@@ -635,7 +635,6 @@ uint64_t wait_bound_ns() { return g_bound_ns.load(); }
 int encode(CUtensorMap *m, const void *ptr, int64_t d, int64_t L, int64_t BH, uint32_t box_rows) {
     return encode_3d(m, ptr, d, L, BH, box_rows);
 }
-int64_t key_split(int64_t BH, int64_t Lq, int64_t Lk, int sm_count) { return bwd_key_split(BH, Lq, Lk, sm_count); }
 uint64_t stats_bytes(int64_t BH, int64_t Lq) { return bwd_stats_bytes(BH, Lq); }
 uint64_t partial_bytes(int64_t BH, int64_t Lk, int64_t parts) { return bwd_partial_bytes(BH, Lk, parts); }
 }  // namespace host

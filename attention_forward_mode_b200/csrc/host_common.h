@@ -20,7 +20,6 @@ int encoder();                    // resolves cuTensorMapEncodeTiled
 uint64_t wait_bound_ns();
 // [BH][L][d] bf16 tensor, boxes of 64 columns x box_rows rows, 128-byte swizzle
 int encode(CUtensorMap *m, const void *ptr, int64_t d, int64_t L, int64_t BH, uint32_t box_rows);
-int64_t key_split(int64_t BH, int64_t Lq, int64_t Lk, int sm_count);
 uint64_t stats_bytes(int64_t BH, int64_t Lq);
 uint64_t partial_bytes(int64_t BH, int64_t Lk, int64_t parts);
 

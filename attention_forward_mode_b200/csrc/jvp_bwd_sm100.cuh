@@ -201,6 +201,37 @@ static __global__ void __launch_bounds__(256) bwd_split_reduce_kernel(const floa
     }
 }
 
+// The same for both split scored variants in one launch (blockIdx.y: dK/dtK or
+// dV/dtV), whose two accumulators share one output scale each.
+static __global__ void __launch_bounds__(256) scored_reduce_kernel(const float4 *__restrict__ pk,
+                                                                   const float4 *__restrict__ pv, int n_split,
+                                                                   long long rows, __nv_bfloat16 *__restrict__ dk,
+                                                                   __nv_bfloat16 *__restrict__ dtk,
+                                                                   __nv_bfloat16 *__restrict__ dv,
+                                                                   __nv_bfloat16 *__restrict__ dtv, float sk) {
+    const bool vside = blockIdx.y != 0;
+    const float4 *__restrict__ partial = vside ? pv : pk;
+    const float sc = vside ? 1.f : sk;
+    const long long n4 = rows * 2 * (HD / 4);  // float4s of one part
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n4;
+         i += (long long)gridDim.x * blockDim.x) {
+        float4 acc = partial[i];
+        for (int s = 1; s < n_split; ++s) {
+            const float4 v = partial[(size_t)s * (size_t)n4 + (size_t)i];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        const long long row = i / (2 * (HD / 4));
+        const int a = (int)((i / (HD / 4)) & 1), c4 = (int)(i % (HD / 4));
+        uint2 w;
+        w.x = pack_bf16x2(acc.x * sc, acc.y * sc);
+        w.y = pack_bf16x2(acc.z * sc, acc.w * sc);
+        *reinterpret_cast<uint2 *>((vside ? (a ? dtv : dv) : (a ? dtk : dk)) + (size_t)row * HD + 4u * c4) = w;
+    }
+}
+
 // Bounded warp-wide wait of the elementwise warps: all 32 lanes poll the
 // barrier together and leave when every lane has seen the phase complete
 // (no lane spins alone while the others wait at a reconvergence point, so
@@ -405,8 +436,9 @@ struct Var {
 // both CTAs' warps).
 // Both CTAs meet at a cluster barrier after setting up and before releasing
 // tensor memory, so neither leaves while the other may still reach it.
+// cta: the CTA's index among those of this variant.
 template <int VAR, int MASK, bool kPair>
-__device__ __forceinline__ void bwd_body(const Params &p) {
+__device__ __forceinline__ void bwd_body(const Params &p, const unsigned cta) {
     using C = Var<VAR, kPair>;
     constexpr bool kCausal = (MASK & MASK_CAUSAL) != 0, kPacked = (MASK & MASK_PACKED) != 0;
     constexpr bool kSplitK = (MASK & MASK_SPLIT) != 0;
@@ -435,7 +467,7 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
     if (kPacked) {
         // (sequence, head) major, row tiles fastest (they share the streamed rows in
         // L2); offsets clamped into the tensors so that bad ones stay memory-safe
-        const int u = (int)(blockIdx.x % p.n_rtiles), sh = (int)(blockIdx.x / p.n_rtiles);
+        const int u = (int)(cta % p.n_rtiles), sh = (int)(cta / p.n_rtiles);
         const int b = sh / p.BH;
         bh = sh % p.BH;
         rt = (kCausal && VAR == V_Q) ? p.n_rtiles - 1 - u : u;  // causal dQ: late (heavy) tiles first
@@ -443,19 +475,26 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
         Lrow_s = max(min(max(p.cu_row[b + 1], 0), p.Lrow), yr0) - yr0;
         yc0 = min(max(p.cu_col[b], 0), p.Lcol);
         Lcol_s = max(min(max(p.cu_col[b + 1], 0), p.Lcol), yc0) - yc0;
+    } else if (kScored) {
+        // groups of slabs whose streamed tensors fit the L2 together, row tiles of all the
+        // group's slabs with the heavy ones under ordered masks (late queries, early keys)
+        // first; split: all tiles of part 0, then of part 1, ...
+        const int u = (int)(cta % (unsigned)(p.n_rtiles * p.BH)), g = u / (p.n_rtiles * p.score.slabs);
+        const int in = u - g * p.n_rtiles * p.score.slabs, n = min(p.score.slabs, p.BH - g * p.score.slabs);
+        bh = g * p.score.slabs + in % n;
+        rt = VAR == V_Q ? p.n_rtiles - 1 - in / n : in / n;
     } else if (kSplitK) {
         // split-major: the n_rtiles * BH tiles of part 0, then of part 1, ...
-        const int cta = (int)(blockIdx.x % (unsigned)(p.n_rtiles * p.BH));
-        rt = cta % p.n_rtiles;
-        bh = cta / p.n_rtiles;
+        const int u = (int)(cta % (unsigned)(p.n_rtiles * p.BH));
+        rt = u % p.n_rtiles;
+        bh = u / p.n_rtiles;
     } else {
         // causal dQ / dtQ: the late (heavy) query tiles of each head first
-        rt = (kCausal && VAR == V_Q) ? p.n_rtiles - 1 - (int)(blockIdx.x % p.n_rtiles)
-                                     : (int)(blockIdx.x % p.n_rtiles);
-        bh = blockIdx.x / p.n_rtiles;
+        rt = (kCausal && VAR == V_Q) ? p.n_rtiles - 1 - (int)(cta % p.n_rtiles) : (int)(cta % p.n_rtiles);
+        bh = cta / p.n_rtiles;
     }
     // split: this CTA's part of the streamed range
-    const int sp = kSplitK ? (int)(blockIdx.x / (unsigned)(p.n_rtiles * p.BH)) : 0;
+    const int sp = kSplitK ? (int)(cta / (unsigned)(p.n_rtiles * p.BH)) : 0;
     const int r0 = rt * BM;  // local first row
     if (kPacked && r0 >= Lrow_s) return;  // past the end of this sequence (uniform for the CTA)
     const int yr = yr0 + r0;              // tensor row of the tile's first row
@@ -1259,14 +1298,36 @@ __device__ __forceinline__ void bwd_body(const Params &p) {
 
 template <int VAR, int MASK = 0>
 __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_bwd_kernel(const __grid_constant__ Params p) {
-    bwd_body<VAR, MASK, false>(p);
+    bwd_body<VAR, MASK, false>(p, blockIdx.x);
 }
 
 // The dQ / dK variants as CTA pairs (grid: an even number of row tiles per head).
 template <int VAR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     attn_jvp_bwd_kernel_pair(const __grid_constant__ Params p) {
-    bwd_body<VAR, 0, true>(p);
+    bwd_body<VAR, 0, true>(p, blockIdx.x);
+}
+
+// The three scored variants in one launch: the CTAs of dK/dtK, then of
+// dQ/dtQ, then of dV/dtV (key side split: MASK_SPLIT in its mask).  They are
+// independent, and with one CTA per SM each variant's last wave would leave
+// SMs idle that the next variant's CTAs fill here.
+struct ParamsAll {
+    Params k, q, v;
+    unsigned n_k, n_q;  // CTAs of the first two
+};
+constexpr uint32_t SMEM_ALL = Var<V_K>::SMEM_BYTES > Var<V_Q>::SMEM_BYTES
+                                  ? (Var<V_K>::SMEM_BYTES > Var<V_V>::SMEM_BYTES ? Var<V_K>::SMEM_BYTES : Var<V_V>::SMEM_BYTES)
+                                  : (Var<V_Q>::SMEM_BYTES > Var<V_V>::SMEM_BYTES ? Var<V_Q>::SMEM_BYTES : Var<V_V>::SMEM_BYTES);
+template <int MASK, bool kSplitK>
+__global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_bwd_scored_kernel(const __grid_constant__ ParamsAll p) {
+    constexpr int KEY = kSplitK ? MASK | MASK_SPLIT : MASK;
+    if (blockIdx.x < p.n_k)
+        bwd_body<V_K, KEY, false>(p.k, blockIdx.x);
+    else if (blockIdx.x < p.n_k + p.n_q)
+        bwd_body<V_Q, MASK, false>(p.q, blockIdx.x - p.n_k);
+    else
+        bwd_body<V_V, KEY, false>(p.v, blockIdx.x - p.n_k - p.n_q);
 }
 
 }  // namespace bwd

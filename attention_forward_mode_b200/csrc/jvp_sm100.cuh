@@ -277,10 +277,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         Lq_s = a1 - a0;
         yk0 = k0;
         Lk_s = k1 - k0;
-    } else if (kCausal || (kScored && p.score.end != nullptr)) {
-        // heavy (late) query tiles first (scored: so they are under prefix and frame-causal masks)
+    } else if (kScored) {
+        // groups of heads whose keys fit the L2 together; in a group the late query tiles of
+        // all heads first, the heavy ones under prefix and frame-causal masks
+        const int g = (int)blockIdx.x / (p.n_qtiles * p.score.slabs);
+        const int in = (int)blockIdx.x - g * p.n_qtiles * p.score.slabs;
+        const int n = min(p.score.slabs, p.BH - g * p.score.slabs);
+        bh = g * p.score.slabs + in % n;
+        qt = p.n_qtiles - 1 - in / n;
+    } else if (kCausal) {
         bh = blockIdx.x % p.BH;
-        qt = p.n_qtiles - 1 - blockIdx.x / p.BH;
+        qt = p.n_qtiles - 1 - blockIdx.x / p.BH;  // heavy (late) query tiles first
     } else {
         qt = blockIdx.x % p.n_qtiles;
         bh = blockIdx.x / p.n_qtiles;

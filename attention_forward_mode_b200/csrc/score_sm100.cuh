@@ -37,6 +37,7 @@ struct Score {
     float cap_out;           // c log2(e): the capped score in log2 units is cap_out tanh
     float cap_second;        // 2 / c
     int H, Hkv, group;       // query heads, key heads, query heads per key head
+    int slabs;               // (batch, head) slabs whose row tiles are scheduled together
 };
 
 // the visible keys of one query row, inside [0, Lk]; rows past the end see none

@@ -36,19 +36,16 @@ cudaError_t set_fwd() {
     return cudaFuncSetAttribute(sm100::attn_jvp_fwd_kernel<false, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sm100::SMEM_BYTES);
 }
-template <int VAR, int MASK>
+template <int MASK, bool kSplitK>
 cudaError_t set_bwd() {
-    return cudaFuncSetAttribute(bwd::attn_jvp_bwd_kernel<VAR, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)bwd::Var<VAR>::SMEM_BYTES);
+    return cudaFuncSetAttribute(bwd::attn_jvp_bwd_scored_kernel<MASK, kSplitK>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bwd::SMEM_ALL);
 }
 template <int MASK>
 cudaError_t set_mask() {
     cudaError_t e = set_fwd<MASK>();
-    if (e == cudaSuccess) e = set_bwd<bwd::V_Q, MASK>();
-    if (e == cudaSuccess) e = set_bwd<bwd::V_K, MASK>();
-    if (e == cudaSuccess) e = set_bwd<bwd::V_V, MASK>();
-    if (e == cudaSuccess) e = set_bwd<bwd::V_K, MASK | bwd::MASK_SPLIT>();
-    if (e == cudaSuccess) e = set_bwd<bwd::V_V, MASK | bwd::MASK_SPLIT>();
+    if (e == cudaSuccess) e = set_bwd<MASK, false>();
+    if (e == cudaSuccess) e = set_bwd<MASK, true>();
     return e;
 }
 
@@ -124,6 +121,13 @@ int with_mask(int mask, F f) {
     }
 }
 
+// (batch, head) slabs scheduled together: their streamed tensors, four of
+// `rows` rows each, take about 100 of the 126 MB of L2 (smaller groups end in a longer
+// tail: 12 heads of 8190 under a causal mask, four at a time, 500 instead of 458 us)
+int slabs_together(int64_t rows, int64_t BH) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(BH, (100 << 20) / (rows * bwd::HD * 8 + 1)));
+}
+
 int fwd_scored(const void *q, const void *k, const void *v, const void *tq, const void *tk, const void *tv, void *o,
                void *to, float *lse, float *mu, const float *slopes, const int32_t *key_begin, const int32_t *key_end,
                const Sizes &z, float scale, float softcap, void *stream) {
@@ -165,6 +169,7 @@ int fwd_scored(const void *q, const void *k, const void *v, const void *tq, cons
     p.scale_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;
     p.bound_ns = host::wait_bound_ns();
     p.score = make_score(z, scale, softcap, slopes, key_begin, key_end);
+    p.score.slabs = (int)(z.H / z.Hkv * slabs_together(z.Lk, BHk));  // heads of a group share their keys
     return with_mask(mask_bits(softcap, slopes), [&](auto mask) {
         constexpr int M = decltype(mask)::value;
         const dim3 grid((unsigned)(p.n_qtiles * BH));
@@ -183,59 +188,67 @@ uint64_t range_bytes(int64_t B, int64_t Lk) {
     return ((uint64_t)B * (uint64_t)((Lk + 127) / 128) * sizeof(int2) + 255u) / 256u * 256u;
 }
 
-// parts of a key-side CTA's streamed queries (the tiles of every head of its group)
+// Parts of a key-side CTA's streamed queries (the 64-row tiles of every head of
+// its group).  All three variants share one launch of one CTA per SM, heaviest
+// CTAs first, so the run takes about the whole work over the SMs and half of
+// the longest CTA: tiles streamed, each with a fixed cost of about eight tiles
+// per CTA, plus the partial sums' traffic (2 KB per key and part, a tile's time
+// moving some 14 MB).  Splits when that is shorter; ties go to fewer parts.
 int64_t split_parts(const Sizes &z, int sm_count) {
-    const int64_t tiles = (z.Lq + bwd::BN - 1) / bwd::BN * (z.H / z.Hkv);
-    return host::key_split(z.B * z.Hkv, tiles * bwd::BN, z.Lk, sm_count);
+    const double fixed = 8.0, mb14 = 14e6;
+    const double q_tiles = (double)((z.Lk + bwd::BN - 1) / bwd::BN);
+    const double q_ctas = (double)((z.Lq + bwd::BM - 1) / bwd::BM * z.B * z.H);
+    const int64_t k_tiles = (z.Lq + bwd::BN - 1) / bwd::BN * (z.H / z.Hkv);
+    const double k_ctas = (double)((z.Lk + bwd::BM - 1) / bwd::BM * z.B * z.Hkv);
+    int64_t best = 1;
+    double best_t = 0.0;
+    for (int64_t s = 1; s <= 16 && s <= k_tiles; ++s) {
+        const double chunk = (double)((k_tiles + s - 1) / s);
+        const double work = q_ctas * (q_tiles + fixed) + 2.0 * k_ctas * (double)s * (chunk + fixed);
+        const double longest = std::max(q_tiles, chunk) + fixed;
+        const double sums = s > 1 ? (double)s * (double)(z.B * z.Hkv * z.Lk) * 4096.0 / mb14 : 0.0;
+        const double t = work / (double)sm_count + 0.5 * longest + sums;
+        if (s == 1 || t < best_t * 0.999) {
+            best = s;
+            best_t = t;
+        }
+    }
+    return best;
 }
 
-// One backward variant over `rows` row-side slabs: r resident, l the long and
-// s the short streamed pair, out scaled by sc; n_split > 1 writes partial sums
-// to `partial` and reduces them.
-template <int VAR, int MASK>
-int launch_one(std::initializer_list<const void *> r, std::initializer_list<const void *> l,
+// Parameters of one backward variant: r resident, l the long and s the short
+// streamed pair, out scaled by sc; n_split > 1: partial sums to `partial`
+int bwd_params(bwd::Params *p, std::initializer_list<const void *> r, std::initializer_list<const void *> l,
                std::initializer_list<const void *> s, void *out0, void *out1, float sc, const Score &score,
                const void *stats, int64_t BHrow, int64_t BHcol, int64_t Lrow, int64_t Lcol, int64_t Lq, float scale,
-               int64_t n_split, float *partial, cudaStream_t stream) {
+               int64_t n_split, float *partial) {
     using namespace ajvp::bwd;
-    Params p;
-    std::memset(&p, 0, sizeof(p));
+    std::memset(p, 0, sizeof(*p));
     int rc, i = 0;
     for (const void *x : r)
-        if ((rc = host::encode(&p.tm_r[i++], x, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
+        if ((rc = host::encode(&p->tm_r[i++], x, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
     i = 0;
     for (const void *x : l)
-        if ((rc = host::encode(&p.tm_l[i++], x, HD, Lcol, BHcol, 64)) != AJVP_OK) return rc;
+        if ((rc = host::encode(&p->tm_l[i++], x, HD, Lcol, BHcol, 64)) != AJVP_OK) return rc;
     i = 0;
     for (const void *x : s)
-        if ((rc = host::encode(&p.tm_s[i++], x, HD, Lcol, BHcol, 64)) != AJVP_OK) return rc;
-    if ((rc = host::encode(&p.tm_out[0], out0, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
-    if ((rc = host::encode(&p.tm_out[1], out1, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
-    p.out_scale[0] = p.out_scale[1] = sc;
-    p.BH = (int)BHrow;
-    p.n_split = (int)n_split;
-    p.partial = partial;
-    p.stats = static_cast<const float4 *>(stats);
-    p.Lrow = (int)Lrow;
-    p.Lcol = (int)Lcol;
-    p.Lq = (int)Lq;
-    p.n_rtiles = (int)((Lrow + BM - 1) / BM);
-    p.scale = scale;
-    p.scale_log2 = scale * kLog2e;
-    p.bound_ns = host::wait_bound_ns();
-    p.score = score;
-    const int64_t n_cta = (int64_t)p.n_rtiles * BHrow * n_split;
-    if (n_cta >= (int64_t(1) << 31)) return AJVP_ERR_TOO_LARGE;
-    attn_jvp_bwd_kernel<VAR, MASK><<<(unsigned)n_cta, NTHREADS, Var<VAR>::SMEM_BYTES, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return host::fail(e);
-    if constexpr ((MASK & MASK_SPLIT) != 0) {
-        const long long rows = (long long)(BHrow * Lrow), n4 = rows * 2 * (HD / 4);
-        bwd_split_reduce_kernel<<<(unsigned)std::min<long long>((n4 + 255) / 256, 148LL * 16), 256, 0, stream>>>(
-            reinterpret_cast<const float4 *>(partial), (int)n_split, rows, static_cast<__nv_bfloat16 *>(out0),
-            static_cast<__nv_bfloat16 *>(out1), sc, sc);
-        if ((e = cudaGetLastError()) != cudaSuccess) return host::fail(e);
-    }
+        if ((rc = host::encode(&p->tm_s[i++], x, HD, Lcol, BHcol, 64)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p->tm_out[0], out0, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
+    if ((rc = host::encode(&p->tm_out[1], out1, HD, Lrow, BHrow, 128)) != AJVP_OK) return rc;
+    p->out_scale[0] = p->out_scale[1] = sc;
+    p->BH = (int)BHrow;
+    p->n_split = (int)n_split;
+    p->partial = partial;
+    p->stats = static_cast<const float4 *>(stats);
+    p->Lrow = (int)Lrow;
+    p->Lcol = (int)Lcol;
+    p->Lq = (int)Lq;
+    p->n_rtiles = (int)((Lrow + BM - 1) / BM);
+    p->scale = scale;
+    p->scale_log2 = scale * kLog2e;
+    p->bound_ns = host::wait_bound_ns();
+    p->score = score;
+    p->score.slabs = slabs_together(Lcol * (BHcol > BHrow ? BHcol / BHrow : 1), BHrow);
     return AJVP_OK;
 }
 
@@ -343,24 +356,38 @@ int attn_jvp_bwd_scored(const void *q, const void *k, const void *v, const void 
         if ((e = cudaGetLastError()) != cudaSuccess) return host::fail(e);
         score.qrange = out;
     }
-    return with_mask(mask_bits(softcap, slopes), [&](auto mask) -> int {
-        constexpr int M = decltype(mask)::value, MS = M | bwd::MASK_SPLIT;
-        int r = launch_one<bwd::V_Q, M>({q, tq, dtout, dout}, {k, tk}, {v, tv}, dq, dtq, scale, score, workspace, BH,
-                                        BHk, Lq, Lk, Lq, scale, 1, nullptr, st);
-        if (r != AJVP_OK) return r;
-        if (parts > 1) {
-            r = launch_one<bwd::V_K, MS>({k, tk, v, tv}, {q, tq}, {dtout, dout}, dk, dtk, scale, score, workspace, BHk,
-                                         BH, Lk, Lq, Lq, scale, parts, partial_k, st);
-            if (r != AJVP_OK) return r;
-            return launch_one<bwd::V_V, MS>({k, tk}, {dout, dtout}, {q, tq}, dv, dtv, 1.f, score, workspace, BHk, BH,
-                                            Lk, Lq, Lq, scale, parts, partial_v, st);
-        }
-        r = launch_one<bwd::V_K, M>({k, tk, v, tv}, {q, tq}, {dtout, dout}, dk, dtk, scale, score, workspace, BHk, BH,
-                                    Lk, Lq, Lq, scale, 1, nullptr, st);
-        if (r != AJVP_OK) return r;
-        return launch_one<bwd::V_V, M>({k, tk}, {dout, dtout}, {q, tq}, dv, dtv, 1.f, score, workspace, BHk, BH, Lk,
-                                       Lq, Lq, scale, 1, nullptr, st);
+    bwd::ParamsAll p;
+    if ((rc = bwd_params(&p.k, {k, tk, v, tv}, {q, tq}, {dtout, dout}, dk, dtk, scale, score, workspace, BHk, BH, Lk, Lq,
+                         Lq, scale, parts, partial_k)) != AJVP_OK)
+        return rc;
+    if ((rc = bwd_params(&p.q, {q, tq, dtout, dout}, {k, tk}, {v, tv}, dq, dtq, scale, score, workspace, BH, BHk, Lq, Lk,
+                         Lq, scale, 1, nullptr)) != AJVP_OK)
+        return rc;
+    if ((rc = bwd_params(&p.v, {k, tk}, {dout, dtout}, {q, tq}, dv, dtv, 1.f, score, workspace, BHk, BH, Lk, Lq, Lq,
+                         scale, parts, partial_v)) != AJVP_OK)
+        return rc;
+    const int64_t n_key = (int64_t)p.k.n_rtiles * BHk * parts, n_query = (int64_t)p.q.n_rtiles * BH;
+    if (2 * n_key + n_query >= (int64_t(1) << 31)) return AJVP_ERR_TOO_LARGE;
+    p.n_k = (unsigned)n_key;
+    p.n_q = (unsigned)n_query;
+    rc = with_mask(mask_bits(softcap, slopes), [&](auto mask) -> int {
+        constexpr int M = decltype(mask)::value;
+        const dim3 grid((unsigned)(2 * n_key + n_query));
+        if (parts > 1)
+            bwd::attn_jvp_bwd_scored_kernel<M, true><<<grid, bwd::NTHREADS, bwd::SMEM_ALL, st>>>(p);
+        else
+            bwd::attn_jvp_bwd_scored_kernel<M, false><<<grid, bwd::NTHREADS, bwd::SMEM_ALL, st>>>(p);
+        const cudaError_t e1 = cudaGetLastError();
+        return e1 == cudaSuccess ? AJVP_OK : host::fail(e1);
     });
+    if (rc != AJVP_OK || parts <= 1) return rc;
+    const long long krows = (long long)(BHk * Lk), n4 = krows * 2 * (bwd::HD / 4);
+    bwd::scored_reduce_kernel<<<dim3((unsigned)std::min<long long>((n4 + 255) / 256, 148LL * 8), 2), 256, 0, st>>>(
+        reinterpret_cast<const float4 *>(partial_k), reinterpret_cast<const float4 *>(partial_v), (int)parts, krows,
+        static_cast<__nv_bfloat16 *>(dk), static_cast<__nv_bfloat16 *>(dtk), static_cast<__nv_bfloat16 *>(dv),
+        static_cast<__nv_bfloat16 *>(dtv), scale);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? AJVP_OK : host::fail(e);
 }
 
 }  // extern "C"
