@@ -39,7 +39,7 @@ EXPORTED = (
     "attn_jvp_set_wait_bound_ns", "attn_jvp_set_persistent_key_tiles", "attn_jvp_set_bwd_pairs",
     "attn_jvp_selftest_wait_timeout",
     "attn_jvp_version", "attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored",
-    "attn_jvp_bwd_scored_workspace_bytes",
+    "attn_jvp_bwd_scored_workspace_bytes", "attn_jvp_cache_append", "attn_jvp_fwd_cache",
 )
 
 _lock = threading.Lock()
@@ -130,6 +130,10 @@ def load_library(path: str = LIB_PATH):
         lib.attn_jvp_bwd_scored.restype = ctypes.c_int
         lib.attn_jvp_bwd_scored_workspace_bytes.argtypes = [i64] * 5
         lib.attn_jvp_bwd_scored_workspace_bytes.restype = ctypes.c_uint64
+        lib.attn_jvp_cache_append.argtypes = [vp] * 15 + [i64] * 9 + [ctypes.c_int, vp]
+        lib.attn_jvp_cache_append.restype = ctypes.c_int
+        lib.attn_jvp_fwd_cache.argtypes = [vp] * 13 + [i64] * 12 + [f32, f32, ctypes.c_int, vp]
+        lib.attn_jvp_fwd_cache.restype = ctypes.c_int
         lib.attn_jvp_version.argtypes = []
         lib.attn_jvp_version.restype = ctypes.c_int
         _lib = lib

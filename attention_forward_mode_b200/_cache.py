@@ -1,0 +1,150 @@
+"""ctypes binding of the paged 8-bit key/value cache: ``attn_jvp_cache_append``
+(rotated keys and values into e4m3 pages) and ``attn_jvp_fwd_cache`` (O, tO and
+lse of a few query tokens per sequence over them).  Argument marshalling only,
+as in ``_binding``.
+
+The cache is four tensors that the caller owns: codes ``k_cache``, ``v_cache``
+(torch.float8_e4m3fn [pages, Hkv, page, 128], page a multiple of 16) and scales
+``k_scale``, ``v_scale`` (float32 [pages, Hkv], powers of two); a value is its
+code times its page's scale.  ``block_table`` (int32 [n_seq, width]) names the
+page of each run of ``page`` tokens of a sequence; nothing needs to be
+initialised before a page's first token is appended."""
+from __future__ import annotations
+
+import torch
+
+from ._binding import _check, _ptr, load_library
+from ._scored import _launch_stream, _tensor
+
+__all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache"]
+
+
+def _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [pages, Hkv, page, d] tensor")
+    pages, Hkv, page, d = k_cache.shape
+    dev = k_cache.device
+    _tensor("k_cache", k_cache, k_cache.shape, torch.float8_e4m3fn)
+    _tensor("v_cache", v_cache, k_cache.shape, torch.float8_e4m3fn, dev)
+    _tensor("k_scale", k_scale, (pages, Hkv), torch.float32, dev)
+    _tensor("v_scale", v_scale, (pages, Hkv), torch.float32, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 [n_seq, width] tensor")
+    n_seq, width = block_table.shape
+    _tensor("block_table", block_table, (n_seq, width), torch.int32, dev)
+    _tensor("cache_lens", cache_lens, (n_seq,), torch.int32, dev)
+    return n_seq, Hkv, pages, page, width, d, dev
+
+
+def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_seqlens, q=None,
+                          tq=None, cos=None, sin=None, interleaved=False, q_out=None, tq_out=None, stream=None):
+    """Append new tokens to the cache, in place.
+
+    k, v: bf16 [Hkv, total, 128], packed: sequence b's new tokens are rows
+    ``cu_seqlens[b]`` .. ``cu_seqlens[b + 1] - 1`` and stand at positions
+    ``cache_lens[b]``, ``cache_lens[b] + 1``, ...; ``cache_lens`` counts the tokens
+    cached before and is left as it is.  With ``cos``, ``sin`` (float32
+    [n_pos, 64], a row per position) the keys are rotated on the way: channels
+    (i, i + 64) by angle i, or (2i, 2i + 1) with ``interleaved``; and ``q``, ``tq``
+    (bf16 [H, total, 128], the same rows) are rotated into ``q_out``, ``tq_out``
+    (allocated when omitted).  A page's scale is the smallest power of two
+    that holds its largest value, over the tokens appended to it so far; a
+    page whose first token is among the new ones starts afresh.  Pages that
+    take new tokens must belong to one sequence.  Returns (q_out, tq_out)."""
+    n_seq, Hkv, pages, page, width, d, dev = _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [Hkv, total, d] tensor")
+    total = k.shape[1]
+    _tensor("k", k, (Hkv, total, d), torch.bfloat16, dev)
+    _tensor("v", v, (Hkv, total, d), torch.bfloat16, dev)
+    _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, dev)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    n_pos = 0
+    if cos is not None:
+        n_pos = cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() == 2 else 0
+        _tensor("cos", cos, (n_pos, d // 2), torch.float32, dev)
+        _tensor("sin", sin, (n_pos, d // 2), torch.float32, dev)
+        if n_pos < 1:
+            raise ValueError("cos and sin need a row per position")
+    H = Hkv
+    if q is not None:
+        if cos is None:
+            raise ValueError("q takes part only to be rotated: cos and sin are needed")
+        H = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        if H < 1 or H % Hkv:
+            raise ValueError(f"q must be [H, total, d] with H a multiple of the key heads ({Hkv})")
+        _tensor("q", q, (H, total, d), torch.bfloat16, dev)
+        q_out = torch.empty_like(q) if q_out is None else _tensor("q_out", q_out, q.shape, torch.bfloat16, dev)
+        if tq is not None:
+            _tensor("tq", tq, q.shape, torch.bfloat16, dev)
+            tq_out = torch.empty_like(q) if tq_out is None else _tensor("tq_out", tq_out, q.shape, torch.bfloat16, dev)
+    if (q is None and (tq is not None or q_out is not None)) or (tq is None and tq_out is not None):
+        raise ValueError("tq goes with q, and an output with its input")
+    with torch.cuda.device(dev):
+        rc = load_library().attn_jvp_cache_append(
+            _ptr(k), _ptr(v), _ptr(q), _ptr(tq), _ptr(q_out), _ptr(tq_out), _ptr(k_cache), _ptr(v_cache),
+            _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(cache_lens), _ptr(cu_seqlens), _ptr(cos), _ptr(sin),
+            n_seq, H, Hkv, total, pages, page, width, n_pos, d, int(bool(interleaved)), _launch_stream(stream, dev))
+    _check(rc, "attn_jvp_cache_append")
+    return q_out, tq_out
+
+
+def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_seqlens=None,
+                       max_seqlen=None, scale=None, softcap=0.0, slopes=None, causal=True, o=None, to=None, lse=None,
+                       stream=None, want_lse=True):
+    """O, tO, lse of the last query tokens of each sequence over its cached
+    keys and values, which carry no tangent: tO is the derivative of O along
+    ``tq`` (None: plain attention, and ``to`` is None).
+
+    q, tq: bf16 [n_seq, H, n, 128], any strides that are multiples of 8 with
+    the channels together; or packed [H, total, 128] with ``cu_seqlens`` (int32
+    [n_seq + 1]) and ``max_seqlen`` (at least the most tokens of one sequence;
+    ``total`` when omitted), the layout of ``attn_jvp_cache_append``.
+    ``cache_lens`` (int32 [n_seq]) counts the cached tokens, the query tokens' own
+    included: token t of n stands at position cache_lens - n + t and sees the
+    keys up to its own (``causal``; rows at negative positions see nothing), or
+    every cached key.  ``softcap`` and ``slopes`` modify the scores as in
+    ``attn_jvp_fwd_scored``.  Returns (o, to, lse), contiguous, shaped like q."""
+    n_seq, Hkv, pages, page, width, d, dev = _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens)
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.device != dev \
+            or q.dim() != (4 if cu_seqlens is None else 3) or q.shape[-1] != d or q.stride(-1) != 1:
+        raise ValueError("q must be a bf16 [n_seq, H, n, d] tensor (packed: [H, total, d]) on the cache's device with "
+                         "its channels together")
+    if cu_seqlens is None:
+        if max_seqlen is not None:
+            raise ValueError("max_seqlen belongs to cu_seqlens")
+        H, n, total, strides = q.shape[1], q.shape[2], 0, q.stride()[:3]
+        if q.shape[0] != n_seq:
+            raise ValueError(f"q is of {q.shape[0]} sequences, the cache of {n_seq}")
+    else:
+        H, total = q.shape[0], q.shape[1]
+        n, strides = total if max_seqlen is None else int(max_seqlen), (0, *q.stride()[:2])
+        _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, dev)
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"query heads ({H}) must be a multiple of the key heads ({Hkv})")
+    if tq is not None and (not isinstance(tq, torch.Tensor) or tq.shape != q.shape or tq.stride() != q.stride()
+                           or tq.dtype != q.dtype or tq.device != dev):
+        raise ValueError("tq must have q's shape, strides, type and device")
+    if slopes is not None:
+        _tensor("slopes", slopes, (H,), torch.float32, dev)
+    shape = tuple(q.shape)
+    o = torch.empty(shape, dtype=torch.bfloat16, device=dev) if o is None else _tensor("o", o, shape, torch.bfloat16, dev)
+    if tq is None:
+        if to is not None:
+            raise ValueError("to goes with tq")
+    else:
+        to = torch.empty(shape, dtype=torch.bfloat16, device=dev) if to is None else \
+            _tensor("to", to, shape, torch.bfloat16, dev)
+    if lse is not None:
+        _tensor("lse", lse, shape[:-1], torch.float32, dev)
+    elif want_lse:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        rc = load_library().attn_jvp_fwd_cache(
+            _ptr(q), _ptr(tq), _ptr(o), _ptr(to), _ptr(lse), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(block_table), _ptr(cache_lens), _ptr(cu_seqlens), _ptr(slopes), n_seq, H, Hkv, n,
+            total, *strides, pages, page, width, d, float(d ** -0.5 if scale is None else scale),
+            float(softcap or 0.0), int(bool(causal)), _launch_stream(stream, dev))
+    _check(rc, "attn_jvp_fwd_cache")
+    return o, to, lse

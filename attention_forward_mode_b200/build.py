@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libattnjvp.so")
-SOURCES = [os.path.join(HERE, "csrc", n) for n in ("api.cu", "scored.cu")]
+SOURCES = [os.path.join(HERE, "csrc", n) for n in ("api.cu", "scored.cu", "cache.cu")]
 DEPS = sorted(glob.glob(os.path.join(HERE, "csrc", "*")) + [os.path.join(ROOT, "include", "attn_jvp.h")])
 
 

@@ -1,0 +1,220 @@
+// cache.cu -- host side of the paged 8-bit cache: attn_jvp_cache_append and
+// attn_jvp_fwd_cache.  Argument checks and launches; no device memory is
+// allocated here.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "attn_jvp.h"
+#include "cache_sm100.cuh"
+#include "host_common.h"
+
+using namespace ajvp;
+
+namespace {
+
+struct Setup {
+    std::once_flag once;
+    cudaError_t error = cudaSuccess;
+};
+Setup g_setup[host::kMaxDevices];
+
+template <bool kTan>
+cudaError_t set_attn() {
+    cudaError_t e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         cache::ATTN_SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+}
+
+int setup(int *dev) {
+    int rc = host::device(dev);
+    if (rc != AJVP_OK) return rc;
+    Setup &s = g_setup[*dev];
+    std::call_once(s.once, [&]() {
+        s.error = set_attn<true>();
+        if (s.error == cudaSuccess) s.error = set_attn<false>();
+    });
+    return s.error == cudaSuccess ? AJVP_OK : host::fail(s.error);
+}
+
+constexpr int64_t kMaxInt = int64_t(1) << 31;
+
+// the cache's own sizes: page a multiple of 16, page indices and positions in 32 bits
+int check_cache(int64_t n_seq, int64_t H, int64_t Hkv, int64_t n_pages, int64_t page, int64_t table_width, int64_t d) {
+    if (n_seq < 0 || H < 0 || Hkv < 1 || H % Hkv != 0 || n_pages < 0 || page < 16 || page % 16 != 0 || table_width < 1 ||
+        d < 1)
+        return AJVP_ERR_INVALID_ARG;
+    if (d != cache::HD) return AJVP_ERR_UNSUPPORTED_DIM;
+    if (n_seq >= kMaxInt || H >= kMaxInt || n_pages >= kMaxInt || page > (1 << 16) || table_width >= (1 << 24) ||
+        table_width * page >= (1 << 24))
+        return AJVP_ERR_TOO_LARGE;
+    return AJVP_OK;
+}
+
+// CTAs per (sequence, key head, row tile), a power of two: doubled while the
+// launch has fewer than two waves of resident CTAs (three per SM) and every
+// part keeps at least two runs of 16 tokens per warp of the longest sequence.
+int split_count(int64_t units, int64_t tokens, int sm_count) {
+    int s = 1;
+    while (s < 16 && units * s < 6 * (int64_t)sm_count && tokens / 16 >= 2 * cache::WARPS * 2 * (int64_t)s) s *= 2;
+    return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_jvp_cache_append(const void *k, const void *v, const void *q, const void *tq, void *q_out, void *tq_out,
+                          void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int32_t *block_table,
+                          const int32_t *cache_lens, const int32_t *cu_seqlens, const float *cos, const float *sin,
+                          int64_t n_seq, int64_t H, int64_t Hkv, int64_t total, int64_t n_pages, int64_t page,
+                          int64_t table_width, int64_t n_pos, int64_t d, int interleaved, void *stream) {
+    int rc = check_cache(n_seq, H, Hkv, n_pages, page, table_width, d);
+    if (rc != AJVP_OK) return rc;
+    if (total < 0 || n_pos < 0 || (!cos) != (!sin) || (cos && n_pos < 1)) return AJVP_ERR_INVALID_ARG;
+    if ((q || tq) && !cos) return AJVP_ERR_INVALID_ARG;  // queries take part only to be rotated
+    if ((tq && !q) || (!q) != (!q_out) || (!tq) != (!tq_out)) return AJVP_ERR_INVALID_ARG;
+    if (total >= kMaxInt || n_pos >= kMaxInt) return AJVP_ERR_TOO_LARGE;
+    if (n_seq == 0 || total == 0) return AJVP_OK;
+    for (const void *p : {k, v, (const void *)k_cache, (const void *)v_cache, (const void *)k_scale,
+                          (const void *)v_scale, (const void *)block_table, (const void *)cache_lens,
+                          (const void *)cu_seqlens})
+        if (!p) return AJVP_ERR_INVALID_ARG;
+    for (const void *p : {k, v, q, tq, (const void *)q_out, (const void *)tq_out, (const void *)k_cache,
+                          (const void *)v_cache, (const void *)cos, (const void *)sin})
+        if (!host::aligned(p, 16)) return AJVP_ERR_MISALIGNED;
+    for (const void *p : {(const void *)k_scale, (const void *)v_scale, (const void *)block_table,
+                          (const void *)cache_lens, (const void *)cu_seqlens})
+        if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
+    const int64_t slots = total / page + 2 * std::min(n_seq, total);  // a sequence's first and last pages may be partial
+    const int64_t chunks = (total + cache::ROWS_PER_CTA - 1) / cache::ROWS_PER_CTA;
+    const int64_t grid = slots * Hkv + (q ? chunks * H : 0);
+    if (grid >= kMaxInt) return AJVP_ERR_TOO_LARGE;
+    int dev = 0;
+    if ((rc = setup(&dev)) != AJVP_OK) return rc;
+    cache::AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.tq = static_cast<const __nv_bfloat16 *>(tq);
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.tq_out = static_cast<__nv_bfloat16 *>(tq_out);
+    p.k8 = static_cast<uint8_t *>(k_cache);
+    p.v8 = static_cast<uint8_t *>(v_cache);
+    p.ks = k_scale;
+    p.vs = v_scale;
+    p.table = block_table;
+    p.lens = cache_lens;
+    p.cu = cu_seqlens;
+    p.cos = cos;
+    p.sin = sin;
+    p.n_seq = (int)n_seq;
+    p.H = (int)H;
+    p.Hkv = (int)Hkv;
+    p.total = (int)total;
+    p.n_pages = (int)n_pages;
+    p.page = (int)page;
+    p.table_width = (int)table_width;
+    p.n_pos = (int)n_pos;
+    p.interleaved = interleaved != 0;
+    p.n_slots = (int)slots;
+    cache::cache_append_kernel<<<(unsigned)grid, cache::APPEND_THREADS, 0, (cudaStream_t)stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? AJVP_OK : host::fail(e);
+}
+
+int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *lse, const void *k_cache,
+                       const void *v_cache, const float *k_scale, const float *v_scale, const int32_t *block_table,
+                       const int32_t *cache_lens, const int32_t *cu_seqlens, const float *slopes, int64_t n_seq,
+                       int64_t H, int64_t Hkv, int64_t n, int64_t total, int64_t stride_b, int64_t stride_h,
+                       int64_t stride_t, int64_t n_pages, int64_t page, int64_t table_width, int64_t d, float scale,
+                       float softcap, int causal, void *stream) {
+    int rc = check_cache(n_seq, H, Hkv, n_pages, page, table_width, d);
+    if (rc != AJVP_OK) return rc;
+    if (n < 0 || total < 0 || !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f)
+        return AJVP_ERR_INVALID_ARG;
+    const float log2e = 1.4426950408889634f;
+    if (softcap > 0.f && (!std::isfinite(2.f * log2e / softcap) || !std::isfinite(softcap * log2e)))
+        return AJVP_ERR_INVALID_ARG;
+    if (cu_seqlens && n > total) return AJVP_ERR_INVALID_ARG;
+    if (n >= kMaxInt || total >= kMaxInt) return AJVP_ERR_TOO_LARGE;
+    if (n_seq == 0 || H == 0 || n == 0 || (cu_seqlens && total == 0)) return AJVP_OK;
+    for (const void *p : {q, (const void *)o, k_cache, v_cache, (const void *)k_scale, (const void *)v_scale,
+                          (const void *)block_table, (const void *)cache_lens})
+        if (!p) return AJVP_ERR_INVALID_ARG;
+    if ((!tq) != (!to)) return AJVP_ERR_INVALID_ARG;
+    for (const void *p : {q, tq, (const void *)o, (const void *)to, (const void *)lse, k_cache, v_cache})
+        if (!host::aligned(p, 16)) return AJVP_ERR_MISALIGNED;
+    if (stride_b % 8 != 0 || stride_h % 8 != 0 || stride_t % 8 != 0) return AJVP_ERR_MISALIGNED;
+    for (const void *p : {(const void *)k_scale, (const void *)v_scale, (const void *)block_table,
+                          (const void *)cache_lens, (const void *)cu_seqlens, (const void *)slopes})
+        if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
+    const int64_t group = H / Hkv, rows = tq ? 8 : 16;
+    if (group * n >= kMaxInt || n_seq * Hkv >= kMaxInt) return AJVP_ERR_TOO_LARGE;
+    const int64_t tiles = (group * n + rows - 1) / rows;
+    if (n_seq * Hkv >= kMaxInt / 16 / tiles) return AJVP_ERR_TOO_LARGE;
+    const int64_t units = n_seq * Hkv * tiles;
+    int dev = 0;
+    if ((rc = setup(&dev)) != AJVP_OK) return rc;
+    cache::AttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.tq = static_cast<const __nv_bfloat16 *>(tq);
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.to = static_cast<__nv_bfloat16 *>(to);
+    p.lse = lse;
+    p.k8 = static_cast<const uint8_t *>(k_cache);
+    p.v8 = static_cast<const uint8_t *>(v_cache);
+    p.ks = k_scale;
+    p.vs = v_scale;
+    p.table = block_table;
+    p.lens = cache_lens;
+    p.slopes = slopes;
+    p.cu = cu_seqlens;
+    p.total = (int)total;
+    p.q_b = cu_seqlens ? 0 : stride_b;
+    p.q_h = stride_h;
+    p.q_t = stride_t;
+    p.o_b = cu_seqlens ? 0 : H * n;
+    p.o_h = cu_seqlens ? total : n;
+    p.cap_in = softcap > 0.f ? 2.f * log2e / softcap : 0.f;
+    p.cap_out = softcap * log2e;
+    p.scale = scale;
+    p.B = (int)n_seq;
+    p.H = (int)H;
+    p.Hkv = (int)Hkv;
+    p.group = (int)group;
+    p.n = (int)n;
+    p.n_pages = (int)n_pages;
+    p.page = (int)page;
+    p.table_width = (int)table_width;
+    p.causal = causal != 0;
+    p.tiles = (int)tiles;
+    p.splits = split_count(units, table_width * page, host::sm_count(dev));
+
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(units * p.splits));
+    cfg.blockDim = dim3(cache::THREADS);
+    cfg.dynamicSmemBytes = cache::ATTN_SMEM;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true>, p)
+                             : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false>, p);
+    return e == cudaSuccess ? AJVP_OK : host::fail(e);
+}
+
+}  // extern "C"

@@ -469,6 +469,89 @@ AJVP_API int attn_jvp_bwd_scored(const void *q, const void *k, const void *v,
 AJVP_API uint64_t attn_jvp_bwd_scored_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk);
 
 /*
+ * attn_jvp_cache_append -- appends new tokens to a paged 8-bit key/value
+ * cache, rotating keys (and queries) by their positions on the way.
+ *
+ *   k, v            : __nv_bfloat16 [Hkv][total][d] new tokens, packed: sequence
+ *                     b's are rows cu_seqlens[b] .. cu_seqlens[b+1]-1 and stand
+ *                     at positions cache_lens[b], cache_lens[b] + 1, ...
+ *   q, tq           : __nv_bfloat16 [H][total][d] queries and their tangents
+ *                     of the same tokens, or NULL (tq needs q); rotated into
+ *                     q_out, tq_out, same layout (NULL with their input)
+ *   k_cache, v_cache: e4m3 codes [n_pages][Hkv][page][d] (updated)
+ *   k_scale, v_scale: float [n_pages][Hkv] (updated); value = code x scale
+ *   block_table     : DEVICE int32 [n_seq][table_width]: the page of each run
+ *                     of `page` tokens of a sequence
+ *   cache_lens      : DEVICE int32 [n_seq] tokens cached before this call
+ *   cu_seqlens      : DEVICE int32 [n_seq + 1], non-decreasing, 0 .. total
+ *   cos, sin        : float [n_pos][d / 2], a row per position, or both NULL: no
+ *                     rotation.  Channels (i, i + d/2), with `interleaved` (2i, 2i+1),
+ *                     become (a cos - b sin, b cos + a sin) of angle i, in fp32
+ *                     without fused multiply-adds.  Positions past the last row
+ *                     take the last row.
+ *
+ * The scale of a page and head is the smallest power of two (exponent -100 ..
+ * 100) with which its largest value is at most 448, over the tokens that this
+ * and earlier calls appended to it; codes are round-to-nearest-even.  When a
+ * later token needs a larger scale, the page's earlier codes are moved to it
+ * (exact but for codes that become subnormal).  A page whose first token is
+ * among the new ones starts afresh, whatever it held.  Slots behind the new
+ * tokens stay as they are.  Tokens past table_width pages, and pages outside
+ * 0 .. n_pages - 1, are not written.  A page that takes new tokens must belong to one
+ * sequence.  The pages describe no cache; this is the definition above.
+ *
+ * Supported: d == 128, page a multiple of 16 up to 65536, table_width x page <
+ * 2^24; tensors, codes, cos and sin 16-byte, the rest 4-byte aligned.  One
+ * kernel, nothing atomic.  n_seq == 0 or total == 0 is a no-op.  Errors as
+ * attn_jvp_fwd.
+ */
+AJVP_API int attn_jvp_cache_append(const void *k, const void *v, const void *q, const void *tq,
+                 void *q_out, void *tq_out, void *k_cache, void *v_cache,
+                 float *k_scale, float *v_scale, const int32_t *block_table,
+                 const int32_t *cache_lens, const int32_t *cu_seqlens, const float *cos, const float *sin,
+                 int64_t n_seq, int64_t H, int64_t Hkv, int64_t total, int64_t n_pages, int64_t page,
+                 int64_t table_width, int64_t n_pos, int64_t d, int interleaved, void *stream);
+
+/*
+ * attn_jvp_fwd_cache -- O and its derivative along tQ, and lse, of a few query
+ * tokens per sequence over the cache (whose keys and values carry no tangent:
+ * clean context).  With the cached K, V of a sequence and the scores of
+ * attn_jvp_fwd_scored:
+ *
+ *   O = P V,   tO = (P .* (dS - rowsum(P .* dS))) V,   dS = (1 - tanh^2) s tQ K^T
+ *
+ *   q, tq           : __nv_bfloat16, d channels together; cu_seqlens NULL: token
+ *                     t < n of sequence b, head h at element
+ *                     b stride_b + h stride_h + t stride_t; else packed: token
+ *                     cu_seqlens[b] + t at h stride_h + (cu_seqlens[b] + t) stride_t.
+ *                     tq NULL: no tangent (to NULL)
+ *   o, to, lse      : __nv_bfloat16 [n_seq][H][n][d] and float [n_seq][H][n] (lse
+ *                     may be NULL); packed: [H][total][d], [H][total]
+ *   k_cache .. block_table : as attn_jvp_cache_append wrote them
+ *   cache_lens      : DEVICE int32 [n_seq] cached tokens, the query tokens' own
+ *                     included: token t of n is at position cache_lens[b] - n + t
+ *   cu_seqlens      : DEVICE int32 [n_seq + 1], or NULL
+ *   slopes          : DEVICE float [H], or NULL; the distance is |position - j|
+ *   n               : query tokens per sequence (packed: at least the most of
+ *                     one sequence, at most total; further ones are not computed)
+ *   causal          : key j visible iff j <= position; 0: every cached key
+ *
+ * Rows that see no key give zeros and lse = -infinity.  Pages outside
+ * 0 .. n_pages - 1 count as hidden; lengths are clamped to the table's capacity.
+ * Meant for decoding: query heads sharing a key head and their tokens are taken
+ * eight (with tangents) or sixteen rows at a time, and every such tile reads the
+ * sequence's codes again.  Supported: d == 128, sizes as attn_jvp_cache_append,
+ * strides multiples of 8 elements; one kernel, no workspace, deterministic.
+ * Errors as attn_jvp_fwd.
+ */
+AJVP_API int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *lse,
+                 const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                 const int32_t *block_table, const int32_t *cache_lens, const int32_t *cu_seqlens,
+                 const float *slopes, int64_t n_seq, int64_t H, int64_t Hkv, int64_t n, int64_t total,
+                 int64_t stride_b, int64_t stride_h, int64_t stride_t, int64_t n_pages, int64_t page,
+                 int64_t table_width, int64_t d, float scale, float softcap, int causal, void *stream);
+
+/*
  * attn_jvp_bwd_host -- attn_jvp_bwd on HOST buffers: every tensor argument
  * (the twelve inputs, lse and mu included, and the six gradients) is host
  * memory in the layouts of attn_jvp_bwd; pinned memory gives overlapped
