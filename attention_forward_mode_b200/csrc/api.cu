@@ -635,6 +635,20 @@ uint64_t wait_bound_ns() { return g_bound_ns.load(); }
 int encode(CUtensorMap *m, const void *ptr, int64_t d, int64_t L, int64_t BH, uint32_t box_rows) {
     return encode_3d(m, ptr, d, L, BH, box_rows);
 }
+int encode_codes(CUtensorMap *m, const void *ptr, int64_t rows, uint32_t box_rows) {
+    cuuint64_t dims[2] = {128u, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {128u};
+    cuuint32_t box[2] = {128u, box_rows};
+    cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        t_last_cuda_error = (int)r;
+        return AJVP_ERR_CUDA;
+    }
+    return AJVP_OK;
+}
 uint64_t stats_bytes(int64_t BH, int64_t Lq) { return bwd_stats_bytes(BH, Lq); }
 uint64_t partial_bytes(int64_t BH, int64_t Lk, int64_t parts) { return bwd_partial_bytes(BH, Lk, parts); }
 }  // namespace host
@@ -1058,7 +1072,8 @@ int attn_jvp_check_device_status(void *stream) {
         e = cudaMemcpyToSymbol(ajvp::g_status_word, &zero, sizeof(int));
         if (e != cudaSuccess) return fail_cuda(e);
     }
-    e = ajvp::host::scored_status(&word);  // the other translation unit's word
+    e = ajvp::host::scored_status(&word);  // the other translation units' words
+    if (e == cudaSuccess) e = ajvp::host::cache_status(&word);
     if (e != cudaSuccess) return fail_cuda(e);
     if (word != 0) return (word & 2) ? AJVP_ERR_DEVICE_LAYOUT : AJVP_ERR_TIMEOUT;
     return AJVP_OK;

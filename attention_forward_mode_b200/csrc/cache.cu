@@ -8,7 +8,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_jvp.h"
 #include "cache_sm100.cuh"
@@ -24,12 +26,12 @@ struct Setup {
 };
 Setup g_setup[host::kMaxDevices];
 
-template <bool kTan>
+template <bool kTan, int NT, int W>
 cudaError_t set_attn() {
-    cudaError_t e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         cache::ATTN_SMEM);
+    cudaError_t e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan, NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         cache::attn_smem(W));
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan, NT, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;
 }
 
@@ -38,8 +40,10 @@ int setup(int *dev) {
     if (rc != AJVP_OK) return rc;
     Setup &s = g_setup[*dev];
     std::call_once(s.once, [&]() {
-        s.error = set_attn<true>();
-        if (s.error == cudaSuccess) s.error = set_attn<false>();
+        for (cudaError_t e : {set_attn<true, 1, 4>(), set_attn<true, 2, 4>(), set_attn<false, 1, 4>(),
+                              set_attn<false, 2, 4>(), set_attn<true, 1, 8>(), set_attn<true, 2, 8>(),
+                              set_attn<false, 1, 8>(), set_attn<false, 2, 8>()})
+            if (s.error == cudaSuccess) s.error = e;
     });
     return s.error == cudaSuccess ? AJVP_OK : host::fail(s.error);
 }
@@ -53,7 +57,7 @@ int check_cache(int64_t n_seq, int64_t H, int64_t Hkv, int64_t n_pages, int64_t 
         return AJVP_ERR_INVALID_ARG;
     if (d != cache::HD) return AJVP_ERR_UNSUPPORTED_DIM;
     if (n_seq >= kMaxInt || H >= kMaxInt || n_pages >= kMaxInt || page > (1 << 16) || table_width >= (1 << 24) ||
-        table_width * page >= (1 << 24))
+        table_width * page >= (1 << 24) || Hkv >= kMaxInt / page || n_pages >= kMaxInt / (Hkv * page))
         return AJVP_ERR_TOO_LARGE;
     return AJVP_OK;
 }
@@ -63,11 +67,24 @@ int check_cache(int64_t n_seq, int64_t H, int64_t Hkv, int64_t n_pages, int64_t 
 // part keeps at least two runs of 16 tokens per warp of the longest sequence.
 int split_count(int64_t units, int64_t tokens, int sm_count) {
     int s = 1;
-    while (s < 16 && units * s < 6 * (int64_t)sm_count && tokens / 16 >= 2 * cache::WARPS * 2 * (int64_t)s) s *= 2;
+    while (s < 16 && units * s < 6 * (int64_t)sm_count && tokens / 16 >= 2 * 4 * 2 * (int64_t)s) s *= 2;
     return s;
 }
 
 }  // namespace
+
+namespace ajvp {
+namespace host {
+cudaError_t cache_status(int *word) {
+    int w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&w, g_status_word, sizeof(int));
+    if (e != cudaSuccess || w == 0) return e;
+    *word |= w;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int));
+}
+}  // namespace host
+}  // namespace ajvp
 
 extern "C" {
 
@@ -157,13 +174,17 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     for (const void *p : {(const void *)k_scale, (const void *)v_scale, (const void *)block_table,
                           (const void *)cache_lens, (const void *)cu_seqlens, (const void *)slopes})
         if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
-    const int64_t group = H / Hkv, rows = tq ? 8 : 16;
+    const int64_t group = H / Hkv;
     if (group * n >= kMaxInt || n_seq * Hkv >= kMaxInt) return AJVP_ERR_TOO_LARGE;
+    // one column tile where the rows fit it (half the accumulators, four CTAs per SM), else two
+    const int64_t one = tq ? 4 : 8, rows = group * n <= one ? one : 2 * one;
     const int64_t tiles = (group * n + rows - 1) / rows;
     if (n_seq * Hkv >= kMaxInt / 16 / tiles) return AJVP_ERR_TOO_LARGE;
     const int64_t units = n_seq * Hkv * tiles;
+    if (n_pages < 1) return AJVP_ERR_INVALID_ARG;
     int dev = 0;
     if ((rc = setup(&dev)) != AJVP_OK) return rc;
+    if ((rc = host::encoder()) != AJVP_OK) return rc;
     cache::AttnParams p;
     std::memset(&p, 0, sizeof(p));
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -197,14 +218,21 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     p.page = (int)page;
     p.table_width = (int)table_width;
     p.causal = causal != 0;
+    p.bound_ns = host::wait_bound_ns();
+    p.box = page % 32 == 0 ? 32 : 16;
+    if ((rc = host::encode_codes(&p.tm_k, k_cache, n_pages * Hkv * page, (uint32_t)p.box)) != AJVP_OK) return rc;
+    if ((rc = host::encode_codes(&p.tm_v, v_cache, n_pages * Hkv * page, (uint32_t)p.box)) != AJVP_OK) return rc;
+    p.page_magic = page == 16 ? 0u : (unsigned)(((uint64_t(1) << 32) + page / 16 - 1) / (page / 16));
     p.tiles = (int)tiles;
     p.splits = split_count(units, table_width * page, host::sm_count(dev));
+    if (getenv("AJVP_S")) p.splits = atoi(getenv("AJVP_S"));
 
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)(units * p.splits));
-    cfg.blockDim = dim3(cache::THREADS);
-    cfg.dynamicSmemBytes = cache::ATTN_SMEM;
+    const int warps = getenv("AJVP_W") ? atoi(getenv("AJVP_W")) : 4;
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = cache::attn_smem(warps);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -212,8 +240,15 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true>, p)
-                             : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false>, p);
+    auto launch = [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        if (rows == one)
+            return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 1, W>, p)
+                      : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, W>, p);
+        return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 2, W>, p)
+                  : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 2, W>, p);
+    };
+    const cudaError_t e = warps == 4 ? launch(std::integral_constant<int, 4>()) : launch(std::integral_constant<int, 8>());
     return e == cudaSuccess ? AJVP_OK : host::fail(e);
 }
 

@@ -237,30 +237,36 @@ static __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(con
 }
 
 // --------------------------------------------------------------- attention
-// O, tO of n query tokens per sequence over the cache.  The rows of one key
-// head (its group's heads x n tokens) are the M rows of m16n8k16 products:
-// with a tangent, rows 0-7 of a tile are queries and rows 8-15 their tangents,
-// so one thread holds S and dS of the same (row, key), and the second product
-// of [P ; P dS] with V gives O and T = sum p dS V at once.  The cache carries
-// no tangent, so tO = T / l - mu O.
+// O, tO of n query tokens per sequence over the cache.  The cache carries no
+// tangent, so with T = sum p dS V, tO = T / l - mu O.
 //
-// This is a decoding step: the work is to read the codes once.  So warps take
-// runs of 16 tokens each, copy them ahead through rings of their own in shared
-// memory (every lane reads back only what it copied), and turn codes into f16
-// operands in registers: 16-byte pieces of key rows are B fragments of Q K^T
-// (the order of channels inside a product is free, and the query fragments
-// follow it), and bytes of value rows of two tokens pair up as B fragments of
-// P V.  mma.sync rather than tcgen05: the products of 16 rows are a few percent
-// of the time, and 128-row accumulators in tensor memory would be empty but for
-// those rows.  Splits of a sequence are the CTAs of one cluster, which join
-// their sums through distributed shared memory: no workspace, one launch, and a
-// fixed order of additions.
+// This is a decoding step: the work is to read the codes once, for a few query
+// rows (the group's heads x n tokens).  Each warp takes runs of 32 tokens (two
+// halves of 16, each inside one page), which the tensor-memory accelerator
+// copies ahead into a ring of its own in shared memory, 128-byte swizzled.  The
+// products have the 16 tokens, or 16 value channels, as rows and the query rows
+// as their 8 columns,
+//     S^T = K Q^T      [16 tokens][8]
+//     O^T += V^T P^T   [128 channels][8]
+// so that few query rows leave little of a product empty.  With a tangent the
+// columns alternate q, tq: one thread holds S and dS of the same (row, key), and
+// the columns of the second product alternate P, P dS, giving O and T at once.
+// K Q^T takes the codes as they are (m16n8k32 in e4m3): a bf16 query channel is
+// the sum of two e4m3 values, its leading four bits and the rest, so two products
+// give the exact sum without turning a code into anything.  V^T P^T is m16n8k16
+// in f16 (e4m3 would leave P eight bits): bytes of two tokens' value rows pair up
+// as A fragments, converted two per instruction, and P^T is turned by movmatrix.
+// mma.sync rather than tcgen05: 128-row accumulators in tensor memory would be
+// nearly empty, and the products are not what bounds the kernel.  Splits of a
+// sequence are the CTAs of one cluster, which join their sums through distributed
+// shared memory: no workspace, one launch, and a fixed order of additions.
 //
-// f16 operands: queries and tangents are scaled by a power of two per row to at
-// most 2 (bf16 values are then exact but for those 2^-14 below the row's
-// largest); P is weighted by its page's value scale, and the running reference
-// M covers both, so |P| <= 2^8; dS is taken relative to the largest key scale
-// so far (E) and 2^-10, so that |dS| < 2^7 and |P dS| < 2^15.
+// Operand ranges: queries and tangents are scaled by a power of two per row so
+// that the largest lies in [128, 256) (channels 2^-10 below it start to lose
+// bits); P is weighted by its page's value scale, and the running reference M
+// covers both, so |P| <= 2^8; dS is taken relative to the row's first run (r, so
+// that a nearly constant dS does not cancel against mu O) and to the largest key
+// scale so far (E) and 2^-18, so that |P dS| < 2^15.
 struct AttnParams {
     const __nv_bfloat16 *q, *tq;  // row (b, h, t) at q_b b + q_h h + q_t t channels; packed: cu[b] + t in place of t
     __nv_bfloat16 *o, *to;        // rows o_b b + o_h h + t (packed: + cu[b])
@@ -272,53 +278,79 @@ struct AttnParams {
     const float *ks, *vs;
     const int *table, *lens;
     const float *slopes;          // [H] or NULL
-    float cap_in, cap_out;        // 2 / c (of scaled scores, in e-units) and c log2(e), 0: no cap
+    float cap_in, cap_out;        // 2 log2(e) / c (of scaled scores) and c log2(e); 0: no cap
     float scale;
     int B, H, Hkv, group, n_pages, page, table_width, causal;
     int n;                        // query tokens per sequence (packed: of the longest)
     int tiles;                    // row tiles per (sequence, key head)
     int splits;                   // CTAs per cluster
+    CUtensorMap tm_k, tm_v;       // codes [rows][128], boxes of `box` rows
+    int box;                      // 32 where pages are multiples of it, else 16
+    unsigned long long bound_ns;
+    unsigned page_magic;          // ceil(2^32 / (page / 16)): x / (page / 16) = umulhi(x, magic); 0 for pages of 16
 };
 
-constexpr int WARPS = 4, THREADS = WARPS * 32;
-constexpr int STAGES = 4;
-constexpr int STAGE_BYTES = 8 * 512;                 // 16 tokens of keys and values
+constexpr int STAGES = 2;
+constexpr int HALF_BYTES = 16 * HD;                  // 16 tokens of keys, or of values
+constexpr int STAGE_BYTES = 4 * HALF_BYTES;          // 32 tokens: keys, then values
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;     // per warp
-constexpr int SCALES_OFF = WARPS * RING_BYTES;       // float2 per warp and stage
-constexpr int STATS_OFF = SCALES_OFF + WARPS * STAGES * 8;
-constexpr int TAN_UNITS = 49;
-constexpr int STATS_FLOATS = TAN_UNITS + 8;          // m, l, g per row, E, the tangent rows' units
-constexpr int ATTN_SMEM = STATS_OFF + (WARPS + 1) * 64 * 4;
-static_assert(STATS_FLOATS <= 64 && 16 * HD * 4 <= RING_BYTES, "the sums of a warp fit its ring");
+// statistics of a warp, or of the CTA: floats at ST_M + row etc.
+constexpr int ST_M = 0, ST_L = 16, ST_G = 32, ST_R = 40, ST_E = 48, ST_UNIT = 49, ST_FLOATS = 64;
+// shared memory of a CTA of `warps` warps: rings, a barrier per warp and stage and
+// the CTA's abort flag, statistics of the warps and of the CTA
+__host__ __device__ constexpr int bars_off(int warps) { return warps * RING_BYTES; }
+__host__ __device__ constexpr int stats_off(int warps) { return bars_off(warps) + warps * STAGES * 8 + 16; }
+__host__ __device__ constexpr int attn_smem(int warps) { return stats_off(warps) + (warps + 1) * ST_FLOATS * 4; }
+static_assert(16 * HD * 4 <= RING_BYTES, "the sums of a warp fit its ring");
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 2-D tiled load global -> shared, completion counted on `bar` (bytes)
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// four e4m3 codes as two f16x2; exact
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+// an 8 x 8 matrix of 16-bit values, row lane / 4, columns 2 (lane % 4) + {0, 1}: its transpose
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float quad_max(float x) {
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// over the eight lanes of the same lane % 4
+__device__ __forceinline__ float column_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+__device__ __forceinline__ float column_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -338,16 +370,31 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ void axpy(float4 &y, float a, float4 x) {
+    y.x = fmaf(a, x.x, y.x);
+    y.y = fmaf(a, x.y, y.y);
+    y.z = fmaf(a, x.z, y.z);
+    y.w = fmaf(a, x.w, y.w);
+}
+// weight of sums at reference m against reference top
+__device__ __forceinline__ float ref_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
+__device__ __forceinline__ float pow2_or_0(int e) { return e >= -126 ? pow2(e) : 0.f; }
 
-// kTan: 8 query rows and their tangents per tile, else 16 query rows.
-template <bool kTan>
-__global__ void __launch_bounds__(THREADS, 3) cache_attn_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int ROWS = kTan ? 8 : 16;    // query rows of a tile
-    constexpr int R = kTan ? 1 : 2;        // query rows per thread
-    extern __shared__ __align__(16) uint8_t smem[];
+// NT column tiles of 8: with a tangent 4 NT query rows and their tangents, else 8 NT query rows.
+// WARPS: 4 (three CTAs per SM), or 8 for launches that leave each SM one CTA at most.
+template <bool kTan, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1) cache_attn_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int ROWS = (kTan ? 4 : 8) * NT;  // query rows of a tile
+    constexpr int R = kTan ? 1 : 2;            // query rows per thread and column tile
+    constexpr int THREADS = 32 * WARPS, STATS_OFF = stats_off(WARPS);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int gr = lane >> 2, c = lane & 3;  // fragment row and column group
+    if (sbase & 1023u) {  // the swizzled copies need it (the same for every CTA)
+        if (threadIdx.x == 0) atomicOr(&g_status_word, 2);
+        return;
+    }
+    const int gr = lane >> 2, c = lane & 3;  // fragment row and column pair
     const int rank = (int)blockIdx.x % p.splits;
     const int unit = (int)blockIdx.x / p.splits;
     const int tile = unit % p.tiles, bh = unit / p.tiles;
@@ -360,301 +407,466 @@ __global__ void __launch_bounds__(THREADS, 3) cache_attn_kernel(const __grid_con
     const int n_rows = p.group * n;
     if (tile * ROWS >= n_rows) return;  // (the same for every CTA of the cluster)
     const int len = min(max(p.lens[b], 0), p.table_width * p.page);
-    // this CTA's runs of 16 tokens
-    const int runs = (len + 15) >> 4;
+    // this CTA's runs of 32 tokens
+    const int runs = (len + 31) >> 5;
     const int per = (runs + p.splits - 1) / p.splits;
     const int run0 = min(rank * per, runs), run1 = min(run0 + per, runs);
 
-    // query fragments: row gr (and gr + 8: its tangent, or query row gr + 8); product s
-    // takes channels base(s) + {0, 1, 2, 3} of this lane, base = 16 c + 4 s, from s = 4 on
-    // 64 + 16 c + 4 (s - 4)
-    uint32_t aq[8][4];
-    float row_scale[2] = {0.f, 0.f};  // power of two per row, times the softmax scale
-    int end[R];                       // keys 0 .. end - 1 are visible
-    int pos[R];
-    float slope2[R];
+    const uint32_t ring = sbase + (uint32_t)warp * RING_BYTES;
+    const uint32_t bars = sbase + bars_off(WARPS) + (uint32_t)warp * STAGES * 8u;
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + bars_off(WARPS) + WARPS * STAGES * 8);
+    if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = tile * ROWS + gr + (kTan ? 0 : 8 * i);
-        const bool live = r < n_rows;
-        const int h = live ? hk * p.group + r / n : 0, t = live ? r % n : 0;
-        const __nv_bfloat16 *src = (kTan && i == 1 ? p.tq : p.q) + (p.q_b * b + p.q_h * h + p.q_t * (first + t));
-        uint2 raw[8];
-        float amax = 0.f;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            raw[s] = live ? *reinterpret_cast<const uint2 *>(src + (s >> 2) * 64 + 16 * c + 4 * (s & 3)) : make_uint2(0u, 0u);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t u = w ? raw[s].y : raw[s].x;
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
-            }
-        }
-        amax = quad_max(amax);
-        // 2^e with amax in [2^e, 2^(e + 1))
-        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -120), 120);
-        const float inv = pow2(-e);
-        row_scale[i] = pow2(e) * p.scale;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            aq[s][i] = pack_f16x2(__uint_as_float(raw[s].x << 16) * inv, __uint_as_float(raw[s].x & 0xffff0000u) * inv);
-            aq[s][2 + i] = pack_f16x2(__uint_as_float(raw[s].y << 16) * inv, __uint_as_float(raw[s].y & 0xffff0000u) * inv);
-        }
-        if (i < R) {
-            pos[i] = len - n + t;
-            end[i] = live && p.causal ? min(max(pos[i] + 1, 0), len) : len;
-            slope2[i] = p.slopes && live ? p.slopes[h] * 1.4426950408889634f : 0.f;
-        }
-    }
-    int least = end[0];  // keys that every row of the tile sees
-#pragma unroll
-    for (int i = 1; i < R; ++i) least = min(least, end[i]);
-    least = __reduce_min_sync(0xffffffffu, least);
-
-    float acc[16][4];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    float m[R], l[R], g = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-    }
-    int E = SCALE_MIN;
-
-    const uint32_t ring = sbase + (uint32_t)warp * RING_BYTES + (uint32_t)lane * 16u;
-    const uint32_t scales = sbase + SCALES_OFF + (uint32_t)warp * STAGES * 8u;
-    const int *const table = p.table + (size_t)b * p.table_width;
-    auto page_of = [&](int run) -> int { return run < run1 ? table[run * 16 / p.page] : -1; };
-    auto copy = [&](int run, int id, int stage) {
-        if (run < run1 && id >= 0 && id < p.n_pages) {
-            const size_t sc = (size_t)id * p.Hkv + hk;
-            const size_t row0 = sc * p.page + (size_t)(run * 16 % p.page);
-            const uint8_t *const kr = p.k8 + (row0 + gr) * HD + 16 * c;
-            const uint8_t *const vr = p.v8 + (row0 + 2 * c) * HD + 16 * gr;
-            const uint32_t d = ring + (uint32_t)stage * STAGE_BYTES;
-            cp_async16(d, kr);
-            cp_async16(d + 512, kr + 64);
-            cp_async16(d + 1024, kr + 8 * HD);
-            cp_async16(d + 1536, kr + 8 * HD + 64);
-            cp_async16(d + 2048, vr);
-            cp_async16(d + 2560, vr + HD);
-            cp_async16(d + 3072, vr + 8 * HD);
-            cp_async16(d + 3584, vr + 9 * HD);
-            if (lane == 0) {
-                cp_async4(scales + (uint32_t)stage * 8u, p.ks + sc);
-                cp_async4(scales + (uint32_t)stage * 8u + 4u, p.vs + sc);
-            }
-        }
-        cp_async_commit();
-    };
-    // ids of the pages of the runs in flight (the run being worked on first), and of the next one
-    int ids[STAGES];
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) ids[s] = page_of(run0 + warp + s * WARPS);
-    ids[STAGES - 1] = page_of(run0 + warp + (STAGES - 1) * WARPS);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) copy(run0 + warp + s * WARPS, ids[s], s);
-    int stage = 0;
-    for (int run = run0 + warp; run < run1; run += WARPS) {
-        const int id = ids[0];
-        copy(run + (STAGES - 1) * WARPS, ids[STAGES - 1], (stage + STAGES - 1) % STAGES);
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) ids[s] = ids[s + 1];
-        ids[STAGES - 1] = page_of(run + STAGES * WARPS);
-        cp_async_wait<STAGES - 1>();
-        __syncwarp();  // the scales are lane 0's copies
-        const uint32_t d = ring + (uint32_t)stage * STAGE_BYTES;
-        const uint32_t sc = scales + (uint32_t)stage * 8u;
-        stage = (stage + 1) % STAGES;
-        if (id < 0 || id >= p.n_pages) continue;  // no such page: its tokens are hidden
-        float kscale, vscale;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(kscale), "=f"(vscale) : "r"(sc) : "memory");
-
-        float S[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[nt][i] = 0.f;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint4 u = ld_shared_u4(d + (uint32_t)(nt * 2 + half) * 512u);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    mma_f16(S[nt], aq[half * 4 + s], e4m3x2_to_f16x2(w[s] & 0xffffu), e4m3x2_to_f16x2(w[s] >> 16));
-            }
-        }
-        // scores in log2 units of keys run * 16 + 8 nt + 2 c + {0, 1}; row i of this thread
-        // sits in S[nt][2 i], S[nt][2 i + 1] (kTan: dS in S[nt][2], S[nt][3])
-        const bool all = (run + 1) * 16 <= least;
-        const float kq = kscale * row_scale[0];
-        float y[R][4], dS[4];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float sc_i = (kTan ? kq : kscale * row_scale[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = run * 16 + 8 * (e >> 1) + 2 * c + (e & 1);
-                const float z = S[e >> 1][2 * i + (e & 1)] * sc_i;
-                if constexpr (kTan) dS[e] = S[e >> 1][2 + (e & 1)];
-                float v = z * 1.4426950408889634f;
-                if (p.cap_out > 0.f) {
-                    float2 t, df;
-                    cap2(make_float2(z, z), p.cap_in, t, df);
-                    v = t.x * p.cap_out;
-                    if constexpr (kTan) dS[e] *= df.x;
-                }
-                v = fmaf(-slope2[i], fabsf((float)(pos[i] - key)), v);
-                const bool seen = all || key < end[i];
-                y[i][e] = seen ? v : -INFINITY;
-                if (kTan && !seen) dS[e] = 0.f;  // (codes past the end may be NaN)
-            }
-        }
-        // running references of y + log2(value scale), lazily raised
-        const int ev = exponent_of(vscale), ek = exponent_of(kscale);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float top = quad_max(fmaxf(fmaxf(y[i][0], y[i][1]), fmaxf(y[i][2], y[i][3]))) + (float)ev;
-            const bool need = top > m[i] + 8.f;
-            if (__any_sync(0xffffffffu, need)) {
-                const float alpha = need ? ex2_approx(m[i] - top) : 1.f;
-                if (need) m[i] = top;
-                l[i] *= alpha;
-                if (kTan) g *= alpha;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    acc[j][2 * i] *= alpha;
-                    acc[j][2 * i + 1] *= alpha;
-                    if (kTan) {
-                        acc[j][2] *= alpha;
-                        acc[j][3] *= alpha;
-                    }
-                }
-            }
-        }
-        if (kTan && ek > E) {  // a larger key scale: T moves to it
-            const float r = ek - E <= 126 ? pow2(E - ek) : 0.f;
-            E = ek;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                acc[j][2] *= r;
-                acc[j][3] *= r;
-            }
-        }
-        uint32_t ap[4];
-        const float rel = kTan ? pow2(max(ek - E, -116) - 10) : 0.f;
-        float w4[2][4];  // P x value scale: [row][key], or P and P dS
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float ref = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float pe = ex2_approx(y[i][e] - ref);
-                l[i] += pe;
-                w4[i][e] = pe * vscale;
-                if constexpr (kTan) {
-                    g = fmaf(pe, dS[e] * (kscale * row_scale[1]), g);
-                    w4[1][e] = w4[0][e] * (dS[e] * rel);
-                }
-            }
-        }
-        ap[0] = pack_f16x2(w4[0][0], w4[0][1]);
-        ap[1] = pack_f16x2(w4[1][0], w4[1][1]);
-        ap[2] = pack_f16x2(w4[0][2], w4[0][3]);
-        ap[3] = pack_f16x2(w4[1][2], w4[1][3]);
-        // values of tokens 2c, 2c + 1, 2c + 8, 2c + 9, channels 16 gr + j; tokens past the
-        // end may hold anything (also NaN codes) and are zeroed
-        uint4 v0 = ld_shared_u4(d + 2048u), v1 = ld_shared_u4(d + 2560u);
-        uint4 v2 = ld_shared_u4(d + 3072u), v3 = ld_shared_u4(d + 3584u);
-        if ((run + 1) * 16 > len) {
-            const int left = len - run * 16 - 2 * c;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            if (left <= 0) v0 = zero;
-            if (left <= 1) v1 = zero;
-            if (left <= 8) v2 = zero;
-            if (left <= 9) v3 = zero;
-        }
-        const uint32_t a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
-        const uint32_t a2[4] = {v2.x, v2.y, v2.z, v2.w}, a3[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t lo01 = __byte_perm(a0[w], a1[w], 0x5140), hi01 = __byte_perm(a0[w], a1[w], 0x7362);
-            const uint32_t lo89 = __byte_perm(a2[w], a3[w], 0x5140), hi89 = __byte_perm(a2[w], a3[w], 0x7362);
-            mma_f16(acc[4 * w], ap, e4m3x2_to_f16x2(lo01 & 0xffffu), e4m3x2_to_f16x2(lo89 & 0xffffu));
-            mma_f16(acc[4 * w + 1], ap, e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo89 >> 16));
-            mma_f16(acc[4 * w + 2], ap, e4m3x2_to_f16x2(hi01 & 0xffffu), e4m3x2_to_f16x2(hi89 & 0xffffu));
-            mma_f16(acc[4 * w + 3], ap, e4m3x2_to_f16x2(hi01 >> 16), e4m3x2_to_f16x2(hi89 >> 16));
-        }
-    }
-    cp_async_wait<0>();
-    __syncwarp();
-
-    // each warp's sums into its ring: [16 rows][128] (rows 8-15: T, or query rows 8-15), its
-    // statistics beside them.  acc[j][0, 1] are row gr, channels 16 (2 c) + j and 16 (2 c + 1) + j.
-    float *const mine = reinterpret_cast<float *>(smem + warp * RING_BYTES);
-    float *const stats = reinterpret_cast<float *>(smem + STATS_OFF) + warp * 64;
-#pragma unroll
-    for (int i = 0; i < R; ++i) l[i] = quad_sum(l[i]);
-    g = quad_sum(g);
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<float4 *>(mine + (gr + 8 * half) * HD + 32 * c + 16 * k + j) =
-                    make_float4(acc[j][2 * half + k], acc[j + 1][2 * half + k], acc[j + 2][2 * half + k],
-                                acc[j + 3][2 * half + k]);
-    if (c == 0) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            stats[gr + 8 * i] = m[i];
-            stats[16 + gr + 8 * i] = l[i];
-        }
-        if (kTan) stats[32 + gr] = g;
-        if (kTan && warp == 0)  // the tangent rows' units, for this CTA's outputs
-            (reinterpret_cast<float *>(smem + STATS_OFF) + WARPS * 64)[TAN_UNITS + gr] = row_scale[1];
-        if (lane == 0) reinterpret_cast<int *>(stats)[48] = E;
+        for (int s = 0; s < STAGES; ++s) mbar_init(bars + 8u * s, 1);
+        if (warp == 0) *abort_flag = 0;
+        fence_barrier_init();
     }
     __syncthreads();
-    // the CTA's sums, in warp order, into warp 0's ring; statistics into slot WARPS
+    const int *const table = p.table + (size_t)b * p.table_width;
+    const int halves = (len + 15) >> 4, per_page = p.page >> 4;
+    auto page_index = [&](int half) -> int { return p.page_magic ? (int)__umulhi((unsigned)half, p.page_magic) : half; };
+    // page of a half (-1: past the end, or no such page)
+    auto page_of = [&](int run, int h) -> int {
+        if (run >= run1 || 2 * run + h >= halves) return -1;
+        const int id = table[page_index(2 * run + h)];
+        return (unsigned)id < (unsigned)p.n_pages ? id : -1;
+    };
+    // {key, value} scales of the runs in flight, read with their copies
+    float2 held[STAGES][2];
+    auto copy = [&](int run, const int (&id)[2], int stage, float2 (&sc)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const size_t at = (size_t)max(id[h], 0) * p.Hkv + hk;
+            sc[h] = id[h] >= 0 ? make_float2(__ldg(p.ks + at), __ldg(p.vs + at)) : make_float2(pow2(SCALE_MIN), pow2(SCALE_MIN));
+        }
+        if (lane != 0 || run >= run1) return;
+        const uint32_t bar = bars + 8u * stage, d = ring + (uint32_t)stage * STAGE_BYTES;
+        const int y0 = (max(id[0], 0) * p.Hkv + hk) * p.page + (2 * run - page_index(2 * run) * per_page) * 16;
+        if (p.box == 32) {  // (both halves are in one page; the second may lie past the end)
+            mbar_arrive_expect_tx(bar, id[0] >= 0 ? 4 * HALF_BYTES : 0);
+            if (id[0] >= 0) {
+                tma_load_2d(d, &p.tm_k, bar, 0, y0);
+                tma_load_2d(d + 2 * HALF_BYTES, &p.tm_v, bar, 0, y0);
+            }
+        } else {
+            mbar_arrive_expect_tx(bar, (id[0] >= 0 ? 2 * HALF_BYTES : 0) + (id[1] >= 0 ? 2 * HALF_BYTES : 0));
+            if (id[0] >= 0) {
+                tma_load_2d(d, &p.tm_k, bar, 0, y0);
+                tma_load_2d(d + 2 * HALF_BYTES, &p.tm_v, bar, 0, y0);
+            }
+            if (id[1] >= 0) {
+                const int y1 = (id[1] * p.Hkv + hk) * p.page + (2 * run + 1 - page_index(2 * run + 1) * per_page) * 16;
+                tma_load_2d(d + HALF_BYTES, &p.tm_k, bar, 0, y1);
+                tma_load_2d(d + 3 * HALF_BYTES, &p.tm_v, bar, 0, y1);
+            }
+        }
+    };
+    // pages of the halves of the run being worked on, of those in flight, and of the one after
+    int ids[STAGES + 1][2];
+#pragma unroll
+    for (int s = 0; s <= STAGES; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ids[s][h] = page_of(run0 + warp + s * WARPS, h);
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) copy(run0 + warp + s * WARPS, ids[s], s, held[s]);
+
+    // query fragments: column gr of each column tile, channels 32 c .. 32 c + 31 of it in this
+    // lane; word w (channels 32 c + 4 w ..) belongs to product w / 2.  hi + lo is the channel.
+    uint32_t hi[NT][8], lo[NT][8];
+    float unit_of[NT];  // power of two of the column's scaling, times the softmax scale
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = tile * ROWS + (kTan ? nt * 4 + (gr >> 1) : nt * 8 + gr);
+        const bool live = r < n_rows;
+        const int h = live ? hk * p.group + r / n : 0, t = live ? r % n : 0;
+        const __nv_bfloat16 *src = (kTan && (gr & 1) ? p.tq : p.q) + (p.q_b * b + p.q_h * h + p.q_t * (first + t));
+        uint4 raw[4];
+        float amax = 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            raw[s] = live ? *reinterpret_cast<const uint4 *>(src + 32 * c + 8 * s) : make_uint4(0u, 0u, 0u, 0u);
+        float x[32];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t u[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                x[8 * s + 2 * w] = __uint_as_float(u[w] << 16);
+                x[8 * s + 2 * w + 1] = __uint_as_float(u[w] & 0xffff0000u);
+                amax = fmaxf(amax, fmaxf(fabsf(x[8 * s + 2 * w]), fabsf(x[8 * s + 2 * w + 1])));
+            }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^e with amax in [2^e, 2^(e + 1))
+        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -120), 120);
+        const float up = pow2(min(7 - e, 127));
+        unit_of[nt] = pow2(e - 6) * (0.5f * p.scale);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const float4 v = make_float4(x[4 * w] * up, x[4 * w + 1] * up, x[4 * w + 2] * up, x[4 * w + 3] * up);
+            hi[nt][w] = pack_e4m3x4(v);
+            const float4 h = unpack_e4m3x4(hi[nt][w]);
+            lo[nt][w] = pack_e4m3x4(make_float4(v.x - h.x, v.y - h.y, v.z - h.z, v.w - h.w));
+        }
+    }
+    // this thread's rows: columns 2 c and 2 c + 1 (a row and its tangent, or two rows)
+    float unit_q[NT][R], unit_t[NT], slope2[NT][R];
+    int end[NT][R], pos[NT][R];  // keys 0 .. end - 1 are visible; the row's position
+    int least = len;             // keys that every row of the warp sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const float u0 = __shfl_sync(0xffffffffu, unit_of[nt], 8 * c), u1 = __shfl_sync(0xffffffffu, unit_of[nt], 8 * c + 4);
+        unit_q[nt][0] = u0;
+        if constexpr (!kTan) unit_q[nt][1] = u1;
+        unit_t[nt] = u1;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = tile * ROWS + (kTan ? nt * 4 + c : nt * 8 + 2 * c + i);
+            const bool live = r < n_rows;
+            pos[nt][i] = len - n + (live ? r % n : 0);
+            end[nt][i] = live && p.causal ? min(max(pos[nt][i] + 1, 0), len) : len;
+            slope2[nt][i] = p.slopes && live ? p.slopes[hk * p.group + r / n] * 1.4426950408889634f : 0.f;
+            least = min(least, end[nt][i]);
+        }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+
+    float acc[NT][8][4];  // channels 16 gr + 2 j + {0, 1} (pairs of elements), columns 2 c + {0, 1}
+    float m[NT][R], l[NT][R], g[NT], r0[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][j][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            m[nt][i] = -INFINITY;
+            l[nt][i] = 0.f;
+        }
+        g[nt] = r0[nt] = 0.f;
+    }
+    int E = SCALE_MIN;
+    bool begun = false;
+
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int run = run0 + warp; run < run1; run += WARPS) {
+        if (!mbar_wait_warp(bars + 8u * stage, phase, abort_flag, p.bound_ns)) break;
+        const bool valid[2] = {ids[0][0] >= 0, ids[0][1] >= 0};  // (a half without a page is hidden)
+        const uint32_t d = ring + (uint32_t)stage * STAGE_BYTES;
+        const float kscale[2] = {held[0][0].x, held[0][1].x}, vscale[2] = {held[0][0].y, held[0][1].y};
+
+        // S^T of tokens gr (elements 0, 1) and gr + 8 (2, 3) of each half; two chains of four products
+        float S[2][NT][4], S2[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[h][nt][i] = S2[h][nt][i] = 0.f;
+            // 16-byte units 2 c, 2 c + 1 of rows gr and gr + 8 (unit u of row r at u ^ (r & 7))
+            const uint32_t dh = d + (uint32_t)(h * HALF_BYTES + gr * HD);
+            const uint32_t u0 = (uint32_t)((2 * c) ^ gr) * 16u, u1 = (uint32_t)((2 * c + 1) ^ gr) * 16u;
+            const uint4 x0 = ld_shared_u4(dh + u0), x1 = ld_shared_u4(dh + u1);
+            const uint4 y0 = ld_shared_u4(dh + 8 * HD + u0), y1 = ld_shared_u4(dh + 8 * HD + u1);
+            const uint32_t a[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            const uint32_t a8[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+            for (int s = 0; s < 8; s += 2)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_e4m3(S[h][nt], a[s], a8[s], a[s + 1], a8[s + 1], hi[nt][s], hi[nt][s + 1]);
+                    mma_e4m3(S2[h][nt], a[s], a8[s], a[s + 1], a8[s + 1], lo[nt][s], lo[nt][s + 1]);
+                }
+        }
+        // log2-unit scores y of this thread's rows at keys run * 32 + 16 h + gr + {0, 8}
+        float y[2][NT][R][2], dS[2][NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float klog = kscale[h] * 1.4426950408889634f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        y[h][nt][i][e] = (S[h][nt][2 * e + i] + S2[h][nt][2 * e + i]) * (klog * unit_q[nt][i]);
+                    if constexpr (kTan) dS[h][nt][e] = (S[h][nt][2 * e + 1] + S2[h][nt][2 * e + 1]) * kscale[h];
+                }
+        }
+        if (p.cap_out > 0.f) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        float2 t, df;
+                        cap2(make_float2(y[h][nt][i][0], y[h][nt][i][1]), p.cap_in * 0.69314718055994531f, t, df);
+                        y[h][nt][i][0] = t.x * p.cap_out;
+                        y[h][nt][i][1] = t.y * p.cap_out;
+                        if constexpr (kTan) {
+                            dS[h][nt][0] *= df.x;
+                            dS[h][nt][1] *= df.y;
+                        }
+                    }
+        }
+        if (p.slopes) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const float dist = (float)(pos[nt][i] - run * 32 - 16 * h - gr);
+                        y[h][nt][i][0] = fmaf(-slope2[nt][i], fabsf(dist), y[h][nt][i][0]);
+                        y[h][nt][i][1] = fmaf(-slope2[nt][i], fabsf(dist - 8.f), y[h][nt][i][1]);
+                    }
+        }
+        if ((run + 1) * 32 > least || !valid[0] || !valid[1]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < R; ++i)
+                            if (!valid[h] || run * 32 + 16 * h + gr + 8 * e >= end[nt][i]) {
+                                y[h][nt][i][e] = -INFINITY;
+                                if constexpr (kTan) dS[h][nt][e] = 0.f;  // (codes past the end may be NaN)
+                            }
+        }
+        // running references of y + log2(value scale): raised when a weight would pass 2^8
+        const float ev[2] = {(float)exponent_of(vscale[0]), (float)exponent_of(vscale[1])};
+        bool need = false;
+        float top[NT][R];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                top[nt][i] = fmaxf(fmaxf(y[0][nt][i][0], y[0][nt][i][1]) + ev[0], fmaxf(y[1][nt][i][0], y[1][nt][i][1]) + ev[1]);
+                need |= top[nt][i] > m[nt][i] + 8.f;
+            }
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float alpha[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float mx = column_max(top[nt][i]);
+                    alpha[i] = 1.f;
+                    if (mx > m[nt][i]) {
+                        alpha[i] = ex2_approx(m[nt][i] - mx);
+                        m[nt][i] = mx;
+                    }
+                    l[nt][i] *= alpha[i];
+                    if constexpr (kTan) g[nt] *= alpha[i];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[nt][j][i] *= alpha[kTan ? 0 : (i & 1)];
+            }
+        }
+        if constexpr (kTan) {
+            const int ek = max(exponent_of(kscale[0]), exponent_of(kscale[1]));
+            if (ek > E) {  // a larger key scale: T moves to it
+                const float r = pow2_or_0(E - ek);
+                E = ek;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        acc[nt][j][1] *= r;
+                        acc[nt][j][3] *= r;
+                    }
+            }
+        }
+        const float rel = kTan ? pow2(-E - 18) : 0.f;
+        uint32_t bp[2][NT][2];  // P^T: tokens 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of column gr
+        float pe[2][NT][R][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float ref = m[nt][i] == -INFINITY ? 0.f : m[nt][i];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) pe[h][nt][i][e] = ex2_approx(y[h][nt][i][e] - ref);
+                l[nt][i] += (pe[0][nt][i][0] + pe[0][nt][i][1]) + (pe[1][nt][i][0] + pe[1][nt][i][1]);
+            }
+        if (kTan && !begun) {  // r: the first run's weighted mean of dS
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w = 0.f, s = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        w += pe[h][nt][0][e];
+                        s = fmaf(pe[h][nt][0][e], dS[h][nt][e], s);
+                    }
+                w = column_sum(w);
+                s = column_sum(s);
+                r0[nt] = w > 0.f ? s / w : 0.f;
+            }
+            begun = true;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float p0 = pe[h][nt][0][e] * vscale[h];
+                    float p1;
+                    if constexpr (kTan) {
+                        const float dc = dS[h][nt][e] - r0[nt];
+                        g[nt] = fmaf(pe[h][nt][0][e], dc, g[nt]);
+                        p1 = p0 * (dc * rel);
+                    } else {
+                        p1 = pe[h][nt][R - 1][e] * vscale[h];
+                    }
+                    bp[h][nt][e] = transpose_8x8(pack_f16x2(p0, p1));
+                }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // values of tokens 2c, 2c + 1, 2c + 8, 2c + 9, channels 16 gr .. 16 gr + 15; tokens past
+            // the end may hold anything (also NaN codes) and are zeroed
+            const uint32_t dh = d + (uint32_t)((2 + h) * HALF_BYTES + 2 * c * HD);
+            const uint32_t u0 = (uint32_t)(gr ^ (2 * c)) * 16u, u1 = HD + (uint32_t)(gr ^ (2 * c + 1)) * 16u;
+            uint4 v0 = ld_shared_u4(dh + u0), v1 = ld_shared_u4(dh + u1);
+            uint4 v2 = ld_shared_u4(dh + 8 * HD + u0), v3 = ld_shared_u4(dh + 8 * HD + u1);
+            if (!valid[h] || run * 32 + 16 * h + 16 > len) {
+                const int left = valid[h] ? len - run * 32 - 16 * h - 2 * c : 0;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                if (left <= 0) v0 = zero;
+                if (left <= 1) v1 = zero;
+                if (left <= 8) v2 = zero;
+                if (left <= 9) v3 = zero;
+            }
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+            const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                // channels 4 w .. 4 w + 3 of two tokens, interleaved: [c0 t, c0 t', c1 t, c1 t'], [c2 .., c3 ..]
+                uint32_t a[8];
+                e4m3x4_to_f16x2(__byte_perm(w0[w], w1[w], 0x5140), a[0], a[1]);
+                e4m3x4_to_f16x2(__byte_perm(w0[w], w1[w], 0x7362), a[2], a[3]);
+                e4m3x4_to_f16x2(__byte_perm(w2[w], w3[w], 0x5140), a[4], a[5]);
+                e4m3x4_to_f16x2(__byte_perm(w2[w], w3[w], 0x7362), a[6], a[7]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(acc[nt][2 * w], a[0], a[1], a[4], a[5], bp[h][nt][0], bp[h][nt][1]);
+                    mma_f16(acc[nt][2 * w + 1], a[2], a[3], a[6], a[7], bp[h][nt][0], bp[h][nt][1]);
+                }
+            }
+        }
+        // this stage is free again: the run STAGES further on
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) held[s][h] = held[s + 1][h];
+        copy(run + STAGES * WARPS, ids[STAGES], stage, held[STAGES - 1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int s = 0; s < STAGES; ++s) ids[s][h] = ids[s + 1][h];
+            ids[STAGES][h] = page_of(run + (STAGES + 1) * WARPS, h);
+        }
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (*abort_flag) {  // a wait gave up: let the copies in flight land before their memory is used again
+        if (lane == 0)
+            for (int s = 0; s < STAGES; ++s) mbar_wait_drain(bars + 8u * s, s < stage ? phase ^ 1u : phase, p.bound_ns);
+    }
+    __syncwarp();
+
+    // each warp's sums into its ring, [columns][128]; its statistics beside them
+    float *const mine = reinterpret_cast<float *>(smem + warp * RING_BYTES);
+    float *const stats = reinterpret_cast<float *>(smem + STATS_OFF) + warp * ST_FLOATS;
+    float *const cst = reinterpret_cast<float *>(smem + STATS_OFF) + WARPS * ST_FLOATS;  // the CTA's
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) l[nt][i] = column_sum(l[nt][i]);
+        if constexpr (kTan) g[nt] = column_sum(g[nt]);
+#pragma unroll
+        for (int col = 0; col < 2; ++col)
+#pragma unroll
+            for (int j = 0; j < 8; j += 2)
+                *reinterpret_cast<float4 *>(mine + (nt * 8 + 2 * c + col) * HD + 16 * gr + 2 * j) =
+                    make_float4(acc[nt][j][col], acc[nt][j][2 + col], acc[nt][j + 1][col], acc[nt][j + 1][2 + col]);
+        if (gr == 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int row = kTan ? nt * 4 + c : nt * 8 + 2 * c + i;
+                stats[ST_M + row] = m[nt][i];
+                stats[ST_L + row] = l[nt][i];
+            }
+            if constexpr (kTan) {
+                stats[ST_G + nt * 4 + c] = g[nt];
+                stats[ST_R + nt * 4 + c] = r0[nt];
+                if (warp == 0) cst[ST_UNIT + nt * 4 + c] = unit_t[nt];
+            }
+        }
+    }
+    if (lane == 0) reinterpret_cast<int *>(stats)[ST_E] = E;
+    __syncthreads();
+    // the CTA's sums, in warp order, into warp 0's ring; its statistics into cst.
+    // T and g of different r: sum p (dS - R) V = sum p (dS - r) V + (r - R) sum p V
     const float *const st = reinterpret_cast<const float *>(smem + STATS_OFF);
-    float *const cst = reinterpret_cast<float *>(smem + STATS_OFF) + WARPS * 64;
     int Ec = SCALE_MIN;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) Ec = max(Ec, reinterpret_cast<const int *>(st + 64 * w)[48]);
-    auto weight = [](float m, float top) -> float { return m == -INFINITY ? 0.f : ex2_approx(m - top); };
-    auto shrink = [](int e, int top) -> float { return e - top >= -126 ? pow2(e - top) : 0.f; };
-    for (int x = threadIdx.x; x < 16 * HD / 4; x += THREADS) {
-        const int r = x / (HD / 4);
-        const int row = kTan ? (r & 7) : r;
-        float top = st[row];
+    for (int w = 0; w < WARPS; ++w) Ec = max(Ec, reinterpret_cast<const int *>(st + ST_FLOATS * w)[ST_E]);
+    for (int x = threadIdx.x; x < ROWS * HD / 4; x += THREADS) {
+        const int row = x / (HD / 4), d4 = x % (HD / 4);
+        float top = -INFINITY, Rc = 0.f;
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) top = fmaxf(top, st[64 * w + row]);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < WARPS; ++w)
+            if (st[ST_FLOATS * w + ST_M + row] > top) {
+                top = st[ST_FLOATS * w + ST_M + row];
+                if (kTan) Rc = st[ST_FLOATS * w + ST_R + row];
+            }
+        float4 so = make_float4(0.f, 0.f, 0.f, 0.f), sT = so;
         float lt = 0.f, gt = 0.f;
+        const int oc = (kTan ? 2 * row : row) * HD + 4 * d4;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            const float a = weight(st[64 * w + row], top);
-            lt = fmaf(a, st[64 * w + 16 + row], lt);
-            if (kTan) gt = fmaf(a, st[64 * w + 32 + row], gt);
-            const float f = kTan && r >= 8 ? a * shrink(reinterpret_cast<const int *>(st + 64 * w)[48], Ec) : a;
-            const float4 v = *reinterpret_cast<const float4 *>(smem + w * RING_BYTES + x * 16);
-            sum.x = fmaf(f, v.x, sum.x);
-            sum.y = fmaf(f, v.y, sum.y);
-            sum.z = fmaf(f, v.z, sum.z);
-            sum.w = fmaf(f, v.w, sum.w);
+            const float *const sw = st + ST_FLOATS * w;
+            const float *const vw = reinterpret_cast<const float *>(smem + w * RING_BYTES);
+            const float f = ref_weight(sw[ST_M + row], top);
+            const float4 v = *reinterpret_cast<const float4 *>(vw + oc);
+            lt = fmaf(f, sw[ST_L + row], lt);
+            axpy(so, f, v);
+            if constexpr (kTan) {
+                const float dr = sw[ST_R + row] - Rc;
+                gt = fmaf(f, fmaf(dr, sw[ST_L + row], sw[ST_G + row]), gt);
+                axpy(sT, f * pow2_or_0(reinterpret_cast<const int *>(sw)[ST_E] - Ec),
+                     *reinterpret_cast<const float4 *>(vw + oc + HD));
+                axpy(sT, f * dr * pow2(-Ec - 18), v);
+            }
         }
-        *reinterpret_cast<float4 *>(smem + x * 16) = sum;  // (this thread's own place in warp 0's ring)
-        if ((x & (HD / 4 - 1)) == 0 && r == row) {
-            cst[row] = top;
-            cst[16 + row] = lt;
-            if (kTan) cst[32 + row] = gt;
+        // (each place of warp 0's ring is read and written by this thread alone)
+        *reinterpret_cast<float4 *>(smem + oc * 4) = so;
+        if constexpr (kTan) *reinterpret_cast<float4 *>(smem + (oc + HD) * 4) = sT;
+        if (d4 == 0) {
+            cst[ST_M + row] = top;
+            cst[ST_L + row] = lt;
+            if constexpr (kTan) {
+                cst[ST_G + row] = gt;
+                cst[ST_R + row] = Rc;
+            }
         }
-        if (x == 0) reinterpret_cast<int *>(cst)[48] = Ec;
+        if (x == 0) reinterpret_cast<int *>(cst)[ST_E] = Ec;
     }
     auto cluster_sync = [&]() {
         if (p.splits > 1)
@@ -664,36 +876,36 @@ __global__ void __launch_bounds__(THREADS, 3) cache_attn_kernel(const __grid_con
     };
     cluster_sync();
     // the cluster's sums, in rank order: the ranks share out the tile's rows x channels
-    const uint32_t cstat = sbase + STATS_OFF + WARPS * 256u;
+    const uint32_t cstat = sbase + STATS_OFF + WARPS * ST_FLOATS * 4u;
     for (int x = rank * THREADS + (int)threadIdx.x; x < ROWS * HD / 4; x += p.splits * THREADS) {
         const int row = x / (HD / 4), d4 = x % (HD / 4), r = tile * ROWS + row;
         if (r >= n_rows) continue;
-        float top = -INFINITY;
+        float top = -INFINITY, Rt = 0.f;
         int Et = SCALE_MIN;
         for (int s = 0; s < p.splits; ++s) {
             const uint32_t a = cluster_map(cstat, (uint32_t)s);
-            top = fmaxf(top, ld_cluster(a + 4u * row));
-            Et = max(Et, __float_as_int(ld_cluster(a + 4u * 48)));
+            const float ms = ld_cluster(a + 4u * (ST_M + row));
+            if (ms > top) {
+                top = ms;
+                if (kTan) Rt = ld_cluster(a + 4u * (ST_R + row));
+            }
+            if (kTan) Et = max(Et, __float_as_int(ld_cluster(a + 4u * ST_E)));
         }
         float4 so = make_float4(0.f, 0.f, 0.f, 0.f), sT = so;
         float lt = 0.f, gt = 0.f;
+        const uint32_t oc = (uint32_t)((kTan ? 2 * row : row) * HD + 4 * d4) * 4u;
         for (int s = 0; s < p.splits; ++s) {
-            const uint32_t a = cluster_map(cstat, (uint32_t)s), v = cluster_map(sbase, (uint32_t)s);
-            const float f = weight(ld_cluster(a + 4u * row), top);
-            lt = fmaf(f, ld_cluster(a + 4u * (16 + row)), lt);
-            const float4 o4 = ld_cluster4(v + (uint32_t)(row * HD + 4 * d4) * 4u);
-            so.x = fmaf(f, o4.x, so.x);
-            so.y = fmaf(f, o4.y, so.y);
-            so.z = fmaf(f, o4.z, so.z);
-            so.w = fmaf(f, o4.w, so.w);
+            const uint32_t a = cluster_map(cstat, (uint32_t)s), v = cluster_map(sbase, (uint32_t)s) + oc;
+            const float f = ref_weight(ld_cluster(a + 4u * (ST_M + row)), top);
+            const float ls = ld_cluster(a + 4u * (ST_L + row));
+            const float4 o4 = ld_cluster4(v);
+            lt = fmaf(f, ls, lt);
+            axpy(so, f, o4);
             if constexpr (kTan) {
-                gt = fmaf(f, ld_cluster(a + 4u * (32 + row)), gt);
-                const float ft = f * shrink(__float_as_int(ld_cluster(a + 4u * 48)), Et);
-                const float4 t4 = ld_cluster4(v + (uint32_t)((row + 8) * HD + 4 * d4) * 4u);
-                sT.x = fmaf(ft, t4.x, sT.x);
-                sT.y = fmaf(ft, t4.y, sT.y);
-                sT.z = fmaf(ft, t4.z, sT.z);
-                sT.w = fmaf(ft, t4.w, sT.w);
+                const float dr = ld_cluster(a + 4u * (ST_R + row)) - Rt;
+                gt = fmaf(f, fmaf(dr, ls, ld_cluster(a + 4u * (ST_G + row))), gt);
+                axpy(sT, f * pow2_or_0(__float_as_int(ld_cluster(a + 4u * ST_E)) - Et), ld_cluster4(v + HD * 4u));
+                axpy(sT, f * dr * pow2(-Et - 18), o4);
             }
         }
         const float inv = lt > 0.f ? 1.f / lt : 0.f;  // a row that sees no key: zeros, lse = -infinity
@@ -702,12 +914,11 @@ __global__ void __launch_bounds__(THREADS, 3) cache_attn_kernel(const __grid_con
         const size_t out = (size_t)(p.o_b * b + p.o_h * h + first + t);
         *reinterpret_cast<uint2 *>(p.o + out * HD + 4 * d4) = make_uint2(pack_bf16x2(ov.x, ov.y), pack_bf16x2(ov.z, ov.w));
         if constexpr (kTan) {
-            // T is in units of 2^(E + 10) times the tangent row's
-            const float mu = gt * inv;
-            const float unit = cst[TAN_UNITS + row] * pow2(Et) * (1024.f * inv);
+            // T is in units of 2^(E + 18), and like g relative to r and in the tangent row's units
+            const float mu = gt * inv, in = pow2(Et + 18) * inv, unit = cst[ST_UNIT + row];
             *reinterpret_cast<uint2 *>(p.to + out * HD + 4 * d4) =
-                make_uint2(pack_bf16x2(fmaf(-mu, ov.x, sT.x * unit), fmaf(-mu, ov.y, sT.y * unit)),
-                           pack_bf16x2(fmaf(-mu, ov.z, sT.z * unit), fmaf(-mu, ov.w, sT.w * unit)));
+                make_uint2(pack_bf16x2(unit * fmaf(-mu, ov.x, sT.x * in), unit * fmaf(-mu, ov.y, sT.y * in)),
+                           pack_bf16x2(unit * fmaf(-mu, ov.z, sT.z * in), unit * fmaf(-mu, ov.w, sT.w * in)));
         }
         if (d4 == 0 && p.lse)
             p.lse[out] = lt > 0.f ? (top + __log2f(lt)) * 0.69314718055994531f : -INFINITY;

@@ -20,6 +20,8 @@ int encoder();                    // resolves cuTensorMapEncodeTiled
 uint64_t wait_bound_ns();
 // [BH][L][d] bf16 tensor, boxes of 64 columns x box_rows rows, 128-byte swizzle
 int encode(CUtensorMap *m, const void *ptr, int64_t d, int64_t L, int64_t BH, uint32_t box_rows);
+// [rows][128] bytes, boxes of 128 columns x box_rows rows, 128-byte swizzle
+int encode_codes(CUtensorMap *m, const void *ptr, int64_t rows, uint32_t box_rows);
 uint64_t stats_bytes(int64_t BH, int64_t Lq);
 uint64_t partial_bytes(int64_t BH, int64_t Lk, int64_t parts);
 
@@ -28,6 +30,7 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 // device status words of the other translation units (each holds its own):
 // read into *word (ORed), cleared when set
 cudaError_t scored_status(int *word);
+cudaError_t cache_status(int *word);
 
 }  // namespace host
 }  // namespace ajvp
