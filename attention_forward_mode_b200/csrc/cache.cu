@@ -26,12 +26,12 @@ struct Setup {
 };
 Setup g_setup[host::kMaxDevices];
 
-template <bool kTan, int NT, int W>
+template <bool kTan, int NT, int W, int S>
 cudaError_t set_attn() {
-    cudaError_t e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan, NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         cache::attn_smem(W));
+    cudaError_t e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan, NT, W, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         cache::attn_smem(W, S));
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan, NT, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(cache::cache_attn_kernel<kTan, NT, W, S>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;
 }
 
@@ -40,9 +40,9 @@ int setup(int *dev) {
     if (rc != AJVP_OK) return rc;
     Setup &s = g_setup[*dev];
     std::call_once(s.once, [&]() {
-        for (cudaError_t e : {set_attn<true, 1, 4>(), set_attn<true, 2, 4>(), set_attn<false, 1, 4>(),
-                              set_attn<false, 2, 4>(), set_attn<true, 1, 8>(), set_attn<true, 2, 8>(),
-                              set_attn<false, 1, 8>(), set_attn<false, 2, 8>()})
+        for (cudaError_t e : {set_attn<true, 1, 4, 2>(), set_attn<true, 2, 4, 2>(), set_attn<false, 1, 4, 2>(),
+                              set_attn<false, 2, 4, 2>(), set_attn<true, 1, 8, 3>(), set_attn<true, 2, 8, 3>(),
+                              set_attn<false, 1, 8, 3>(), set_attn<false, 2, 8, 3>()})
             if (s.error == cudaSuccess) s.error = e;
     });
     return s.error == cudaSuccess ? AJVP_OK : host::fail(s.error);
@@ -177,7 +177,7 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     const int64_t group = H / Hkv;
     if (group * n >= kMaxInt || n_seq * Hkv >= kMaxInt) return AJVP_ERR_TOO_LARGE;
     // one column tile where the rows fit it (half the accumulators, four CTAs per SM), else two
-    const int64_t one = tq ? 4 : 8, rows = group * n <= one ? one : 2 * one;
+    const int64_t one = tq ? 4 : 8, rows = getenv("AJVP_NT") ? one * atoi(getenv("AJVP_NT")) : (group * n <= one ? one : 2 * one);
     const int64_t tiles = (group * n + rows - 1) / rows;
     if (n_seq * Hkv >= kMaxInt / 16 / tiles) return AJVP_ERR_TOO_LARGE;
     const int64_t units = n_seq * Hkv * tiles;
@@ -232,7 +232,7 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     cfg.gridDim = dim3((unsigned)(units * p.splits));
     const int warps = getenv("AJVP_W") ? atoi(getenv("AJVP_W")) : 4;
     cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = cache::attn_smem(warps);
+    cfg.dynamicSmemBytes = warps == 4 ? cache::attn_smem(4, 2) : cache::attn_smem(8, 3);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -240,15 +240,16 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto launch = [&](auto w) {
-        constexpr int W = decltype(w)::value;
+    auto launch = [&](auto w, auto stages) {
+        constexpr int W = decltype(w)::value, S = decltype(stages)::value;
         if (rows == one)
-            return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 1, W>, p)
-                      : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, W>, p);
-        return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 2, W>, p)
-                  : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 2, W>, p);
+            return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 1, W, S>, p)
+                      : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, W, S>, p);
+        return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 2, W, S>, p)
+                  : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 2, W, S>, p);
     };
-    const cudaError_t e = warps == 4 ? launch(std::integral_constant<int, 4>()) : launch(std::integral_constant<int, 8>());
+    const cudaError_t e = warps == 4 ? launch(std::integral_constant<int, 4>(), std::integral_constant<int, 2>())
+                                     : launch(std::integral_constant<int, 8>(), std::integral_constant<int, 3>());
     return e == cudaSuccess ? AJVP_OK : host::fail(e);
 }
 

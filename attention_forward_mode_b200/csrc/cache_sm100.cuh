@@ -290,18 +290,18 @@ struct AttnParams {
     unsigned page_magic;          // ceil(2^32 / (page / 16)): x / (page / 16) = umulhi(x, magic); 0 for pages of 16
 };
 
-constexpr int STAGES = 2;
 constexpr int HALF_BYTES = 16 * HD;                  // 16 tokens of keys, or of values
 constexpr int STAGE_BYTES = 4 * HALF_BYTES;          // 32 tokens: keys, then values
-constexpr int RING_BYTES = STAGES * STAGE_BYTES;     // per warp
 // statistics of a warp, or of the CTA: floats at ST_M + row etc.
 constexpr int ST_M = 0, ST_L = 16, ST_G = 32, ST_R = 40, ST_E = 48, ST_UNIT = 49, ST_FLOATS = 64;
-// shared memory of a CTA of `warps` warps: rings, a barrier per warp and stage and
-// the CTA's abort flag, statistics of the warps and of the CTA
-__host__ __device__ constexpr int bars_off(int warps) { return warps * RING_BYTES; }
-__host__ __device__ constexpr int stats_off(int warps) { return bars_off(warps) + warps * STAGES * 8 + 16; }
-__host__ __device__ constexpr int attn_smem(int warps) { return stats_off(warps) + (warps + 1) * ST_FLOATS * 4; }
-static_assert(16 * HD * 4 <= RING_BYTES, "the sums of a warp fit its ring");
+// shared memory of a CTA: the warps' rings of `stages` runs, a barrier per warp and
+// stage and the CTA's abort flag, statistics of the warps and of the CTA
+__host__ __device__ constexpr int bars_off(int warps, int stages) { return warps * stages * STAGE_BYTES; }
+__host__ __device__ constexpr int stats_off(int warps, int stages) { return bars_off(warps, stages) + warps * stages * 8 + 16; }
+__host__ __device__ constexpr int attn_smem(int warps, int stages) {
+    return stats_off(warps, stages) + (warps + 1) * ST_FLOATS * 4;
+}
+static_assert(16 * HD * 4 <= STAGE_BYTES, "the sums of a warp fit a stage");
 
 // 2-D tiled load global -> shared, completion counted on `bar` (bytes)
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y) {
@@ -359,15 +359,14 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 __device__ __forceinline__ void axpy(float4 &y, float a, float4 x) {
@@ -381,12 +380,15 @@ __device__ __forceinline__ float ref_weight(float m, float top) { return m == -I
 __device__ __forceinline__ float pow2_or_0(int e) { return e >= -126 ? pow2(e) : 0.f; }
 
 // NT column tiles of 8: with a tangent 4 NT query rows and their tangents, else 8 NT query rows.
-// WARPS: 4 (three CTAs per SM), or 8 for launches that leave each SM one CTA at most.
-template <bool kTan, int NT, int WARPS>
+// WARPS x STAGES: 4 x 2 (three CTAs per SM for one column tile, two for two), or
+// 8 x 3 for launches of at most one CTA per SM, where a warp's own copies have to
+// cover the latency.
+template <bool kTan, int NT, int WARPS, int STAGES>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1) cache_attn_kernel(const __grid_constant__ AttnParams p) {
     constexpr int ROWS = (kTan ? 4 : 8) * NT;  // query rows of a tile
     constexpr int R = kTan ? 1 : 2;            // query rows per thread and column tile
-    constexpr int THREADS = 32 * WARPS, STATS_OFF = stats_off(WARPS);
+    constexpr int THREADS = 32 * WARPS, STATS_OFF = stats_off(WARPS, STAGES);
+    constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // per warp
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -413,8 +415,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     const int run0 = min(rank * per, runs), run1 = min(run0 + per, runs);
 
     const uint32_t ring = sbase + (uint32_t)warp * RING_BYTES;
-    const uint32_t bars = sbase + bars_off(WARPS) + (uint32_t)warp * STAGES * 8u;
-    volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + bars_off(WARPS) + WARPS * STAGES * 8);
+    const uint32_t bars = sbase + bars_off(WARPS, STAGES) + (uint32_t)warp * STAGES * 8u;
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + bars_off(WARPS, STAGES) + WARPS * STAGES * 8);
     if (lane == 0) {
 #pragma unroll
         for (int s = 0; s < STAGES; ++s) mbar_init(bars + 8u * s, 1);
@@ -875,36 +877,41 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             __syncthreads();
     };
     cluster_sync();
-    // the cluster's sums, in rank order: the ranks share out the tile's rows x channels
-    const uint32_t cstat = sbase + STATS_OFF + WARPS * ST_FLOATS * 4u;
+    // the cluster's sums, in rank order: the ranks share out the tile's rows x channels.  All
+    // ranks' statistics first, by independent loads, into memory that the rings no longer need
+    float *const ast = reinterpret_cast<float *>(smem + RING_BYTES);
+    for (int i = threadIdx.x; i < p.splits * ST_FLOATS; i += THREADS)
+        ast[i] = ld_cluster(cluster_map(sbase + STATS_OFF + (WARPS * ST_FLOATS + (i & (ST_FLOATS - 1))) * 4u,
+                                        (uint32_t)(i / ST_FLOATS)));
+    __syncthreads();
     for (int x = rank * THREADS + (int)threadIdx.x; x < ROWS * HD / 4; x += p.splits * THREADS) {
         const int row = x / (HD / 4), d4 = x % (HD / 4), r = tile * ROWS + row;
         if (r >= n_rows) continue;
         float top = -INFINITY, Rt = 0.f;
         int Et = SCALE_MIN;
         for (int s = 0; s < p.splits; ++s) {
-            const uint32_t a = cluster_map(cstat, (uint32_t)s);
-            const float ms = ld_cluster(a + 4u * (ST_M + row));
-            if (ms > top) {
-                top = ms;
-                if (kTan) Rt = ld_cluster(a + 4u * (ST_R + row));
+            const float *const a = ast + s * ST_FLOATS;
+            if (a[ST_M + row] > top) {
+                top = a[ST_M + row];
+                if (kTan) Rt = a[ST_R + row];
             }
-            if (kTan) Et = max(Et, __float_as_int(ld_cluster(a + 4u * ST_E)));
+            if (kTan) Et = max(Et, __float_as_int(a[ST_E]));
         }
         float4 so = make_float4(0.f, 0.f, 0.f, 0.f), sT = so;
         float lt = 0.f, gt = 0.f;
         const uint32_t oc = (uint32_t)((kTan ? 2 * row : row) * HD + 4 * d4) * 4u;
+#pragma unroll 4
         for (int s = 0; s < p.splits; ++s) {
-            const uint32_t a = cluster_map(cstat, (uint32_t)s), v = cluster_map(sbase, (uint32_t)s) + oc;
-            const float f = ref_weight(ld_cluster(a + 4u * (ST_M + row)), top);
-            const float ls = ld_cluster(a + 4u * (ST_L + row));
+            const float *const a = ast + s * ST_FLOATS;
+            const uint32_t v = cluster_map(sbase, (uint32_t)s) + oc;
+            const float f = ref_weight(a[ST_M + row], top);
             const float4 o4 = ld_cluster4(v);
-            lt = fmaf(f, ls, lt);
+            lt = fmaf(f, a[ST_L + row], lt);
             axpy(so, f, o4);
             if constexpr (kTan) {
-                const float dr = ld_cluster(a + 4u * (ST_R + row)) - Rt;
-                gt = fmaf(f, fmaf(dr, ls, ld_cluster(a + 4u * (ST_G + row))), gt);
-                axpy(sT, f * pow2_or_0(__float_as_int(ld_cluster(a + 4u * ST_E)) - Et), ld_cluster4(v + HD * 4u));
+                const float dr = a[ST_R + row] - Rt;
+                gt = fmaf(f, fmaf(dr, a[ST_L + row], a[ST_G + row]), gt);
+                axpy(sT, f * pow2_or_0(__float_as_int(a[ST_E]) - Et), ld_cluster4(v + HD * 4u));
                 axpy(sT, f * dr * pow2(-Et - 18), o4);
             }
         }
