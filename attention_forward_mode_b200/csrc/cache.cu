@@ -8,9 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <cstdlib>
 #include <mutex>
-#include <type_traits>
 
 #include "attn_jvp.h"
 #include "cache_sm100.cuh"
@@ -41,8 +39,7 @@ int setup(int *dev) {
     Setup &s = g_setup[*dev];
     std::call_once(s.once, [&]() {
         for (cudaError_t e : {set_attn<true, 1, 4, 2>(), set_attn<true, 2, 4, 2>(), set_attn<false, 1, 4, 2>(),
-                              set_attn<false, 2, 4, 2>(), set_attn<true, 1, 8, 3>(), set_attn<true, 2, 8, 3>(),
-                              set_attn<false, 1, 8, 3>(), set_attn<false, 2, 8, 3>()})
+                              set_attn<false, 2, 4, 2>(), set_attn<true, 1, 8, 3>(), set_attn<false, 1, 8, 3>()})
             if (s.error == cudaSuccess) s.error = e;
     });
     return s.error == cudaSuccess ? AJVP_OK : host::fail(s.error);
@@ -62,13 +59,43 @@ int check_cache(int64_t n_seq, int64_t H, int64_t Hkv, int64_t n_pages, int64_t 
     return AJVP_OK;
 }
 
-// CTAs per (sequence, key head, row tile), a power of two: doubled while the
-// launch has fewer than two waves of resident CTAs (three per SM) and every
-// part keeps at least two runs of 16 tokens per warp of the longest sequence.
-int split_count(int64_t units, int64_t tokens, int sm_count) {
-    int s = 1;
-    while (s < 16 && units * s < 6 * (int64_t)sm_count && tokens / 16 >= 2 * 4 * 2 * (int64_t)s) s *= 2;
-    return s;
+// How a launch is cut up.  A unit is a (sequence, key head, row tile); every
+// further row tile of a key head reads its codes again (from L2).
+struct Plan {
+    int tiles;   // row tiles per (sequence, key head)
+    int nt;      // column tiles of a row tile: 4 nt rows with tangents, 8 nt without
+    int warps;   // per CTA
+    int splits;  // CTAs per unit
+};
+
+// Measured over 18 shapes of 1 .. 64 sequences of 16 .. 32760 tokens, within 10 % of
+// the best of all (nt, warps, splits) on a 148-SM B200 wherever the table is as long
+// as the sequences:
+// nt 2 (rows that do not fit one column tile): halves the reading and converting
+//   of codes, but with few units two tiles run side by side (4 sequences, 4 key heads,
+//   8 rows with tangents: 18 against 22 us; 16 sequences of 8 key heads, 5 rows: 92
+//   against 62), so from 64 units on.
+// splits: as many as keep every CTA resident at once (three of four warps per SM, two
+//   of nt 2, a tenth left free for clusters that do not fill their place), while each
+//   warp keeps two runs of 32 tokens (8 sequences of 2048, 12 heads: 1, 2, 4, 8 parts
+//   take 21, 15.5, 13, 21 us).
+// warps 8: up to an SM's worth of CTAs, where only more warps per SM hide the
+//   latency of a run (one sequence of 4096, 12 heads: 10.5 against 11.8 us); clusters of
+//   them fill no more than some 120 SMs.
+Plan make_plan(int64_t n_seq, int64_t Hkv, int64_t rows, bool tangent, int64_t tokens, int sm_count) {
+    const int64_t one = tangent ? 4 : 8;
+    Plan p;
+    const int64_t wide = n_seq * Hkv * ((rows + 2 * one - 1) / (2 * one));
+    p.nt = rows > one && wide >= 64 ? 2 : 1;
+    p.tiles = (int)((rows + p.nt * one - 1) / (p.nt * one));
+    const int64_t units = n_seq * Hkv * p.tiles, runs = (tokens + 31) / 32;
+    const int64_t most8 = sm_count * 13 / 16;
+    p.warps = p.nt == 1 && units * 8 <= most8 ? 8 : 4;
+    const int64_t most = p.warps == 8 ? most8 : sm_count * (p.nt == 1 ? 3 : 2) * 9 / 10;
+    const int64_t least = 8;  // runs of a CTA: one per warp of eight, two per warp of four
+    p.splits = 1;
+    while (p.splits < 16 && units * p.splits * 2 <= most && runs >= least * p.splits * 2) p.splits *= 2;
+    return p;
 }
 
 }  // namespace
@@ -176,12 +203,9 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
         if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
     const int64_t group = H / Hkv;
     if (group * n >= kMaxInt || n_seq * Hkv >= kMaxInt) return AJVP_ERR_TOO_LARGE;
-    // one column tile where the rows fit it (half the accumulators, four CTAs per SM), else two
-    const int64_t one = tq ? 4 : 8, rows = getenv("AJVP_NT") ? one * atoi(getenv("AJVP_NT")) : (group * n <= one ? one : 2 * one);
-    const int64_t tiles = (group * n + rows - 1) / rows;
-    if (n_seq * Hkv >= kMaxInt / 16 / tiles) return AJVP_ERR_TOO_LARGE;
-    const int64_t units = n_seq * Hkv * tiles;
     if (n_pages < 1) return AJVP_ERR_INVALID_ARG;
+    const int64_t most_tiles = (group * n + (tq ? 3 : 7)) / (tq ? 4 : 8);
+    if (n_seq * Hkv >= kMaxInt / 16 / most_tiles) return AJVP_ERR_TOO_LARGE;
     int dev = 0;
     if ((rc = setup(&dev)) != AJVP_OK) return rc;
     if ((rc = host::encoder()) != AJVP_OK) return rc;
@@ -219,20 +243,18 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     p.table_width = (int)table_width;
     p.causal = causal != 0;
     p.bound_ns = host::wait_bound_ns();
-    p.box = page % 32 == 0 ? 32 : 16;
-    if ((rc = host::encode_codes(&p.tm_k, k_cache, n_pages * Hkv * page, (uint32_t)p.box)) != AJVP_OK) return rc;
-    if ((rc = host::encode_codes(&p.tm_v, v_cache, n_pages * Hkv * page, (uint32_t)p.box)) != AJVP_OK) return rc;
+    if ((rc = host::encode_codes(&p.tm_k, k_cache, n_pages * Hkv * page, 16)) != AJVP_OK) return rc;
+    if ((rc = host::encode_codes(&p.tm_v, v_cache, n_pages * Hkv * page, 16)) != AJVP_OK) return rc;
     p.page_magic = page == 16 ? 0u : (unsigned)(((uint64_t(1) << 32) + page / 16 - 1) / (page / 16));
-    p.tiles = (int)tiles;
-    p.splits = split_count(units, table_width * page, host::sm_count(dev));
-    if (getenv("AJVP_S")) p.splits = atoi(getenv("AJVP_S"));
+    const Plan plan = make_plan(n_seq, Hkv, group * n, tq != nullptr, table_width * page, host::sm_count(dev));
+    p.tiles = plan.tiles;
+    p.splits = plan.splits;
 
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(units * p.splits));
-    const int warps = getenv("AJVP_W") ? atoi(getenv("AJVP_W")) : 4;
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = warps == 4 ? cache::attn_smem(4, 2) : cache::attn_smem(8, 3);
+    cfg.gridDim = dim3((unsigned)(n_seq * Hkv * plan.tiles * plan.splits));
+    cfg.blockDim = dim3(32 * plan.warps);
+    cfg.dynamicSmemBytes = plan.warps == 4 ? cache::attn_smem(4, 2) : cache::attn_smem(8, 3);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -240,16 +262,13 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto launch = [&](auto w, auto stages) {
-        constexpr int W = decltype(w)::value, S = decltype(stages)::value;
-        if (rows == one)
-            return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 1, W, S>, p)
-                      : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, W, S>, p);
-        return tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 2, W, S>, p)
-                  : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 2, W, S>, p);
-    };
-    const cudaError_t e = warps == 4 ? launch(std::integral_constant<int, 4>(), std::integral_constant<int, 2>())
-                                     : launch(std::integral_constant<int, 8>(), std::integral_constant<int, 3>());
+    const cudaError_t e =
+        plan.warps == 8 ? (tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 1, 8, 3>, p)
+                              : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, 8, 3>, p))
+        : plan.nt == 1 ? (tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 1, 4, 2>, p)
+                             : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, 4, 2>, p))
+                       : (tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 2, 4, 2>, p)
+                             : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 2, 4, 2>, p));
     return e == cudaSuccess ? AJVP_OK : host::fail(e);
 }
 

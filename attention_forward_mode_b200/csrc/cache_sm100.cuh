@@ -251,22 +251,23 @@ static __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(con
 // so that few query rows leave little of a product empty.  With a tangent the
 // columns alternate q, tq: one thread holds S and dS of the same (row, key), and
 // the columns of the second product alternate P, P dS, giving O and T at once.
-// K Q^T takes the codes as they are (m16n8k32 in e4m3): a bf16 query channel is
-// the sum of two e4m3 values, its leading four bits and the rest, so two products
-// give the exact sum without turning a code into anything.  V^T P^T is m16n8k16
-// in f16 (e4m3 would leave P eight bits): bytes of two tokens' value rows pair up
-// as A fragments, converted two per instruction, and P^T is turned by movmatrix.
+// The codes become f16 operands in registers, two per instruction (m16n8k32 in
+// e4m3 takes them as they are, but needs the queries in two parts and P in three,
+// and measured slower: 174 instead of 132 us for 64 sequences of up to 8192
+// tokens).  Bytes of two tokens' value rows pair up as A fragments, and P^T is
+// turned by movmatrix.
 // mma.sync rather than tcgen05: 128-row accumulators in tensor memory would be
 // nearly empty, and the products are not what bounds the kernel.  Splits of a
 // sequence are the CTAs of one cluster, which join their sums through distributed
 // shared memory: no workspace, one launch, and a fixed order of additions.
 //
 // Operand ranges: queries and tangents are scaled by a power of two per row so
-// that the largest lies in [128, 256) (channels 2^-10 below it start to lose
-// bits); P is weighted by its page's value scale, and the running reference M
-// covers both, so |P| <= 2^8; dS is taken relative to the row's first run (r, so
-// that a nearly constant dS does not cancel against mu O) and to the largest key
-// scale so far (E) and 2^-18, so that |P dS| < 2^15.
+// that the largest lies in [1, 2) (bf16 channels are then exact but for those
+// 2^-14 below it).  P is weighted by its page's value scale and a row's reference
+// M covers both: it is set so that the largest weight is 2^7 and moves when one
+// would pass 2^8.75, so weights 2^-21 below the row's largest start to lose bits.
+// P dS, with dS relative to the row's first run (r, so that a nearly constant dS
+// does not cancel against mu O), has a power of two of its own, kept the same way.
 struct AttnParams {
     const __nv_bfloat16 *q, *tq;  // row (b, h, t) at q_b b + q_h h + q_t t channels; packed: cu[b] + t in place of t
     __nv_bfloat16 *o, *to;        // rows o_b b + o_h h + t (packed: + cu[b])
@@ -284,16 +285,16 @@ struct AttnParams {
     int n;                        // query tokens per sequence (packed: of the longest)
     int tiles;                    // row tiles per (sequence, key head)
     int splits;                   // CTAs per cluster
-    CUtensorMap tm_k, tm_v;       // codes [rows][128], boxes of `box` rows
-    int box;                      // 32 where pages are multiples of it, else 16
+    CUtensorMap tm_k, tm_v;       // codes [rows][128], boxes of 16 rows
     unsigned long long bound_ns;
     unsigned page_magic;          // ceil(2^32 / (page / 16)): x / (page / 16) = umulhi(x, magic); 0 for pages of 16
 };
 
+constexpr int EW_MIN = -120;                         // T's unit before any weight
 constexpr int HALF_BYTES = 16 * HD;                  // 16 tokens of keys, or of values
 constexpr int STAGE_BYTES = 4 * HALF_BYTES;          // 32 tokens: keys, then values
 // statistics of a warp, or of the CTA: floats at ST_M + row etc.
-constexpr int ST_M = 0, ST_L = 16, ST_G = 32, ST_R = 40, ST_E = 48, ST_UNIT = 49, ST_FLOATS = 64;
+constexpr int ST_M = 0, ST_L = 16, ST_G = 32, ST_R = 40, ST_E = 48, ST_UNIT = 56, ST_FLOATS = 64;
 // shared memory of a CTA: the warps' rings of `stages` runs, a barrier per warp and
 // stage and the CTA's abort flag, statistics of the warps and of the CTA
 __host__ __device__ constexpr int bars_off(int warps, int stages) { return warps * stages * STAGE_BYTES; }
@@ -310,19 +311,20 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same without an addend
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // four e4m3 codes as two f16x2; exact
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -331,15 +333,15 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t &lo, uint32
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 // an 8 x 8 matrix of 16-bit values, row lane / 4, columns 2 (lane % 4) + {0, 1}: its transpose
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 // over the eight lanes of the same lane % 4
 __device__ __forceinline__ float column_max(float x) {
@@ -377,6 +379,10 @@ __device__ __forceinline__ void axpy(float4 &y, float a, float4 x) {
 }
 // weight of sums at reference m against reference top
 __device__ __forceinline__ float ref_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
+// e with |x| in [2^e, 2^(e + 1)), at most 119
+__device__ __forceinline__ int binary_exponent(float x) {
+    return min((int)((__float_as_uint(x) >> 23) & 255u) - 127, 119);
+}
 __device__ __forceinline__ float pow2_or_0(int e) { return e >= -126 ? pow2(e) : 0.f; }
 
 // NT column tiles of 8: with a tangent 4 NT query rows and their tangents, else 8 NT query rows.
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + bars_off(WARPS, STAGES) + WARPS * STAGES * 8);
     if (lane == 0) {
 #pragma unroll
-        for (int s = 0; s < STAGES; ++s) mbar_init(bars + 8u * s, 1);
+        for (int s = 0; s < STAGES; ++s) mbar_init(bars + 8u * s, 2);  // lanes 0 and 1
         if (warp == 0) *abort_flag = 0;
         fence_barrier_init();
     }
@@ -427,54 +433,39 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     const int *const table = p.table + (size_t)b * p.table_width;
     const int halves = (len + 15) >> 4, per_page = p.page >> 4;
     auto page_index = [&](int half) -> int { return p.page_magic ? (int)__umulhi((unsigned)half, p.page_magic) : half; };
-    // page of a half (-1: past the end, or no such page)
-    auto page_of = [&](int run, int h) -> int {
-        if (run >= run1 || 2 * run + h >= halves) return -1;
-        const int id = table[page_index(2 * run + h)];
+    // lane h < 2 looks after half h of every run: its page (-1: past the end, or no such page) ...
+    auto page_of = [&](int run) -> int {
+        if (lane >= 2 || run >= run1 || 2 * run + lane >= halves) return -1;
+        const int id = table[page_index(2 * run + lane)];
         return (unsigned)id < (unsigned)p.n_pages ? id : -1;
     };
-    // {key, value} scales of the runs in flight, read with their copies
-    float2 held[STAGES][2];
-    auto copy = [&](int run, const int (&id)[2], int stage, float2 (&sc)[2]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const size_t at = (size_t)max(id[h], 0) * p.Hkv + hk;
-            sc[h] = id[h] >= 0 ? make_float2(__ldg(p.ks + at), __ldg(p.vs + at)) : make_float2(pow2(SCALE_MIN), pow2(SCALE_MIN));
-        }
-        if (lane != 0 || run >= run1) return;
-        const uint32_t bar = bars + 8u * stage, d = ring + (uint32_t)stage * STAGE_BYTES;
-        const int y0 = (max(id[0], 0) * p.Hkv + hk) * p.page + (2 * run - page_index(2 * run) * per_page) * 16;
-        if (p.box == 32) {  // (both halves are in one page; the second may lie past the end)
-            mbar_arrive_expect_tx(bar, id[0] >= 0 ? 4 * HALF_BYTES : 0);
-            if (id[0] >= 0) {
-                tma_load_2d(d, &p.tm_k, bar, 0, y0);
-                tma_load_2d(d + 2 * HALF_BYTES, &p.tm_v, bar, 0, y0);
-            }
-        } else {
-            mbar_arrive_expect_tx(bar, (id[0] >= 0 ? 2 * HALF_BYTES : 0) + (id[1] >= 0 ? 2 * HALF_BYTES : 0));
-            if (id[0] >= 0) {
-                tma_load_2d(d, &p.tm_k, bar, 0, y0);
-                tma_load_2d(d + 2 * HALF_BYTES, &p.tm_v, bar, 0, y0);
-            }
-            if (id[1] >= 0) {
-                const int y1 = (id[1] * p.Hkv + hk) * p.page + (2 * run + 1 - page_index(2 * run + 1) * per_page) * 16;
-                tma_load_2d(d + HALF_BYTES, &p.tm_k, bar, 0, y1);
-                tma_load_2d(d + 3 * HALF_BYTES, &p.tm_v, bar, 0, y1);
+    // ... and its copy; returns its {key, value} scales (0: hidden)
+    auto copy = [&](int run, int id, int stage) -> float2 {
+        float2 sc = make_float2(0.f, 0.f);
+        if (lane < 2 && run < run1) {
+            const uint32_t bar = bars + 8u * stage, d = ring + (uint32_t)(stage * STAGE_BYTES + lane * HALF_BYTES);
+            if (id >= 0) {
+                const int at = id * p.Hkv + hk, half = 2 * run + lane;
+                const int y = at * p.page + (half - page_index(half) * per_page) * 16;
+                mbar_arrive_expect_tx(bar, 2 * HALF_BYTES);
+                tma_load_2d(d, &p.tm_k, bar, 0, y);
+                tma_load_2d(d + 2 * HALF_BYTES, &p.tm_v, bar, 0, y);
+                sc = make_float2(__ldg(p.ks + at), __ldg(p.vs + at));
+            } else {
+                mbar_arrive(bar);
             }
         }
+        return sc;
     };
-    // pages of the halves of the run being worked on, of those in flight, and of the one after
-    int ids[STAGES + 1][2];
+    float2 held[STAGES];  // scales of the runs in flight, the one being worked on first
+    int id_next;          // page of the run after them
 #pragma unroll
-    for (int s = 0; s <= STAGES; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) ids[s][h] = page_of(run0 + warp + s * WARPS, h);
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) copy(run0 + warp + s * WARPS, ids[s], s, held[s]);
+    for (int s = 0; s < STAGES; ++s) held[s] = copy(run0 + warp + s * WARPS, page_of(run0 + warp + s * WARPS), s);
+    id_next = page_of(run0 + warp + STAGES * WARPS);
 
-    // query fragments: column gr of each column tile, channels 32 c .. 32 c + 31 of it in this
-    // lane; word w (channels 32 c + 4 w ..) belongs to product w / 2.  hi + lo is the channel.
-    uint32_t hi[NT][8], lo[NT][8];
+    // query fragments: column gr of each column tile; product w takes channels 32 c + 4 w
+    // .. 32 c + 4 w + 3 of this lane
+    uint32_t bq[NT][8][2];
     float unit_of[NT];  // power of two of the column's scaling, times the softmax scale
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -502,14 +493,12 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // 2^e with amax in [2^e, 2^(e + 1))
         const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -120), 120);
-        const float up = pow2(min(7 - e, 127));
-        unit_of[nt] = pow2(e - 6) * (0.5f * p.scale);
+        const float inv = pow2(-e);
+        unit_of[nt] = pow2(e) * p.scale;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            const float4 v = make_float4(x[4 * w] * up, x[4 * w + 1] * up, x[4 * w + 2] * up, x[4 * w + 3] * up);
-            hi[nt][w] = pack_e4m3x4(v);
-            const float4 h = unpack_e4m3x4(hi[nt][w]);
-            lo[nt][w] = pack_e4m3x4(make_float4(v.x - h.x, v.y - h.y, v.z - h.z, v.w - h.w));
+            bq[nt][w][0] = pack_f16x2(x[4 * w] * inv, x[4 * w + 1] * inv);
+            bq[nt][w][1] = pack_f16x2(x[4 * w + 2] * inv, x[4 * w + 3] * inv);
         }
     }
     // this thread's rows: columns 2 c and 2 c + 1 (a row and its tangent, or two rows)
@@ -536,6 +525,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
 
     float acc[NT][8][4];  // channels 16 gr + 2 j + {0, 1} (pairs of elements), columns 2 c + {0, 1}
     float m[NT][R], l[NT][R], g[NT], r0[NT];
+    int ew[NT];  // T is in units of 2^ew
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -548,40 +538,54 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             l[nt][i] = 0.f;
         }
         g[nt] = r0[nt] = 0.f;
+        ew[nt] = EW_MIN;
     }
-    int E = SCALE_MIN;
     bool begun = false;
 
     int stage = 0;
     uint32_t phase = 0;
     for (int run = run0 + warp; run < run1; run += WARPS) {
         if (!mbar_wait_warp(bars + 8u * stage, phase, abort_flag, p.bound_ns)) break;
-        const bool valid[2] = {ids[0][0] >= 0, ids[0][1] >= 0};  // (a half without a page is hidden)
         const uint32_t d = ring + (uint32_t)stage * STAGE_BYTES;
-        const float kscale[2] = {held[0][0].x, held[0][1].x}, vscale[2] = {held[0][0].y, held[0][1].y};
+        float kscale[2], vscale[2];
+        bool valid[2];  // (a half without a page is hidden)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            kscale[h] = __shfl_sync(0xffffffffu, held[0].x, h);
+            vscale[h] = __shfl_sync(0xffffffffu, held[0].y, h);
+            valid[h] = kscale[h] != 0.f;
+        }
 
-        // S^T of tokens gr (elements 0, 1) and gr + 8 (2, 3) of each half; two chains of four products
+        // S^T of tokens gr (elements 0, 1) and gr + 8 (2, 3) of each half; two chains of four
+        // products each
         float S[2][NT][4], S2[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[h][nt][i] = S2[h][nt][i] = 0.f;
             // 16-byte units 2 c, 2 c + 1 of rows gr and gr + 8 (unit u of row r at u ^ (r & 7))
             const uint32_t dh = d + (uint32_t)(h * HALF_BYTES + gr * HD);
             const uint32_t u0 = (uint32_t)((2 * c) ^ gr) * 16u, u1 = (uint32_t)((2 * c + 1) ^ gr) * 16u;
             const uint4 x0 = ld_shared_u4(dh + u0), x1 = ld_shared_u4(dh + u1);
             const uint4 y0 = ld_shared_u4(dh + 8 * HD + u0), y1 = ld_shared_u4(dh + 8 * HD + u1);
-            const uint32_t a[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            const uint32_t a8[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+            const uint32_t lo[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            const uint32_t up[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-            for (int s = 0; s < 8; s += 2)
+            for (int w = 0; w < 4; ++w) {
+                uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+                e4m3x4_to_f16x2(lo[w], a0, a2);
+                e4m3x4_to_f16x2(up[w], a1, a3);
+                e4m3x4_to_f16x2(lo[4 + w], b0, b2);
+                e4m3x4_to_f16x2(up[4 + w], b1, b3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_e4m3(S[h][nt], a[s], a8[s], a[s + 1], a8[s + 1], hi[nt][s], hi[nt][s + 1]);
-                    mma_e4m3(S2[h][nt], a[s], a8[s], a[s + 1], a8[s + 1], lo[nt][s], lo[nt][s + 1]);
+                    if (w == 0) {
+                        mma_f16_first(S[h][nt], a0, a1, a2, a3, bq[nt][w][0], bq[nt][w][1]);
+                        mma_f16_first(S2[h][nt], b0, b1, b2, b3, bq[nt][4 + w][0], bq[nt][4 + w][1]);
+                    } else {
+                        mma_f16(S[h][nt], a0, a1, a2, a3, bq[nt][w][0], bq[nt][w][1]);
+                        mma_f16(S2[h][nt], b0, b1, b2, b3, bq[nt][4 + w][0], bq[nt][4 + w][1]);
+                    }
                 }
+            }
         }
         // log2-unit scores y of this thread's rows at keys run * 32 + 16 h + gr + {0, 8}
         float y[2][NT][R][2], dS[2][NT][2];
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                                 if constexpr (kTan) dS[h][nt][e] = 0.f;  // (codes past the end may be NaN)
                             }
         }
-        // running references of y + log2(value scale): raised when a weight would pass 2^8
+        // running references: weights 2^(y + ev - m), the largest 2^7 when set, at most 2^8.75 = 430
         const float ev[2] = {(float)exponent_of(vscale[0]), (float)exponent_of(vscale[1])};
         bool need = false;
         float top[NT][R];
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 top[nt][i] = fmaxf(fmaxf(y[0][nt][i][0], y[0][nt][i][1]) + ev[0], fmaxf(y[1][nt][i][0], y[1][nt][i][1]) + ev[1]);
-                need |= top[nt][i] > m[nt][i] + 8.f;
+                need |= top[nt][i] > m[nt][i] + 8.75f;
             }
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                 float alpha[R];
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const float mx = column_max(top[nt][i]);
+                    const float mx = column_max(top[nt][i]) - 7.f;
                     alpha[i] = 1.f;
                     if (mx > m[nt][i]) {
                         alpha[i] = ex2_approx(m[nt][i] - mx);
@@ -673,23 +677,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                     for (int i = 0; i < 4; ++i) acc[nt][j][i] *= alpha[kTan ? 0 : (i & 1)];
             }
         }
-        if constexpr (kTan) {
-            const int ek = max(exponent_of(kscale[0]), exponent_of(kscale[1]));
-            if (ek > E) {  // a larger key scale: T moves to it
-                const float r = pow2_or_0(E - ek);
-                E = ek;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        acc[nt][j][1] *= r;
-                        acc[nt][j][3] *= r;
-                    }
-            }
-        }
-        const float rel = kTan ? pow2(-E - 18) : 0.f;
-        uint32_t bp[2][NT][2];  // P^T: tokens 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of column gr
-        float pe[2][NT][R][2];
+        float pe[2][NT][R][2];  // exp2(y - m)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -718,23 +706,64 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             }
             begun = true;
         }
+        float wt[2][NT][2][2];  // the columns of P^T: [half][][column 2 c + i][token gr + 8 e]
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float p0 = pe[h][nt][0][e] * vscale[h];
-                    float p1;
+                    wt[h][nt][0][e] = pe[h][nt][0][e] * vscale[h];
                     if constexpr (kTan) {
                         const float dc = dS[h][nt][e] - r0[nt];
                         g[nt] = fmaf(pe[h][nt][0][e], dc, g[nt]);
-                        p1 = p0 * (dc * rel);
+                        wt[h][nt][1][e] = wt[h][nt][0][e] * dc;
                     } else {
-                        p1 = pe[h][nt][R - 1][e] * vscale[h];
+                        wt[h][nt][1][e] = pe[h][nt][R - 1][e] * vscale[h];
                     }
-                    bp[h][nt][e] = transpose_8x8(pack_f16x2(p0, p1));
                 }
+        if constexpr (kTan) {  // P dS in units of 2^ew, at most 448 of them
+            float most[NT];
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                most[nt] = fmaxf(fmaxf(fabsf(wt[0][nt][1][0]), fabsf(wt[0][nt][1][1])),
+                                 fmaxf(fabsf(wt[1][nt][1][0]), fabsf(wt[1][nt][1][1])));
+                over |= most[nt] > 448.f * pow2(ew[nt]);
+            }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float mx = column_max(most[nt]);
+                    const int e = binary_exponent(mx) - 7;  // mx in [2^7, 2^8) units
+                    if (e > ew[nt]) {
+                        const float r = pow2_or_0(ew[nt] - e);
+                        ew[nt] = e;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            acc[nt][j][1] *= r;
+                            acc[nt][j][3] *= r;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float to_units = pow2(-ew[nt]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) wt[h][nt][1][e] *= to_units;
+            }
+        }
+        uint32_t bp[2][NT][2];  // P^T: tokens 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of column gr
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    bp[h][nt][e] = transpose_8x8(pack_f16x2(wt[h][nt][0][e], wt[h][nt][1][e]));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             // values of tokens 2c, 2c + 1, 2c + 8, 2c + 9, channels 16 gr .. 16 gr + 15; tokens past
@@ -771,16 +800,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         // this stage is free again: the run STAGES further on
         __syncwarp();
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) held[s][h] = held[s + 1][h];
-        copy(run + STAGES * WARPS, ids[STAGES], stage, held[STAGES - 1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int s = 0; s < STAGES; ++s) ids[s][h] = ids[s + 1][h];
-            ids[STAGES][h] = page_of(run + (STAGES + 1) * WARPS, h);
-        }
+        for (int s = 0; s < STAGES - 1; ++s) held[s] = held[s + 1];
+        held[STAGES - 1] = copy(run + STAGES * WARPS, id_next, stage);
+        id_next = page_of(run + (STAGES + 1) * WARPS);
         if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -817,27 +839,30 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             if constexpr (kTan) {
                 stats[ST_G + nt * 4 + c] = g[nt];
                 stats[ST_R + nt * 4 + c] = r0[nt];
+                reinterpret_cast<int *>(stats)[ST_E + nt * 4 + c] = ew[nt];
                 if (warp == 0) cst[ST_UNIT + nt * 4 + c] = unit_t[nt];
             }
         }
     }
-    if (lane == 0) reinterpret_cast<int *>(stats)[ST_E] = E;
     __syncthreads();
     // the CTA's sums, in warp order, into warp 0's ring; its statistics into cst.
     // T and g of different r: sum p (dS - R) V = sum p (dS - r) V + (r - R) sum p V
     const float *const st = reinterpret_cast<const float *>(smem + STATS_OFF);
-    int Ec = SCALE_MIN;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) Ec = max(Ec, reinterpret_cast<const int *>(st + ST_FLOATS * w)[ST_E]);
     for (int x = threadIdx.x; x < ROWS * HD / 4; x += THREADS) {
         const int row = x / (HD / 4), d4 = x % (HD / 4);
         float top = -INFINITY, Rc = 0.f;
+        int Ec = EW_MIN;  // the largest unit, and none that r - R would overflow in
 #pragma unroll
         for (int w = 0; w < WARPS; ++w)
             if (st[ST_FLOATS * w + ST_M + row] > top) {
                 top = st[ST_FLOATS * w + ST_M + row];
                 if (kTan) Rc = st[ST_FLOATS * w + ST_R + row];
             }
+        if constexpr (kTan)
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+                Ec = max(Ec, max(reinterpret_cast<const int *>(st + ST_FLOATS * w)[ST_E + row],
+                                 binary_exponent(st[ST_FLOATS * w + ST_R + row] - Rc)));
         float4 so = make_float4(0.f, 0.f, 0.f, 0.f), sT = so;
         float lt = 0.f, gt = 0.f;
         const int oc = (kTan ? 2 * row : row) * HD + 4 * d4;
@@ -852,9 +877,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             if constexpr (kTan) {
                 const float dr = sw[ST_R + row] - Rc;
                 gt = fmaf(f, fmaf(dr, sw[ST_L + row], sw[ST_G + row]), gt);
-                axpy(sT, f * pow2_or_0(reinterpret_cast<const int *>(sw)[ST_E] - Ec),
+                axpy(sT, f * pow2_or_0(reinterpret_cast<const int *>(sw)[ST_E + row] - Ec),
                      *reinterpret_cast<const float4 *>(vw + oc + HD));
-                axpy(sT, f * dr * pow2(-Ec - 18), v);
+                axpy(sT, f * (dr * pow2(-Ec)), v);
             }
         }
         // (each place of warp 0's ring is read and written by this thread alone)
@@ -866,9 +891,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             if constexpr (kTan) {
                 cst[ST_G + row] = gt;
                 cst[ST_R + row] = Rc;
+                reinterpret_cast<int *>(cst)[ST_E + row] = Ec;
             }
         }
-        if (x == 0) reinterpret_cast<int *>(cst)[ST_E] = Ec;
     }
     auto cluster_sync = [&]() {
         if (p.splits > 1)
@@ -877,42 +902,52 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             __syncthreads();
     };
     cluster_sync();
-    // the cluster's sums, in rank order: the ranks share out the tile's rows x channels.  All
-    // ranks' statistics first, by independent loads, into memory that the rings no longer need
+    // The cluster's sums: the ranks share out the tile's rows x channels.  Each fetches all
+    // ranks' statistics and its part of their sums by independent loads, into memory that the
+    // rings no longer need, and adds them up in rank order.
+    constexpr int KINDS = kTan ? 2 : 1;                  // O, T
+    const int part = ROWS * (HD / 4) / p.splits;         // float4 places of a rank (splits divide 16)
     float *const ast = reinterpret_cast<float *>(smem + RING_BYTES);
+    float4 *const sums = reinterpret_cast<float4 *>(smem + RING_BYTES + 16 * ST_FLOATS * 4);  // [rank][kind][part]
     for (int i = threadIdx.x; i < p.splits * ST_FLOATS; i += THREADS)
         ast[i] = ld_cluster(cluster_map(sbase + STATS_OFF + (WARPS * ST_FLOATS + (i & (ST_FLOATS - 1))) * 4u,
                                         (uint32_t)(i / ST_FLOATS)));
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.splits * KINDS * part; i += THREADS) {
+        const int s = i / (KINDS * part), k = i / part % KINDS, x = rank * part + i % part;
+        const int row = x / (HD / 4), d4 = x % (HD / 4);
+        sums[i] = ld_cluster4(cluster_map(sbase, (uint32_t)s) + (uint32_t)((KINDS * row + k) * HD + 4 * d4) * 4u);
+    }
     __syncthreads();
-    for (int x = rank * THREADS + (int)threadIdx.x; x < ROWS * HD / 4; x += p.splits * THREADS) {
-        const int row = x / (HD / 4), d4 = x % (HD / 4), r = tile * ROWS + row;
+    for (int i = threadIdx.x; i < part; i += THREADS) {
+        const int x = rank * part + i, row = x / (HD / 4), d4 = x % (HD / 4), r = tile * ROWS + row;
         if (r >= n_rows) continue;
         float top = -INFINITY, Rt = 0.f;
-        int Et = SCALE_MIN;
+        int Et = EW_MIN;
         for (int s = 0; s < p.splits; ++s) {
             const float *const a = ast + s * ST_FLOATS;
             if (a[ST_M + row] > top) {
                 top = a[ST_M + row];
                 if (kTan) Rt = a[ST_R + row];
             }
-            if (kTan) Et = max(Et, __float_as_int(a[ST_E]));
         }
+        if constexpr (kTan)
+            for (int s = 0; s < p.splits; ++s)
+                Et = max(Et, max(__float_as_int(ast[s * ST_FLOATS + ST_E + row]),
+                                 binary_exponent(ast[s * ST_FLOATS + ST_R + row] - Rt)));
         float4 so = make_float4(0.f, 0.f, 0.f, 0.f), sT = so;
         float lt = 0.f, gt = 0.f;
-        const uint32_t oc = (uint32_t)((kTan ? 2 * row : row) * HD + 4 * d4) * 4u;
-#pragma unroll 4
         for (int s = 0; s < p.splits; ++s) {
             const float *const a = ast + s * ST_FLOATS;
-            const uint32_t v = cluster_map(sbase, (uint32_t)s) + oc;
             const float f = ref_weight(a[ST_M + row], top);
-            const float4 o4 = ld_cluster4(v);
+            const float4 o4 = sums[s * KINDS * part + i];
             lt = fmaf(f, a[ST_L + row], lt);
             axpy(so, f, o4);
             if constexpr (kTan) {
                 const float dr = a[ST_R + row] - Rt;
                 gt = fmaf(f, fmaf(dr, a[ST_L + row], a[ST_G + row]), gt);
-                axpy(sT, f * pow2_or_0(__float_as_int(a[ST_E]) - Et), ld_cluster4(v + HD * 4u));
-                axpy(sT, f * dr * pow2(-Et - 18), o4);
+                axpy(sT, f * pow2_or_0(__float_as_int(a[ST_E + row]) - Et), sums[(s * KINDS + 1) * part + i]);
+                axpy(sT, f * (dr * pow2(-Et)), o4);
             }
         }
         const float inv = lt > 0.f ? 1.f / lt : 0.f;  // a row that sees no key: zeros, lse = -infinity
@@ -921,8 +956,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         const size_t out = (size_t)(p.o_b * b + p.o_h * h + first + t);
         *reinterpret_cast<uint2 *>(p.o + out * HD + 4 * d4) = make_uint2(pack_bf16x2(ov.x, ov.y), pack_bf16x2(ov.z, ov.w));
         if constexpr (kTan) {
-            // T is in units of 2^(E + 18), and like g relative to r and in the tangent row's units
-            const float mu = gt * inv, in = pow2(Et + 18) * inv, unit = cst[ST_UNIT + row];
+            // T is in units of 2^E, and like g relative to r and in the tangent row's units
+            const float mu = gt * inv, in = pow2(Et) * inv, unit = cst[ST_UNIT + row];
             *reinterpret_cast<uint2 *>(p.to + out * HD + 4 * d4) =
                 make_uint2(pack_bf16x2(unit * fmaf(-mu, ov.x, sT.x * in), unit * fmaf(-mu, ov.y, sT.y * in)),
                            pack_bf16x2(unit * fmaf(-mu, ov.z, sT.z * in), unit * fmaf(-mu, ov.w, sT.w * in)));
