@@ -138,8 +138,12 @@ int attn_jvp_cache_append(const void *k, const void *v, const void *q, const voi
                           (const void *)cache_lens, (const void *)cu_seqlens})
         if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
     const int64_t slots = total / page + 2 * std::min(n_seq, total);  // a sequence's first and last pages may be partial
-    const int64_t chunks = (total + cache::ROWS_PER_CTA - 1) / cache::ROWS_PER_CTA;
-    const int64_t grid = slots * Hkv + (q ? chunks * H : 0);
+    const int64_t chunks = (total + cache::APPEND_WARPS - 1) / cache::APPEND_WARPS;
+    // a warp per (page, head) while the sequences bring no more tokens on average than a warp holds
+    const bool by_warp = total <= cache::HELD * n_seq;
+    const int64_t page_ctas = by_warp ? (slots * Hkv + cache::APPEND_WARPS - 1) / cache::APPEND_WARPS : slots * Hkv;
+    const int64_t grid = page_ctas + (q ? chunks * ((H + cache::HEADS_PER_WARP - 1) / cache::HEADS_PER_WARP) : 0);
+    if (slots * Hkv >= kMaxInt) return AJVP_ERR_TOO_LARGE;
     if (grid >= kMaxInt) return AJVP_ERR_TOO_LARGE;
     int dev = 0;
     if ((rc = setup(&dev)) != AJVP_OK) return rc;
@@ -168,9 +172,12 @@ int attn_jvp_cache_append(const void *k, const void *v, const void *q, const voi
     p.page = (int)page;
     p.table_width = (int)table_width;
     p.n_pos = (int)n_pos;
-    p.interleaved = interleaved != 0;
     p.n_slots = (int)slots;
-    cache::cache_append_kernel<<<(unsigned)grid, cache::APPEND_THREADS, 0, (cudaStream_t)stream>>>(p);
+    using namespace ajvp::cache;
+    auto *const kernel = !cos ? (by_warp ? cache_append_kernel<true, ROT_NONE> : cache_append_kernel<false, ROT_NONE>)
+                         : interleaved ? (by_warp ? cache_append_kernel<true, ROT_PAIRS> : cache_append_kernel<false, ROT_PAIRS>)
+                                       : (by_warp ? cache_append_kernel<true, ROT_HALVES> : cache_append_kernel<false, ROT_HALVES>);
+    kernel<<<(unsigned)grid, APPEND_THREADS, 0, (cudaStream_t)stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? AJVP_OK : host::fail(e);
 }

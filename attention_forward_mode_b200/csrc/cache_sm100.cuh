@@ -62,44 +62,59 @@ struct AppendParams {
     const int *lens;               // [n_seq] tokens already cached
     const int *cu;                 // [n_seq + 1]
     const float *cos, *sin;        // [n_pos][64] by token position, or NULL: no rotation
-    int n_seq, H, Hkv, total, n_pages, page, table_width, n_pos, interleaved;
+    int n_seq, H, Hkv, total, n_pages, page, table_width, n_pos;
     int n_slots;                   // page CTAs per key head (an upper bound of the touched pages)
 };
 
 constexpr int APPEND_THREADS = 256, APPEND_WARPS = APPEND_THREADS / 32;
-constexpr int ROWS_PER_CTA = 32;  // query rows per CTA
+constexpr int HELD = 4;               // tokens of a page that a warp keeps in registers
+constexpr int HEADS_PER_WARP = 4;     // query heads that share one reading of a row's angles
 
-// Four channels of a row (lane l: 4l .. 4l + 3) turned by the angles of the
-// row's position.  Products and sums are rounded one by one (no fused
-// multiply-add), so that the result, and with it the scale, is that of the
-// formula evaluated step by step in fp32.
-__device__ __forceinline__ float4 rotate(const AppendParams &p, float4 x, int pos, int lane) {
+constexpr int ROT_NONE = 0, ROT_HALVES = 1, ROT_PAIRS = 2;
+// The angles of a position for a lane's four channels (lane l: 4l .. 4l + 3).
+struct Angles {
+    float4 c, s;
+};
+template <int ROT>
+__device__ __forceinline__ Angles angles_of(const AppendParams &p, int pos, int lane) {
     const size_t at = (size_t)min(max(pos, 0), p.n_pos - 1) * (HD / 2);
-    if (p.interleaved) {  // pairs (4l, 4l + 1), (4l + 2, 4l + 3): angles 2l, 2l + 1
+    Angles a;
+    if constexpr (ROT == ROT_PAIRS) {  // pairs (4l, 4l + 1), (4l + 2, 4l + 3): angles 2l, 2l + 1
         const float2 c = *reinterpret_cast<const float2 *>(p.cos + at + 2 * lane);
         const float2 s = *reinterpret_cast<const float2 *>(p.sin + at + 2 * lane);
-        return make_float4(__fsub_rn(__fmul_rn(x.x, c.x), __fmul_rn(x.y, s.x)),
-                           __fadd_rn(__fmul_rn(x.y, c.x), __fmul_rn(x.x, s.x)),
-                           __fsub_rn(__fmul_rn(x.z, c.y), __fmul_rn(x.w, s.y)),
-                           __fadd_rn(__fmul_rn(x.w, c.y), __fmul_rn(x.z, s.y)));
+        a.c = make_float4(c.x, c.x, c.y, c.y);
+        a.s = make_float4(-s.x, s.x, -s.y, s.y);
+    } else {  // pairs (i, i + 64): lane l's partner channels are lane l ^ 16's
+        a.c = *reinterpret_cast<const float4 *>(p.cos + at + 4 * (lane & 15));
+        a.s = *reinterpret_cast<const float4 *>(p.sin + at + 4 * (lane & 15));
+        if (lane < 16) a.s = make_float4(-a.s.x, -a.s.y, -a.s.z, -a.s.w);
     }
-    // pairs (i, i + 64): lane l's partner channels are lane l ^ 16's
-    const float4 c = *reinterpret_cast<const float4 *>(p.cos + at + 4 * (lane & 15));
-    const float4 s = *reinterpret_cast<const float4 *>(p.sin + at + 4 * (lane & 15));
-    const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, 16), __shfl_xor_sync(0xffffffffu, x.y, 16),
-                                 __shfl_xor_sync(0xffffffffu, x.z, 16), __shfl_xor_sync(0xffffffffu, x.w, 16));
-    const float sign = lane < 16 ? -1.f : 1.f;  // first halves a cos - b sin, second halves b cos + a sin
-    return make_float4(__fadd_rn(__fmul_rn(x.x, c.x), sign * __fmul_rn(y.x, s.x)),
-                       __fadd_rn(__fmul_rn(x.y, c.y), sign * __fmul_rn(y.y, s.y)),
-                       __fadd_rn(__fmul_rn(x.z, c.z), sign * __fmul_rn(y.z, s.z)),
-                       __fadd_rn(__fmul_rn(x.w, c.w), sign * __fmul_rn(y.w, s.w)));
+    return a;
+}
+// x cos + partner (-+ sin).  Products and sums are rounded one by one (no fused
+// multiply-add), so that the result, and with it the scale, is that of the
+// formula evaluated step by step in fp32.
+template <int ROT>
+__device__ __forceinline__ float4 rotate(float4 x, const Angles &a) {
+    float4 y;
+    if constexpr (ROT == ROT_PAIRS)
+        y = make_float4(x.y, x.x, x.w, x.z);
+    else
+        y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, 16), __shfl_xor_sync(0xffffffffu, x.y, 16),
+                        __shfl_xor_sync(0xffffffffu, x.z, 16), __shfl_xor_sync(0xffffffffu, x.w, 16));
+    return make_float4(__fadd_rn(__fmul_rn(x.x, a.c.x), __fmul_rn(y.x, a.s.x)),
+                       __fadd_rn(__fmul_rn(x.y, a.c.y), __fmul_rn(y.y, a.s.y)),
+                       __fadd_rn(__fmul_rn(x.z, a.c.z), __fmul_rn(y.z, a.s.z)),
+                       __fadd_rn(__fmul_rn(x.w, a.c.w), __fmul_rn(y.w, a.s.w)));
 }
 
-__device__ __forceinline__ float4 load_bf16x4(const __nv_bfloat16 *row, int lane) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(row + 4 * lane);
+__device__ __forceinline__ float4 bf16x4(uint2 u) {
     const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
     const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
     return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ uint2 raw_bf16x4(const __nv_bfloat16 *row, int lane) {
+    return *reinterpret_cast<const uint2 *>(row + 4 * lane);
 }
 __device__ __forceinline__ float amax4(float m, float4 x) {
     return fmaxf(fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
@@ -111,41 +126,59 @@ __device__ __forceinline__ int2 new_rows(const AppendParams &p, int b) {
     return make_int2(r0, max(min(max(p.cu[b + 1], 0), p.total), r0));
 }
 
-// One CTA per (touched page, key head), both caches: the new tokens' largest
-// value (rotated keys), the page's new scale, codes of its earlier tokens moved
-// to that scale when it grew, then the new codes.  The page is one CTA's own, so
-// nothing is atomic.  CTAs past the page slots rotate q and tq, ROWS_PER_CTA
-// rows of a head each.  Bound by its bytes (keys and values read twice, the
-// second time from L1/L2).
-static __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(const __grid_constant__ AppendParams p) {
+// A (touched page, key head), both caches: the new tokens' largest value (rotated
+// keys), the page's new scale, codes of its earlier tokens moved to that scale when
+// it grew, then the new codes.  It is one CTA's own, or one warp's (kWarp: a few
+// tokens per sequence, where a CTA's other warps would idle: 64 sequences of one
+// token 14 against 4.5 us), so nothing is atomic; each warp's first HELD tokens stay in
+// registers between the maximum and the codes, the rest are read again from L1/L2.
+// CTAs past the page slots rotate q and tq: a warp takes one row of HEADS_PER_WARP
+// heads, so that the row's angles, as many bytes as two heads' channels, are read
+// once for them.  Bound by its bytes.
+template <bool kWarp, int ROT>
+__global__ void __launch_bounds__(APPEND_THREADS, 4) cache_append_kernel(const __grid_constant__ AppendParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_page_ctas = p.n_slots * p.Hkv;
-    if ((int)blockIdx.x >= n_page_ctas) {
-        const int chunks = (p.total + ROWS_PER_CTA - 1) / ROWS_PER_CTA;
-        const int u = (int)blockIdx.x - n_page_ctas, h = u / chunks, row0 = (u - h * chunks) * ROWS_PER_CTA;
-        for (int row = row0 + warp; row < min(row0 + ROWS_PER_CTA, p.total); row += APPEND_WARPS) {
-            int lo = 0, hi = p.n_seq;  // the last sequence that starts at or before the row
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (p.cu[mid] <= row) lo = mid; else hi = mid;
-            }
-            const int2 rows = new_rows(p, lo);
-            if (row < rows.x || row >= rows.y) continue;  // behind the last sequence: not written
-            const int pos = max(p.lens[lo], 0) + row - rows.x;
-            const size_t off = ((size_t)h * p.total + row) * HD;
-            const float4 x = rotate(p, load_bf16x4(p.q + off, lane), pos, lane);
-            uint2 w = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-            *reinterpret_cast<uint2 *>(p.q_out + off + 4 * lane) = w;
+    const int n_page_ctas = kWarp ? (p.n_slots * p.Hkv + APPEND_WARPS - 1) / APPEND_WARPS : p.n_slots * p.Hkv;
+    if (ROT != ROT_NONE && (int)blockIdx.x >= n_page_ctas) {
+        const int chunks = (p.total + APPEND_WARPS - 1) / APPEND_WARPS;
+        const int u = (int)blockIdx.x - n_page_ctas, h0 = u / chunks * HEADS_PER_WARP;
+        const int row = (u % chunks) * APPEND_WARPS + warp;
+        if (row >= p.total) return;
+        uint2 x[HEADS_PER_WARP], t[HEADS_PER_WARP];
+#pragma unroll
+        for (int i = 0; i < HEADS_PER_WARP; ++i) {
+            const size_t off = ((size_t)min(h0 + i, p.H - 1) * p.total + row) * HD;
+            x[i] = raw_bf16x4(p.q + off, lane);
+            t[i] = p.tq ? raw_bf16x4(p.tq + off, lane) : make_uint2(0u, 0u);
+        }
+        int lo = 0, hi = p.n_seq;  // the last sequence that starts at or before the row: among 32 by a vote
+        while (hi - lo > 32) {
+            const int mid = (lo + hi) >> 1;
+            if (p.cu[mid] <= row) lo = mid; else hi = mid;
+        }
+        const unsigned started = __ballot_sync(0xffffffffu, lo + lane < hi && p.cu[lo + lane] <= row);
+        lo += started ? 31 - __clz(started) : 0;
+        const int2 rows = new_rows(p, lo);
+        if (row < rows.x || row >= rows.y) return;  // behind the last sequence: not written
+        const Angles a = angles_of<ROT>(p, max(p.lens[lo], 0) + row - rows.x, lane);
+#pragma unroll
+        for (int i = 0; i < HEADS_PER_WARP; ++i) {
+            if (h0 + i >= p.H) break;
+            const size_t off = ((size_t)(h0 + i) * p.total + row) * HD + 4 * lane;
+            const float4 y = rotate<ROT>(bf16x4(x[i]), a);
+            *reinterpret_cast<uint2 *>(p.q_out + off) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
             if (p.tq) {
-                const float4 t = rotate(p, load_bf16x4(p.tq + off, lane), pos, lane);
-                w = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
-                *reinterpret_cast<uint2 *>(p.tq_out + off + 4 * lane) = w;
+                const float4 z = rotate<ROT>(bf16x4(t[i]), a);
+                *reinterpret_cast<uint2 *>(p.tq_out + off) = make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
             }
         }
         return;
     }
     // the slot'th touched page over all sequences, counted by every warp for itself
-    const int slot = (int)blockIdx.x / p.Hkv, hk = (int)blockIdx.x - slot * p.Hkv;
+    const int unit = kWarp ? (int)blockIdx.x * APPEND_WARPS + warp : (int)blockIdx.x;
+    const int slot = unit / p.Hkv, hk = unit - slot * p.Hkv;
+    constexpr int STRIDE = kWarp ? 1 : APPEND_WARPS;  // tokens: every STRIDE'th from t0
+    const int t0 = kWarp ? 0 : warp;
     int before = 0, b = -1, nth = 0;
     for (int b0 = 0; b0 < p.n_seq && b < 0; b0 += 32) {
         int pages = 0;
@@ -168,7 +201,7 @@ static __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(con
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (b < 0) return;  // past the last touched page (the same for the whole CTA)
+    if (b < 0) return;  // past the last touched page (the same for the whole unit)
     const int2 rows = new_rows(p, b);
     const int start = max(p.lens[b], 0), at = start / p.page + nth;
     if (at >= p.table_width) return;  // past the sequence's pages: not written
@@ -181,42 +214,65 @@ static __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(con
     const int first = rows.x + (int)(page0 + kept - start);
     const __nv_bfloat16 *const krow = p.k + ((size_t)hk * p.total + first) * HD;
     const __nv_bfloat16 *const vrow = p.v + ((size_t)hk * p.total + first) * HD;
-    const bool turn = p.cos != nullptr;
 
+    // this warp's tokens: kept + t0 + STRIDE i
+    auto key = [&](int t) -> float4 {
+        const float4 x = bf16x4(raw_bf16x4(krow + (size_t)(t - kept) * HD, lane));
+        if constexpr (ROT == ROT_NONE)
+            return x;
+        else
+            return rotate<ROT>(x, angles_of<ROT>(p, (int)(page0 + t), lane));
+    };
+    auto value = [&](int t) -> uint2 { return raw_bf16x4(vrow + (size_t)(t - kept) * HD, lane); };
     float ka = 0.f, va = 0.f;
-    for (int t = kept + warp; t < last; t += APPEND_WARPS) {
-        float4 x = load_bf16x4(krow + (size_t)(t - kept) * HD, lane);
-        if (turn) x = rotate(p, x, (int)(page0 + t), lane);
-        ka = amax4(ka, x);
-        va = amax4(va, load_bf16x4(vrow + (size_t)(t - kept) * HD, lane));
+    float4 kh[HELD];
+    uint2 vh[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {  // (past the end: the last token once more, so that all loads are under way at once)
+        const int t = min(kept + t0 + STRIDE * i, last - 1);
+        kh[i] = key(t);
+        vh[i] = value(t);
+    }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        ka = amax4(ka, kh[i]);
+        va = amax4(va, bf16x4(vh[i]));
+    }
+    for (int t = kept + t0 + STRIDE * HELD; t < last; t += STRIDE) {
+        ka = amax4(ka, key(t));
+        va = amax4(va, bf16x4(value(t)));
     }
     // positive floats order like their bits
     const uint32_t kb = __reduce_max_sync(0xffffffffu, __float_as_uint(ka));
     const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(va));
-    __shared__ uint32_t s_k[APPEND_WARPS], s_v[APPEND_WARPS];
-    if (lane == 0) {
-        s_k[warp] = kb;
-        s_v[warp] = vb;
-    }
     const size_t sc = (size_t)id * p.Hkv + hk;
     // the old scales, read before any thread writes the new ones; a page that starts here has none
     const int ek_old = kept > 0 ? exponent_of(p.ks[sc]) : SCALE_MIN, ev_old = kept > 0 ? exponent_of(p.vs[sc]) : SCALE_MIN;
-    __syncthreads();
-    uint32_t km = s_k[0], vm = s_v[0];
+    uint32_t km = kb, vm = vb;
+    if constexpr (kWarp) {
+        __syncwarp();
+    } else {
+        __shared__ uint32_t s_k[APPEND_WARPS], s_v[APPEND_WARPS];
+        if (lane == 0) {
+            s_k[warp] = kb;
+            s_v[warp] = vb;
+        }
+        __syncthreads();
 #pragma unroll
-    for (int w = 1; w < APPEND_WARPS; ++w) {
-        km = max(km, s_k[w]);
-        vm = max(vm, s_v[w]);
+        for (int w = 0; w < APPEND_WARPS; ++w) {
+            km = max(km, s_k[w]);
+            vm = max(vm, s_v[w]);
+        }
     }
     const int ek = max(scale_exponent(__uint_as_float(km)), ek_old), ev = max(scale_exponent(__uint_as_float(vm)), ev_old);
-    if (threadIdx.x == 0) {
+    if (kWarp ? lane == 0 : threadIdx.x == 0) {
         p.ks[sc] = pow2(ek);
         p.vs[sc] = pow2(ev);
     }
     uint8_t *const kc = p.k8 + sc * p.page * HD, *const vc = p.v8 + sc * p.page * HD;
     auto moved = [&](uint8_t *codes, int from, int to) {
         const float r = from - to >= -126 ? pow2(from - to) : 0.f;
-        for (int t = warp; t < kept; t += APPEND_WARPS) {
+        for (int t = t0; t < kept; t += STRIDE) {
             uint32_t *const w = reinterpret_cast<uint32_t *>(codes + (size_t)t * HD) + lane;
             const float4 x = unpack_e4m3x4(*w);
             *w = pack_e4m3x4(make_float4(x.x * r, x.y * r, x.z * r, x.w * r));
@@ -225,15 +281,18 @@ static __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(con
     if (kept > 0 && ek > ek_old) moved(kc, ek_old, ek);
     if (kept > 0 && ev > ev_old) moved(vc, ev_old, ev);
     const float kr = pow2(-ek), vr = pow2(-ev);
-    for (int t = kept + warp; t < last; t += APPEND_WARPS) {
-        float4 x = load_bf16x4(krow + (size_t)(t - kept) * HD, lane);
-        if (turn) x = rotate(p, x, (int)(page0 + t), lane);
+    auto store = [&](int t, float4 x, float4 y) {
         reinterpret_cast<uint32_t *>(kc + (size_t)t * HD)[lane] =
             pack_e4m3x4(make_float4(x.x * kr, x.y * kr, x.z * kr, x.w * kr));
-        const float4 y = load_bf16x4(vrow + (size_t)(t - kept) * HD, lane);
         reinterpret_cast<uint32_t *>(vc + (size_t)t * HD)[lane] =
             pack_e4m3x4(make_float4(y.x * vr, y.y * vr, y.z * vr, y.w * vr));
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int t = kept + t0 + STRIDE * i;
+        if (t < last) store(t, kh[i], bf16x4(vh[i]));
     }
+    for (int t = kept + t0 + STRIDE * HELD; t < last; t += STRIDE) store(t, key(t), bf16x4(value(t)));
 }
 
 // --------------------------------------------------------------- attention
