@@ -63,10 +63,10 @@ from ._scored import (  # noqa: E402,F401
     bwd_scored_workspace_bytes,
     key_bounds,
 )
-from .autograd import AttnJvpFunction, attn_jvp_autograd  # noqa: E402,F401
+from .autograd import AttnJvpFunction, AttnJvpScoredFunction, attn_jvp_autograd  # noqa: E402,F401
 
 __all__ = [
-    "AttnJvpFunction", "attn_jvp_autograd", "attn_jvp", "attn_jvp_bwd", "attn_jvp_bwd_causal",
+    "AttnJvpFunction", "AttnJvpScoredFunction", "attn_jvp_autograd", "attn_jvp", "attn_jvp_bwd", "attn_jvp_bwd_causal",
     "attn_jvp_fwd_causal_stats", "attn_jvp_bwd_varlen", "attn_jvp_fwd_varlen_stats", "attn_jvp_bwd_host",
     "bwd_host_workspace_bytes", "default_bwd_heads_per_chunk", "attn_jvp_fwd_causal", "attn_jvp_fwd_varlen",
     "attn_jvp_fwd_stats", "bwd_workspace_bytes", "bwd_key_split_parts", "attn_jvp_fwd", "attn_jvp_fwd_f32",

@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from ._binding import _check, _ptr, load_library
-from ._scored import _launch_stream, _tensor
+from ._scored import _launch_scope, _tensor
 
 __all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache"]
 
@@ -75,17 +75,19 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
         if H < 1 or H % Hkv:
             raise ValueError(f"q must be [H, total, d] with H a multiple of the key heads ({Hkv})")
         _tensor("q", q, (H, total, d), torch.bfloat16, dev)
-        q_out = torch.empty_like(q) if q_out is None else _tensor("q_out", q_out, q.shape, torch.bfloat16, dev)
-        if tq is not None:
-            _tensor("tq", tq, q.shape, torch.bfloat16, dev)
-            tq_out = torch.empty_like(q) if tq_out is None else _tensor("tq_out", tq_out, q.shape, torch.bfloat16, dev)
+        for name, x in (("tq", tq), ("q_out", q_out), ("tq_out", tq_out)):
+            if x is not None:
+                _tensor(name, x, q.shape, torch.bfloat16, dev)
     if (q is None and (tq is not None or q_out is not None)) or (tq is None and tq_out is not None):
         raise ValueError("tq goes with q, and an output with its input")
-    with torch.cuda.device(dev):
+    scope, handle = _launch_scope(stream, dev)
+    with scope:
+        q_out = torch.empty_like(q) if q is not None and q_out is None else q_out
+        tq_out = torch.empty_like(tq) if tq is not None and tq_out is None else tq_out
         rc = load_library().attn_jvp_cache_append(
             _ptr(k), _ptr(v), _ptr(q), _ptr(tq), _ptr(q_out), _ptr(tq_out), _ptr(k_cache), _ptr(v_cache),
             _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(cache_lens), _ptr(cu_seqlens), _ptr(cos), _ptr(sin),
-            n_seq, H, Hkv, total, pages, page, width, n_pos, d, int(bool(interleaved)), _launch_stream(stream, dev))
+            n_seq, H, Hkv, total, pages, page, width, n_pos, d, int(bool(interleaved)), handle)
     _check(rc, "attn_jvp_cache_append")
     return q_out, tq_out
 
@@ -128,23 +130,23 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
         raise ValueError("tq must have q's shape, strides, type and device")
     if slopes is not None:
         _tensor("slopes", slopes, (H,), torch.float32, dev)
-    shape = tuple(q.shape)
-    o = torch.empty(shape, dtype=torch.bfloat16, device=dev) if o is None else _tensor("o", o, shape, torch.bfloat16, dev)
-    if tq is None:
-        if to is not None:
-            raise ValueError("to goes with tq")
-    else:
-        to = torch.empty(shape, dtype=torch.bfloat16, device=dev) if to is None else \
-            _tensor("to", to, shape, torch.bfloat16, dev)
+    shape = q.shape
+    if tq is None and to is not None:
+        raise ValueError("to goes with tq")
+    for name, x in (("o", o), ("to", to)):
+        if x is not None:
+            _tensor(name, x, shape, torch.bfloat16, dev)
     if lse is not None:
         _tensor("lse", lse, shape[:-1], torch.float32, dev)
-    elif want_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    scope, handle = _launch_scope(stream, dev)
+    with scope:
+        o = torch.empty(shape, dtype=torch.bfloat16, device=dev) if o is None else o
+        to = torch.empty(shape, dtype=torch.bfloat16, device=dev) if to is None and tq is not None else to
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if lse is None and want_lse else lse
         rc = load_library().attn_jvp_fwd_cache(
             _ptr(q), _ptr(tq), _ptr(o), _ptr(to), _ptr(lse), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
             _ptr(v_scale), _ptr(block_table), _ptr(cache_lens), _ptr(cu_seqlens), _ptr(slopes), n_seq, H, Hkv, n,
             total, *strides, pages, page, width, d, float(d ** -0.5 if scale is None else scale),
-            float(softcap or 0.0), int(bool(causal)), _launch_stream(stream, dev))
+            float(softcap or 0.0), int(bool(causal)), handle)
     _check(rc, "attn_jvp_fwd_cache")
     return o, to, lse

@@ -5,6 +5,8 @@ and ``key_bounds``, which writes the usual masks as such intervals.
 Argument marshalling only, as in ``_binding``."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from ._binding import GRAD_NAMES, _check, _ptr, load_library
@@ -13,9 +15,12 @@ __all__ = ["attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_sco
            "key_bounds"]
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _tensor(name, x, shape, dtype, device=None):
     """x is a contiguous CUDA tensor of this shape and type (on this device)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype or tuple(x.shape) != tuple(shape) \
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype or x.shape != shape \
             or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
     if device is not None and x.device != device:
@@ -23,15 +28,19 @@ def _tensor(name, x, shape, dtype, device=None):
     return x
 
 
-def _launch_stream(stream, device) -> int:
-    """Handle of ``stream``, by default torch's current stream of ``device``."""
+def _launch_scope(stream, device):
+    """(context, handle) of a call: inside the context ``device`` is current and
+    memory is allocated for the stream that the call launches on (torch's
+    current stream of the device, or ``stream``), so that nothing allocated
+    for the call is handed out again, or was last used, on another one."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != device:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-        return stream.cuda_stream
-    return int(stream)
+        here = torch.cuda.current_device() == device.index
+        return _HERE if here else torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
 def _sizes(q, k, v, tq, tk, tv):
@@ -52,15 +61,14 @@ def _score_args(slopes, key_begin, key_end, softcap, scale, sizes, device):
     B, H, _, Lq, _, d = sizes
     if slopes is not None:
         _tensor("slopes", slopes, (H,), torch.float32, device)
-    bounds = []
     for name, x in (("key_begin", key_begin), ("key_end", key_end)):
-        if x is not None:
-            if isinstance(x, torch.Tensor) and x.dim() == 1:  # the same for every sequence of the batch
-                _tensor(name, x, (Lq,), torch.int32, device)
-                x = x.expand(B, Lq).contiguous()
-            _tensor(name, x, (B, Lq), torch.int32, device)
-        bounds.append(x)
-    return slopes, bounds[0], bounds[1], float(softcap or 0.0), float(d ** -0.5 if scale is None else scale)
+        if x is not None:  # (one dimension: the same for every sequence of the batch)
+            _tensor(name, x, (Lq,) if isinstance(x, torch.Tensor) and x.dim() == 1 else (B, Lq), torch.int32, device)
+    return float(softcap or 0.0), float(d ** -0.5 if scale is None else scale)
+
+
+def _per_sequence(x, B):
+    return x.expand(B, x.shape[0]).contiguous() if x is not None and x.dim() == 1 else x
 
 
 def _fwd(entry, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end, o, to, lse, mu, stream, want_lse,
@@ -68,17 +76,24 @@ def _fwd(entry, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end,
     sizes = _sizes(q, k, v, tq, tk, tv)
     B, H, _, Lq, _, _ = sizes
     dev = q.device
-    slopes, key_begin, key_end, softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
-    o = torch.empty_like(q) if o is None else _tensor("o", o, q.shape, torch.bfloat16, dev)
-    to = torch.empty_like(q) if to is None else _tensor("to", to, q.shape, torch.bfloat16, dev)
-    stat = lambda name, x, want: (_tensor(name, x, (B, H, Lq), torch.float32, dev) if x is not None  # noqa: E731
-                                  else torch.empty((B, H, Lq), device=dev) if want else None)
-    lse, mu = stat("lse", lse, want_lse), stat("mu", mu, want_mu)
-    rows = (_ptr(o), _ptr(to), _ptr(lse)) + ((_ptr(mu),) if want_mu else ())
-    with torch.cuda.device(dev):
+    softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
+    for name, x in (("o", o), ("to", to)):
+        if x is not None:
+            _tensor(name, x, q.shape, torch.bfloat16, dev)
+    for name, x in (("lse", lse), ("mu", mu)):
+        if x is not None:
+            _tensor(name, x, (B, H, Lq), torch.float32, dev)
+    scope, handle = _launch_scope(stream, dev)
+    with scope:
+        o = torch.empty_like(q) if o is None else o
+        to = torch.empty_like(q) if to is None else to
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        mu = torch.empty((B, H, Lq), dtype=torch.float32, device=dev) if mu is None and want_mu else mu
+        key_begin, key_end = _per_sequence(key_begin, B), _per_sequence(key_end, B)
+        rows = (_ptr(o), _ptr(to), _ptr(lse)) + ((_ptr(mu),) if want_mu else ())
         rc = getattr(load_library(), entry)(_ptr(q), _ptr(k), _ptr(v), _ptr(tq), _ptr(tk), _ptr(tv), *rows,
                                             _ptr(slopes), _ptr(key_begin), _ptr(key_end), *sizes, scale, softcap,
-                                            _launch_stream(stream, dev))
+                                            handle)
     _check(rc, entry)
     return o, to, lse, mu
 
@@ -122,22 +137,26 @@ def attn_jvp_bwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout, scale=
     sizes = _sizes(q, k, v, tq, tk, tv)
     B, H, _, Lq, _, _ = sizes
     dev = q.device
-    slopes, key_begin, key_end, softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
+    softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
     for name, x in (("o", o), ("to", to), ("dout", dout), ("dtout", dtout)):
         _tensor(name, x, q.shape, torch.bfloat16, dev)
     for name, x in (("lse", lse), ("mu", mu)):
         _tensor(name, x, (B, H, Lq), torch.float32, dev)
     grads = dict(grads or {})
-    for name in GRAD_NAMES:
-        like = q if name in ("dq", "dtq") else k
-        if grads.get(name) is None:
-            grads[name] = torch.empty_like(like)
-        _tensor(name, grads[name], like.shape, torch.bfloat16, dev)
-    with torch.cuda.device(dev):
-        handle = _launch_stream(stream, dev)
+    like = {n: q if n in ("dq", "dtq") else k for n in GRAD_NAMES}
+    for n in GRAD_NAMES:
+        if grads.get(n) is not None:
+            _tensor(n, grads[n], like[n].shape, torch.bfloat16, dev)
+    if workspace is not None:
+        _tensor("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+    scope, handle = _launch_scope(stream, dev)
+    with scope:
+        for n in GRAD_NAMES:
+            if grads.get(n) is None:
+                grads[n] = torch.empty_like(like[n])
         if workspace is None:
             workspace = torch.empty(max(1, bwd_scored_workspace_bytes(*sizes[:5])), dtype=torch.uint8, device=dev)
-        _tensor("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+        key_begin, key_end = _per_sequence(key_begin, B), _per_sequence(key_end, B)
         rc = load_library().attn_jvp_bwd_scored(
             _ptr(q), _ptr(k), _ptr(v), _ptr(tq), _ptr(tk), _ptr(tv), _ptr(o), _ptr(to), _ptr(lse), _ptr(mu),
             _ptr(dout), _ptr(dtout), *(_ptr(grads[n]) for n in GRAD_NAMES), _ptr(slopes), _ptr(key_begin),

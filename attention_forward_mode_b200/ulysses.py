@@ -28,6 +28,11 @@ the six gradients to sequence shards.
 ``causal=True`` selects the causal kernels as the local step: after the
 exchange every rank holds whole sequences in their original order, so the
 mask (key j visible to query i iff j <= i + Lk - Lq) applies unchanged.
+
+``score`` (a dict of softcap, slopes, key_begin, key_end, any of them) selects the
+scored kernels: slopes are given for all H heads and bounds for the whole
+sequences, on every rank.  k, v, tk, tv may then have fewer heads Hkv, of which
+H is a multiple; Hkv must divide by P as well.
 """
 from __future__ import annotations
 
@@ -35,6 +40,20 @@ import torch
 import torch.distributed as dist
 
 from ._binding import attn_jvp
+
+
+def _scored_local(fn, score, H, Hkv, world, group):
+    """``fn`` of the scored entry points with this rank's share of the heads' slopes."""
+    if Hkv < 1 or H % Hkv or Hkv % world:
+        raise ValueError(f"key heads ({Hkv}) must divide the query heads ({H}) and by the group size ({world})")
+    opts = {n: x for n, x in dict(score or {}).items() if x is not None}
+    unknown = set(opts) - {"softcap", "slopes", "key_begin", "key_end"}
+    if unknown:
+        raise ValueError(f"unknown score options {sorted(unknown)}")
+    if "slopes" in opts and world > 1:
+        r, n = dist.get_rank(group), H // world
+        opts["slopes"] = opts["slopes"][r * n:(r + 1) * n].contiguous()
+    return lambda *args: fn(*args, **opts)
 
 
 def _to_heads(x: torch.Tensor, world: int, group) -> torch.Tensor:
@@ -61,13 +80,15 @@ def _to_sequence(y: torch.Tensor, world: int, group) -> torch.Tensor:
     return recv.permute(1, 2, 0, 3, 4, 5).reshape(n, B, world * hp, Ls, e)
 
 
-def ulysses_attn_jvp(q, k, v, tq, tk, tv, scale=None, group=None, local_fn=None, causal=False):
+def ulysses_attn_jvp(q, k, v, tq, tk, tv, scale=None, group=None, local_fn=None, causal=False, score=None):
     """O, tO, lse for sequence-sharded inputs (see the module docstring).
 
     ``local_fn(q, k, v, tq, tk, tv, scale) -> (o, to, lse)`` computes the
     attention JVP of the gathered head shard; it defaults to the CUDA kernel
-    (``attn_jvp``, or ``attn_jvp_fwd_causal`` with ``causal``).  Collective
-    calls are made in the same order on every rank.
+    (``attn_jvp``, ``attn_jvp_fwd_causal`` with ``causal``, or
+    ``attn_jvp_fwd_scored`` with ``score`` or shared key heads, called with the
+    options of ``score`` as keywords).  Collective calls are made in the same order
+    on every rank.
     """
     grouped = dist.is_initialized()
     world = dist.get_world_size(group) if grouped else 1
@@ -77,7 +98,13 @@ def ulysses_attn_jvp(q, k, v, tq, tk, tv, scale=None, group=None, local_fn=None,
         raise ValueError(f"heads ({H}) must divide by the group size ({world})")
     if scale is None:
         scale = d ** -0.5
-    if local_fn is not None:
+    if score is not None or k.shape[1] != H:
+        if causal:
+            raise ValueError("causal goes into the score's bounds")
+        if local_fn is None:
+            from ._scored import attn_jvp_fwd_scored as local_fn
+        fn = _scored_local(local_fn, score, H, k.shape[1], world, group)
+    elif local_fn is not None:
         fn = local_fn
     elif causal:
         from ._binding import attn_jvp_fwd_causal
@@ -97,7 +124,7 @@ def ulysses_attn_jvp(q, k, v, tq, tk, tv, scale=None, group=None, local_fn=None,
     return out[0], out[1], lse_s
 
 
-def ulysses_attn_jvp_train(q, k, v, tq, tk, tv, scale=None, group=None, local_fwd=None, causal=False):
+def ulysses_attn_jvp_train(q, k, v, tq, tk, tv, scale=None, group=None, local_fwd=None, causal=False, score=None):
     """Forward of ``ulysses_attn_jvp`` that also keeps what the backward needs.
 
     Returns (o, to, lse, ctx): the sequence-sharded outputs as
@@ -105,7 +132,8 @@ def ulysses_attn_jvp_train(q, k, v, tq, tk, tv, scale=None, group=None, local_fw
     holding the head-sharded inputs and the forward's head-sharded O, tO, lse
     and mu.  ``local_fwd(q, k, v, tq, tk, tv, scale) -> (o, to, lse, mu)``
     defaults to the library's ``attn_jvp_fwd_stats`` (``attn_jvp_fwd_causal_stats``
-    with ``causal``, which ``ulysses_attn_jvp_bwd`` then follows).
+    with ``causal``, ``attn_jvp_fwd_scored_stats`` with ``score`` or shared key
+    heads), which ``ulysses_attn_jvp_bwd`` then follows.
     """
     from ._binding import attn_jvp_fwd_causal_stats, attn_jvp_fwd_stats
     grouped = dist.is_initialized()
@@ -115,10 +143,19 @@ def ulysses_attn_jvp_train(q, k, v, tq, tk, tv, scale=None, group=None, local_fw
         raise ValueError(f"heads ({H}) must divide by the group size ({world})")
     if scale is None:
         scale = d ** -0.5
-    fn = local_fwd if local_fwd is not None else (attn_jvp_fwd_causal_stats if causal else attn_jvp_fwd_stats)
+    heads = None  # (H, Hkv) of a scored call
+    if score is not None or k.shape[1] != H:
+        if causal:
+            raise ValueError("causal goes into the score's bounds")
+        from ._scored import attn_jvp_fwd_scored_stats
+        heads = (H, k.shape[1])
+        fn = _scored_local(local_fwd or attn_jvp_fwd_scored_stats, score, *heads, world, group)
+    else:
+        fn = local_fwd if local_fwd is not None else (attn_jvp_fwd_causal_stats if causal else attn_jvp_fwd_stats)
     if not grouped:
         o, to, lse, mu = fn(q, k, v, tq, tk, tv, scale)
-        ctx = dict(inputs=(q, k, v, tq, tk, tv), outputs=(o, to, lse, mu), scale=scale, world=1, causal=causal)
+        ctx = dict(inputs=(q, k, v, tq, tk, tv), outputs=(o, to, lse, mu), scale=scale, world=1, causal=causal,
+                   score=score, heads=heads)
         return o, to, lse, ctx
     qs = _to_heads(torch.stack((q, tq)), world, group)        # [2, B, H/P, Lq, d]
     ks = _to_heads(torch.stack((k, v, tk, tv)), world, group)  # [4, B, H/P, Lk, d]
@@ -127,7 +164,8 @@ def ulysses_attn_jvp_train(q, k, v, tq, tk, tv, scale=None, group=None, local_fw
     o, to, lse, mu = fn(*inputs, scale)
     out = _to_sequence(torch.stack((o, to)), world, group)
     lse_s = _to_sequence(lse.unsqueeze(0).unsqueeze(-1).contiguous(), world, group)[0, ..., 0]
-    ctx = dict(inputs=inputs, outputs=(o, to, lse, mu), scale=scale, world=world, causal=causal)
+    ctx = dict(inputs=inputs, outputs=(o, to, lse, mu), scale=scale, world=world, causal=causal, score=score,
+               heads=heads)
     return out[0], out[1], lse_s, ctx
 
 
@@ -141,12 +179,17 @@ def ulysses_attn_jvp_bwd(ctx, dout, dtout, group=None, local_bwd=None):
     sequence shards (one all-to-all for the query side, one for the key
     side).  ``local_bwd(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout,
     scale) -> dict`` defaults to the library's ``attn_jvp_bwd`` (or
-    ``attn_jvp_bwd_causal`` when the forward was causal).  Returns a dict dq,
+    ``attn_jvp_bwd_causal`` when the forward was causal, ``attn_jvp_bwd_scored`` when
+    it was scored).  Returns a dict dq,
     dk, dv, dtq, dtk, dtv shaped like the inputs.
     """
     from ._binding import attn_jvp_bwd, attn_jvp_bwd_causal
-    fn = local_bwd if local_bwd is not None else (attn_jvp_bwd_causal if ctx.get("causal") else attn_jvp_bwd)
     world = ctx["world"]
+    if ctx.get("heads") is not None:
+        from ._scored import attn_jvp_bwd_scored
+        fn = _scored_local(local_bwd or attn_jvp_bwd_scored, ctx["score"], *ctx["heads"], world, group)
+    else:
+        fn = local_bwd if local_bwd is not None else (attn_jvp_bwd_causal if ctx.get("causal") else attn_jvp_bwd)
     if world == 1:
         return fn(*ctx["inputs"], *ctx["outputs"], dout, dtout, ctx["scale"])
     cot = _to_heads(torch.stack((dout, dtout)), world, group)  # [2, B, H/P, Lq, d]

@@ -147,3 +147,197 @@ def test_attention_over_the_cache(case):
         # fp32 scores of 128 products (2^-17 absolute here), the cap's tanh c 2^-21
         tol = 2.0 ** -15 * (1.0 + rlse[~empty].abs())
         assert ((lse[b][~empty].double() - rlse[~empty]).abs() <= tol).all()
+
+
+def test_pages_that_do_not_exist_and_ends_inside_tiles():
+    """Pages outside the cache are neither written nor seen; their tokens count as hidden."""
+    lens, page, Hkv, H = [200, 70], 16, 2, 4
+    cache, table, g = filled(2, Hkv, page, lens, seed=31)
+    n_pages = cache[0].shape[0]
+    table[0, 3], table[0, 7], table[1, 4] = -1, n_pages, 2 ** 31 - 1
+    q, tq = (torch.randn((2, H, 2, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, to, lse = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens_d)
+    want = ref.attention(list(q), list(tq), *cache, table.cpu().cuda(), lens, 128 ** -0.5)
+    for b, (ro, rto, rlse, bo, bto) in enumerate(want):
+        assert ((o[b].double() - ro).abs() <= bo).all() and ((to[b].double() - rto).abs() <= bto).all()
+    before = [t.clone() for t in cache]
+    bad = torch.full_like(table, -5)
+    k = torch.randn((Hkv, 40, 128), generator=g, device="cuda").bfloat16()
+    cu = torch.tensor([0, 40, 40], dtype=torch.int32, device="cuda")
+    ajvp.attn_jvp_cache_append(k, k, *cache, bad, lens_d, cu)
+    # past the table's capacity too
+    ajvp.attn_jvp_cache_append(k, k, *cache, table, torch.full_like(lens_d, table.shape[1] * page), cu)
+    torch.cuda.synchronize()
+    for a, b in zip(before, cache):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_rows_behind_the_last_sequence_stay_as_they_were():
+    Hkv, H, page, total = 1, 2, 16, 20
+    cache, table, g = filled(2, Hkv, page, [30, 9], seed=32)
+    cu = torch.tensor([0, 5, 12], dtype=torch.int32, device="cuda")  # rows 12 .. 19 belong to nobody
+    lens = torch.tensor([30, 9], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((Hkv, total, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    q, tq = (torch.randn((H, total, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    cos, sin = angles(64)
+    out = [torch.full_like(q, 3.0) for _ in range(2)]
+    wide = torch.cat([table, torch.arange(2, device="cuda", dtype=torch.int32)[:, None] + int(table.max()) + 1], 1)
+    cache = [torch.cat([t, t[:4]], 0) if t.dim() == 2 else torch.cat([t.view(torch.uint8), t.view(torch.uint8)[:4]], 0)
+             .view(t.dtype) for t in cache]
+    ajvp.attn_jvp_cache_append(k, v, *cache, wide, lens, cu, q=q, tq=tq, cos=cos, sin=sin, q_out=out[0], tq_out=out[1])
+    lens = lens + (cu[1:] - cu[:-1])
+    o, to = torch.full_like(q, 5.0), torch.full_like(q, 5.0)
+    lse = torch.full((H, total), 5.0, device="cuda")
+    ajvp.attn_jvp_fwd_cache(out[0], out[1], *cache, wide, lens, cu_seqlens=cu, max_seqlen=7, o=o, to=to, lse=lse)
+    torch.cuda.synchronize()
+    assert all((t[:, 12:] == 3.0).all() for t in out) and all((t[:, 12:] == 5.0).all() for t in (o, to, lse))
+    rows = [(0, 5), (5, 12)]
+    want = ref.attention([out[0][:, a:b] for a, b in rows], [out[1][:, a:b] for a, b in rows], *cache, wide,
+                         lens.tolist(), 128 ** -0.5)
+    for (a, b), (ro, rto, rlse, bo, bto) in zip(rows, want):
+        assert ((o[:, a:b].double() - ro).abs() <= bo).all() and ((to[:, a:b].double() - rto).abs() <= bto).all()
+        assert ((lse[:, a:b].double() - rlse).abs() <= 2.0 ** -15 * (1.0 + rlse.abs())).all()
+
+
+def test_append_then_attend_like_dense_attention():
+    """Chunks joining two caches over several steps, attended after each: the same as scored attention
+    over the values that the cache stands for."""
+    H, Hkv, page, chunk, steps = 4, 2, 32, 48, 4
+    table, pages = tables(2, -(-chunk * steps // page), 1, 33)
+    cache, table = empty_cache(pages, Hkv, page, 33), table.cuda()
+    g = torch.Generator(device="cuda").manual_seed(33)
+    cos, sin = angles(chunk * steps)
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, chunk, 2 * chunk], dtype=torch.int32, device="cuda")
+    slopes = torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], device="cuda")
+    for step in range(steps):
+        k, v = (torch.randn((Hkv, 2 * chunk, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+        q, tq = (torch.randn((H, 2 * chunk, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+        q, tq = ajvp.attn_jvp_cache_append(k, v, *cache, table, lens, cu, q=q, tq=tq, cos=cos, sin=sin, interleaved=True)
+        lens += chunk
+        n = (step + 1) * chunk
+        packed = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens, cu_seqlens=cu, max_seqlen=chunk, softcap=30.0,
+                                         slopes=slopes)
+        # the same rows as a strided [n_seq, H, n, d] view
+        view = [t.view(H, 2, chunk, 128).transpose(0, 1) for t in (q, tq)]
+        dense = ajvp.attn_jvp_fwd_cache(*view, *cache, table, lens, softcap=30.0, slopes=slopes)
+        for a, b in zip(packed, dense):
+            assert torch.equal(a.view(H, 2, chunk, *a.shape[2:]).transpose(0, 1), b)
+        kd, vd = (c[table.long()].float().mul(f[table.long()][..., None, None]).transpose(1, 2).flatten(2, 3)[:, :, :n]
+                  .contiguous().bfloat16() for c, f in ((cache[0], cache[2]), (cache[1], cache[3])))  # exact: 4 bits
+        z = torch.zeros_like(kd)
+        begin, end = ajvp.key_bounds(chunk, n, causal=True)
+        o, to, lse = ajvp.attn_jvp_fwd_scored(view[0].contiguous(), kd, vd, view[1].contiguous(), z, z, softcap=30.0,
+                                              slopes=slopes, key_begin=begin, key_end=end)
+        # both are within the roundings of their weights (f16 and bf16) and outputs of the same values
+        for a, b, times in ((dense[0], o, 3), (dense[1], to, 4)):
+            assert (a.double() - b.double()).norm() <= times * ref.UB * b.double().norm()
+        assert ((dense[2] - lse).abs() <= 2.0 ** -14 * (1 + lse.abs())).all()
+
+
+def test_scales_far_apart_and_constant_tangents():
+    """Pages whose values differ by powers of two, and a tangent whose dS hardly varies."""
+    H, page, L = 2, 16, 320
+    table, pages = tables(1, L // page, 0, 34)
+    cache, table = empty_cache(pages, 1, page, 34), table.cuda()
+    g = torch.Generator(device="cuda").manual_seed(34)
+    size = 2.0 ** torch.randint(-12, 13, (1, L // page, 1, 1), generator=g, device="cuda").float()
+    k = (torch.randn((1, L // page, page, 128), generator=g, device="cuda") * size * 0.02).view(1, L, 128).bfloat16()
+    size = 2.0 ** torch.randint(-20, 21, (1, L // page, 1, 1), generator=g, device="cuda").float()
+    v = (torch.randn((1, L // page, page, 128), generator=g, device="cuda") * size).view(1, L, 128).bfloat16()
+    zero, cu = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    ajvp.attn_jvp_cache_append(k, v, *cache, table, zero, cu)
+    q, tq = (torch.randn((1, H, 1, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    for t in (tq, q):  # (tq = q: dS follows S)
+        o, to, lse = ajvp.attn_jvp_fwd_cache(q, t, *cache, table, lens)
+        ro, rto, rlse, bo, bto = ref.attention(list(q), list(t), *cache, table, [L], 128 ** -0.5)[0]
+        assert ((o[0].double() - ro).abs() <= bo).all() and ((to[0].double() - rto).abs() <= bto).all()
+        # scores reach some hundreds here, fp32 sums of products up to as much
+        assert ((lse[0].double() - rlse).abs() <= 2.0 ** -15 * (1.0 + rlse.abs())).all()
+
+
+def test_one_key_has_no_tangent():
+    cache, table, g = filled(3, 2, 16, [1, 1, 1], seed=35)
+    q, tq = (torch.randn((3, 4, 1, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    o, to, _ = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, torch.ones(3, dtype=torch.int32, device="cuda"))
+    # P = 1: tO is zero but for fp32 roundings of dS - r, some 2^-23 of |dS| |V|
+    assert (to.abs() <= 2.0 ** -18 * 60.0 * o.abs().amax()).all()
+
+
+def test_codes_past_32_bit_offsets():
+    """The last pages of a cache of more than 2^31 bytes of codes."""
+    page, Hkv, pages = 64, 1, (1 << 31) // (64 * 128) + 3
+    if torch.cuda.get_device_properties(0).total_memory < 3 * (1 << 32):
+        pytest.skip("needs 5 GB")
+    k8, v8 = (torch.empty((pages, Hkv, page, 128), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((pages, Hkv), device="cuda") for _ in range(2))
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(36)
+    k, v = (torch.randn((1, 150, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    zero, cu = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, 150], dtype=torch.int32, device="cuda")
+    ajvp.attn_jvp_cache_append(k, v, k8, v8, ks, vs, table, zero, cu)
+    q, tq = (torch.randn((1, 2, 1, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    o, to, _ = ajvp.attn_jvp_fwd_cache(q, tq, k8, v8, ks, vs, table, torch.tensor([150], dtype=torch.int32, device="cuda"))
+    at = table[0].long()
+    ro, rto, _, bo, bto = ref.attention(list(q), list(tq), k8[at], v8[at], ks[at], vs[at],
+                                        torch.arange(3, device="cuda")[None], [150], 128 ** -0.5)[0]
+    assert ((o[0].double() - ro).abs() <= bo).all() and ((to[0].double() - rto).abs() <= bto).all()
+
+
+def test_decoding_in_a_graph():
+    """One captured step (append, attend, lengthen), replayed: the same as eager steps on a copy."""
+    H, Hkv, page, steps = 4, 2, 16, 40
+    table, pages = tables(2, 5, 0, 37)
+    table = table.cuda()
+    g = torch.Generator(device="cuda").manual_seed(37)
+    cos, sin = angles(80)
+    lens = [torch.tensor([7, 20], dtype=torch.int32, device="cuda") for _ in range(2)]
+    caches = [[torch.zeros((pages, Hkv, page, 128), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+               for _ in range(2)] + [torch.full((pages, Hkv), 2.0 ** -8, device="cuda") for _ in range(2)] for _ in range(2)]
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    new = [torch.empty((h, 2, 128), dtype=torch.bfloat16, device="cuda") for h in (Hkv, Hkv, H, H)]
+
+    def step(cache, n):
+        q, tq = ajvp.attn_jvp_cache_append(new[0], new[1], *cache, table, n, cu, q=new[2], tq=new[3], cos=cos, sin=sin)
+        n += 1
+        return ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, n, cu_seqlens=cu, max_seqlen=1)
+
+    def feed(i):
+        for t in new:
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda") * (1.0 + 0.2 * i))
+
+    feed(0)
+    step(caches[0], lens[0])
+    step(caches[1], lens[1])
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    keep = [t.clone() for t in caches[0]], lens[0].clone()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        out = step(caches[0], lens[0])
+    for a, b in zip(caches[0], keep[0]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # (capturing runs nothing)
+    for i in range(1, steps):
+        feed(i)
+        graph.replay()
+        want = step(caches[1], lens[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+    for a, b in zip(*caches):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert ajvp.check_device_status() == ajvp.AJVP_OK
+
+
+def test_two_streams_share_a_cache():
+    cache, table, g = filled(4, 2, 64, [900, 50, 1300, 2], seed=38)
+    lens = torch.tensor([900, 50, 1300, 2], dtype=torch.int32, device="cuda")
+    q, tq = (torch.randn((4, 6, 3, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    first = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens, stream=s) for s in streams] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for out in pair:
+            assert all(torch.equal(a, b) for a, b in zip(out, first))

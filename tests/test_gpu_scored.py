@@ -99,3 +99,199 @@ def test_forward_and_backward(case):
     assert ajvp.check_device_status() == ajvp.AJVP_OK
     for n in ajvp._binding.GRAD_NAMES:
         ref.check(n, g[n], rg[n], eg[n])
+
+
+def run(inp, cot, kw, **more):
+    x = [inp[n] for n in NAMES]
+    out = ajvp.attn_jvp_fwd_scored_stats(*x, **kw)
+    return out, ajvp.attn_jvp_bwd_scored(*x, *out, cot["dout"], cot["dtout"], **kw, **more)
+
+
+def against_reference(inp, cot, kw, out, g, scale=128 ** -0.5):
+    B = inp["q"].shape[0]
+    x = [inp[n] for n in NAMES]
+    (ro, rto, rlse, _), (eo, eto) = ref.forward(*x, scale, bounds=True, **ref_opts(kw, B))
+    ref.check("o", out[0], ro, eo)
+    ref.check("to", out[1], rto, eto)
+    empty = torch.isinf(rlse)
+    assert torch.equal(torch.isinf(out[2]), empty)
+    assert ((out[2] - rlse)[~empty].abs() <= 2.0 ** -15 * (1.0 + rlse[~empty].abs())).all()
+    rg, eg = ref.backward(*x, cot["dout"], cot["dtout"], scale, bounds=True, **ref_opts(kw, B))
+    for n in ajvp.GRAD_NAMES:
+        ref.check(n, g[n], rg[n], eg[n])
+    assert ajvp.check_device_status() == ajvp.AJVP_OK
+
+
+@pytest.mark.parametrize("kw,scale,std", [
+    (dict(softcap=0.5), 128 ** -0.5, 1.0),       # scores far past the cap: the exponential's tanh
+    (dict(softcap=200.0), 128 ** -0.5, 1.0),     # a cap too wide for a fixed reference
+    (dict(softcap=200.0, bias=1.0), 128 ** -0.5, 1.0),
+    (dict(softcap=30.0), -(128 ** -0.5), 1.0),   # negative and zero scales
+    (dict(bias=1.0), -(128 ** -0.5), 1.0),
+    (dict(bias=1.0), 0.0, 1.0),
+    (dict(softcap=30.0), 0.0, 1.0),
+    (dict(), 0.0, 1.0),
+    (dict(bias=40.0), 128 ** -0.5, 1.0),         # slopes too steep for separate maxima
+    (dict(bias=-0.01), 128 ** -0.5, 1.0),        # a bias that grows with distance
+    (dict(softcap=30.0, bias=-0.01), 128 ** -0.5, 1.0),
+    (dict(softcap=50.0, bias=1.0), 128 ** -0.5, 3.0),  # peaked rows
+], ids=str)
+def test_score_ranges(kw, scale, std):
+    B, H, L = 1, 2, 300
+    inp, cot = make(B, H, 1, L, L, seed=11, std=std)
+    kw = dict(kw)
+    if "bias" in kw:
+        kw["slopes"] = slopes_of(H) * kw.pop("bias")
+    kw.update(masks("random", B, L, L, seed=4))
+    x = [inp[n] for n in NAMES]
+    out = ajvp.attn_jvp_fwd_scored_stats(*x, scale=scale, **kw)
+    g = ajvp.attn_jvp_bwd_scored(*x, *out, cot["dout"], cot["dtout"], scale=scale, **kw)
+    against_reference(inp, cot, kw, out, g, scale)
+
+
+def test_largest_bias_may_be_far():
+    """Rows whose visible keys all lie far from them: the bias of the nearest is the reference."""
+    B, H, L = 1, 2, 700
+    inp, cot = make(B, H, H, L, L, seed=12)
+    begin = torch.zeros(L, dtype=torch.int32, device="cuda")
+    end = torch.full((L,), 20, dtype=torch.int32, device="cuda")
+    for cap in (0.0, 30.0):
+        kw = dict(softcap=cap, slopes=slopes_of(H) * 2.0, key_begin=begin, key_end=end)
+        out, g = run(inp, cot, kw)
+        assert torch.isfinite(out[2]).all()
+        # fp32 biases of some 700 x 1 hold 2^-14 of themselves: scores, and so weights, 2^-14 x 1000 off
+        (ro, rto, rlse, _), (eo, eto) = ref.forward(*(inp[n] for n in NAMES), 128 ** -0.5, bounds=True, **ref_opts(kw, B))
+        ref.check("o", out[0], ro, eo + 2.0 ** -10)
+        ref.check("to", out[1], rto, eto + 2.0 ** -8)
+        # biases reach 87 (126 in log2 units): each fp32 step on them rounds by up to 2^-24 x 126 < 2^-17,
+        # as do the sums of 128 products; where a score cancels its bias that stays, so the bound is absolute there
+        assert ((out[2] - rlse).abs() <= 2.0 ** -15 * (1.0 + rlse.abs())).all()
+
+
+def test_one_bound_alone_and_per_batch_bounds():
+    B, H, L = 3, 2, 150
+    inp, cot = make(B, H, H, L, L, seed=13)
+    begin, end = random_bounds(B, L, L, 3)
+    for kw in (dict(key_begin=begin), dict(key_end=end), dict(key_begin=begin, key_end=end)):
+        out, g = run(inp, cot, kw)
+        against_reference(inp, cot, kw, out, g)
+
+
+def test_plain_options_match_the_unmasked_and_causal_entries():
+    inp, _ = make(2, 2, 2, 300, 260, seed=14)
+    x = [inp[n] for n in NAMES]
+    a, b = ajvp.attn_jvp_fwd_scored(*x), ajvp.attn_jvp_fwd(*x)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    bounds = dict(zip(("key_begin", "key_end"), ajvp.key_bounds(300, 260, causal=True)))
+    a, b = ajvp.attn_jvp_fwd_scored(*x, **bounds), ajvp.attn_jvp_fwd_causal(*x)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+def test_split_and_unsplit_key_sides():
+    """A small workspace runs the key side unsplit; both agree with the definition, and each with itself."""
+    inp, cot = make(1, 4, 2, 1500, 70, seed=15)
+    x = [inp[n] for n in NAMES]
+    kw = dict(softcap=20.0, slopes=slopes_of(4))
+    full = ajvp.bwd_scored_workspace_bytes(1, 4, 2, 1500, 70)
+    least = (16 * (4 * 1500 + 64) + 255) // 256 * 256 + 256
+    assert full > least  # (this shape splits)
+    out = ajvp.attn_jvp_fwd_scored_stats(*x, **kw)
+    got = []
+    for size in (full, least, full, least):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")  # NaN bits: nothing is read before it is written
+        got.append(ajvp.attn_jvp_bwd_scored(*x, *out, cot["dout"], cot["dtout"], workspace=ws, **kw))
+        against_reference(inp, cot, kw, out, got[-1])
+    for n in ajvp.GRAD_NAMES:
+        assert torch.equal(got[0][n], got[2][n]) and torch.equal(got[1][n], got[3][n])
+
+
+def test_autograd_of_shared_heads():
+    B, H, Hkv, L = 1, 6, 2, 200
+    inp, cot = make(B, H, Hkv, L, L, seed=16)
+    begin, end = ajvp.key_bounds(L, causal=True, prefix=30)
+    kw = dict(softcap=25.0, slopes=slopes_of(H), key_begin=begin, key_end=end)
+    leaves = {n: inp[n].clone().requires_grad_(True) for n in NAMES}
+    o, to = ajvp.attn_jvp_autograd(*(leaves[n] for n in NAMES), **kw)
+    ((o.float() * cot["dout"].float()).sum() + (to.float() * cot["dtout"].float()).sum()).backward()
+    _, g = run(inp, cot, kw)
+    for n, gn in zip(NAMES, ("dq", "dk", "dv", "dtq", "dtk", "dtv")):
+        assert torch.equal(leaves[n].grad, g[gn]), n
+    # a cap alone, causal by its own argument, one output unused
+    leaves = {n: inp[n].clone().requires_grad_(True) for n in NAMES}
+    o, _ = ajvp.attn_jvp_autograd(*(leaves[n] for n in NAMES), softcap=25.0, causal=True)
+    (o.float() * cot["dout"].float()).sum().backward()
+    rg, eg = ref.backward(*(inp[n] for n in NAMES), cot["dout"], torch.zeros_like(cot["dtout"]), 128 ** -0.5, bounds=True,
+                          softcap=25.0, end=ajvp.key_bounds(L, causal=True)[1].expand(B, -1))
+    for n, gn in zip(NAMES, ("dq", "dk", "dv", "dtq", "dtk", "dtv")):
+        ref.check(gn, leaves[n].grad, rg[gn], eg[gn])
+
+
+def test_in_a_graph_beside_an_eager_call_on_another_stream():
+    inp, cot = make(1, 4, 2, 400, 90, seed=17)
+    x = [inp[n] for n in NAMES]
+    begin, end = ajvp.key_bounds(400, 90, causal=True, prefix=40)
+    kw = dict(softcap=30.0, slopes=slopes_of(4), key_begin=begin.expand(1, -1).contiguous(),
+              key_end=end.expand(1, -1).contiguous())
+    run(inp, cot, kw)
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        out, g = run(inp, cot, kw)
+    for seed in (18, 19):
+        new, _ = make(1, 4, 2, 400, 90, seed=seed)
+        for n in NAMES:
+            inp[n].copy_(new[n])
+        torch.cuda.synchronize()
+        other = torch.cuda.Stream()
+        with torch.cuda.stream(other):
+            out2, g2 = run(inp, cot, kw)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, out2))
+        assert all(torch.equal(g[n], g2[n]) for n in g)
+    # an explicit stream: what the call allocates belongs to that stream
+    out3 = ajvp.attn_jvp_fwd_scored_stats(*x, stream=other, **kw)
+    g3 = ajvp.attn_jvp_bwd_scored(*x, *out3, cot["dout"], cot["dtout"], stream=other.cuda_stream, **kw)
+    other.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out3, out2)) and all(torch.equal(g3[n], g2[n]) for n in g3)
+
+
+def test_no_query_rows_give_zero_key_gradients():
+    inp, cot = make(1, 2, 1, 4, 50, seed=20)
+    e = {n: inp[n][:, :, :0].contiguous() for n in ("q", "tq")}
+    z = torch.zeros((1, 2, 0), device="cuda")
+    g = ajvp.attn_jvp_bwd_scored(e["q"], inp["k"], inp["v"], e["tq"], inp["tk"], inp["tv"], e["q"], e["q"], z, z, e["q"],
+                                 e["q"])
+    assert g["dq"].shape[2] == 0 and all((g[n] == 0).all() for n in ("dk", "dv", "dtk", "dtv"))
+
+
+def test_rows_at_the_end_are_written_alone():
+    """Outputs inside a larger buffer: nothing behind them changes."""
+    inp, cot = make(1, 1, 1, 70, 70, seed=21)
+    x = [inp[n] for n in NAMES]
+    big = torch.full((2, 70 * 128 + 640), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, to = (t[: 70 * 128].view(1, 1, 70, 128) for t in big)
+    ajvp.attn_jvp_fwd_scored(*x, o=o, to=to, softcap=20.0)
+    torch.cuda.synchronize()
+    assert (big[:, 70 * 128:] == 7.0).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 12, 4, 4100, 4100), (2, 3, 3, 2049, 515)])
+def test_larger_shapes_by_the_norm(shape):
+    """Relative 2-norm errors of larger calls: roundings of weights, gradients and outputs are
+    independent, at most two of them per output here, each at most U and U / sqrt(3) in the mean."""
+    B, H, Hkv, Lq, Lk = shape
+    inp, cot = make(B, H, Hkv, Lq, Lk, seed=22)
+    kw = dict(softcap=30.0, slopes=slopes_of(H), **masks("prefix", B, Lq, Lk, 0))
+    out, g = run(inp, cot, kw)
+    x = [inp[n] for n in NAMES]
+    for h in range(0, H, max(1, H // Hkv)):  # group by group: 64-bit scores of all heads would not fit
+        hs, hk = slice(h, h + H // Hkv), slice(h * Hkv // H, h * Hkv // H + 1)
+        part = [x[0][:, hs], x[1][:, hk], x[2][:, hk], x[3][:, hs], x[4][:, hk], x[5][:, hk]]
+        opt = ref_opts(dict(kw, slopes=kw["slopes"][hs]), B)
+        ro, rto, _, _ = ref.forward(*part, 128 ** -0.5, **opt)
+        rg = ref.backward(*part, cot["dout"][:, hs], cot["dtout"][:, hs], 128 ** -0.5, **opt)
+        pairs = [(out[0][:, hs], ro), (out[1][:, hs], rto)]
+        pairs += [(g[n][:, hs if n in ("dq", "dtq") else hk], rg[n]) for n in rg]
+        for got, want in pairs:
+            assert (got.double() - want).norm() <= ref.U * want.norm()
