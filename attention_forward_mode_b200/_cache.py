@@ -14,25 +14,23 @@ from __future__ import annotations
 import torch
 
 from ._binding import _check, _ptr, load_library
-from ._scored import _launch_scope, _tensor
+from ._scored import _BF16, _F32, _I32, _launch_scope, _tensor, _tensors
 
 __all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache"]
 
 
 def _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens):
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a [pages, Hkv, page, d] tensor")
-    pages, Hkv, page, d = k_cache.shape
-    dev = k_cache.device
-    _tensor("k_cache", k_cache, k_cache.shape, torch.float8_e4m3fn)
-    _tensor("v_cache", v_cache, k_cache.shape, torch.float8_e4m3fn, dev)
-    _tensor("k_scale", k_scale, (pages, Hkv), torch.float32, dev)
-    _tensor("v_scale", v_scale, (pages, Hkv), torch.float32, dev)
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a CUDA [pages, Hkv, page, d] tensor")
+    shape, dev = k_cache.shape, k_cache.device
+    pages, Hkv, page, d = shape
+    _tensors(("k_cache", "v_cache"), (k_cache, v_cache), shape, torch.float8_e4m3fn, dev)
+    _tensors(("k_scale", "v_scale"), (k_scale, v_scale), (pages, Hkv), _F32, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be an int32 [n_seq, width] tensor")
     n_seq, width = block_table.shape
-    _tensor("block_table", block_table, (n_seq, width), torch.int32, dev)
-    _tensor("cache_lens", cache_lens, (n_seq,), torch.int32, dev)
+    _tensor("block_table", block_table, (n_seq, width), _I32, dev)
+    _tensor("cache_lens", cache_lens, (n_seq,), _I32, dev)
     return n_seq, Hkv, pages, page, width, d, dev
 
 
@@ -55,16 +53,14 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a [Hkv, total, d] tensor")
     total = k.shape[1]
-    _tensor("k", k, (Hkv, total, d), torch.bfloat16, dev)
-    _tensor("v", v, (Hkv, total, d), torch.bfloat16, dev)
-    _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, dev)
+    _tensors(("k", "v"), (k, v), (Hkv, total, d), _BF16, dev)
+    _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), _I32, dev)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     n_pos = 0
     if cos is not None:
         n_pos = cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() == 2 else 0
-        _tensor("cos", cos, (n_pos, d // 2), torch.float32, dev)
-        _tensor("sin", sin, (n_pos, d // 2), torch.float32, dev)
+        _tensors(("cos", "sin"), (cos, sin), (n_pos, d // 2), _F32, dev)
         if n_pos < 1:
             raise ValueError("cos and sin need a row per position")
     H = Hkv
@@ -74,10 +70,10 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
         H = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
         if H < 1 or H % Hkv:
             raise ValueError(f"q must be [H, total, d] with H a multiple of the key heads ({Hkv})")
-        _tensor("q", q, (H, total, d), torch.bfloat16, dev)
+        _tensor("q", q, (H, total, d), _BF16, dev)
         for name, x in (("tq", tq), ("q_out", q_out), ("tq_out", tq_out)):
             if x is not None:
-                _tensor(name, x, q.shape, torch.bfloat16, dev)
+                _tensor(name, x, q.shape, _BF16, dev)
     if (q is None and (tq is not None or q_out is not None)) or (tq is None and tq_out is not None):
         raise ValueError("tq goes with q, and an output with its input")
     scope, handle = _launch_scope(stream, dev)
@@ -85,10 +81,12 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
         q_out = torch.empty_like(q) if q is not None and q_out is None else q_out
         tq_out = torch.empty_like(tq) if tq is not None and tq_out is None else tq_out
         rc = load_library().attn_jvp_cache_append(
-            _ptr(k), _ptr(v), _ptr(q), _ptr(tq), _ptr(q_out), _ptr(tq_out), _ptr(k_cache), _ptr(v_cache),
-            _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(cache_lens), _ptr(cu_seqlens), _ptr(cos), _ptr(sin),
+            k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(tq), _ptr(q_out), _ptr(tq_out), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
+            cu_seqlens.data_ptr(), _ptr(cos), _ptr(sin),
             n_seq, H, Hkv, total, pages, page, width, n_pos, d, int(bool(interleaved)), handle)
-    _check(rc, "attn_jvp_cache_append")
+    if rc:
+        _check(rc, "attn_jvp_cache_append")
     return q_out, tq_out
 
 
@@ -122,31 +120,33 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
     else:
         H, total = q.shape[0], q.shape[1]
         n, strides = total if max_seqlen is None else int(max_seqlen), (0, *q.stride()[:2])
-        _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, dev)
+        _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), _I32, dev)
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"query heads ({H}) must be a multiple of the key heads ({Hkv})")
     if tq is not None and (not isinstance(tq, torch.Tensor) or tq.shape != q.shape or tq.stride() != q.stride()
                            or tq.dtype != q.dtype or tq.device != dev):
         raise ValueError("tq must have q's shape, strides, type and device")
     if slopes is not None:
-        _tensor("slopes", slopes, (H,), torch.float32, dev)
+        _tensor("slopes", slopes, (H,), _F32, dev)
     shape = q.shape
     if tq is None and to is not None:
         raise ValueError("to goes with tq")
     for name, x in (("o", o), ("to", to)):
         if x is not None:
-            _tensor(name, x, shape, torch.bfloat16, dev)
+            _tensor(name, x, shape, _BF16, dev)
     if lse is not None:
-        _tensor("lse", lse, shape[:-1], torch.float32, dev)
+        _tensor("lse", lse, shape[:-1], _F32, dev)
     scope, handle = _launch_scope(stream, dev)
     with scope:
-        o = torch.empty(shape, dtype=torch.bfloat16, device=dev) if o is None else o
-        to = torch.empty(shape, dtype=torch.bfloat16, device=dev) if to is None and tq is not None else to
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        o = q.new_empty(shape) if o is None else o
+        to = q.new_empty(shape) if to is None and tq is not None else to
+        lse = q.new_empty(shape[:-1], dtype=_F32) if lse is None and want_lse else lse
         rc = load_library().attn_jvp_fwd_cache(
-            _ptr(q), _ptr(tq), _ptr(o), _ptr(to), _ptr(lse), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(block_table), _ptr(cache_lens), _ptr(cu_seqlens), _ptr(slopes), n_seq, H, Hkv, n,
+            q.data_ptr(), _ptr(tq), o.data_ptr(), _ptr(to), _ptr(lse), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(), _ptr(cu_seqlens),
+            _ptr(slopes), n_seq, H, Hkv, n,
             total, *strides, pages, page, width, d, float(d ** -0.5 if scale is None else scale),
             float(softcap or 0.0), int(bool(causal)), handle)
-    _check(rc, "attn_jvp_fwd_cache")
+    if rc:
+        _check(rc, "attn_jvp_fwd_cache")
     return o, to, lse

@@ -16,6 +16,8 @@ __all__ = ["attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_sco
 
 
 _HERE = contextlib.nullcontext()
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
 
 
 def _tensor(name, x, shape, dtype, device=None):
@@ -28,6 +30,16 @@ def _tensor(name, x, shape, dtype, device=None):
     return x
 
 
+def _tensors(names, xs, shape, dtype, device):
+    """Every x is such a tensor of one shape and type.  (The calls are short: what
+    a check costs counts, so the common case is one pass.)"""
+    for x in xs:
+        if type(x) is not torch.Tensor or x.dtype is not dtype or x.shape != shape or x.device != device \
+                or not x.is_contiguous():
+            for name, y in zip(names, xs):
+                _tensor(name, y, shape, dtype, device)
+
+
 def _launch_scope(stream, device):
     """(context, handle) of a call: inside the context ``device`` is current and
     memory is allocated for the stream that the call launches on (torch's
@@ -35,7 +47,8 @@ def _launch_scope(stream, device):
     for the call is handed out again, or was last used, on another one."""
     if stream is None:
         here = torch.cuda.current_device() == device.index
-        return _HERE if here else torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+        handle = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+        return _HERE if here else torch.cuda.device(device), handle
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
@@ -47,23 +60,21 @@ def _sizes(q, k, v, tq, tk, tv):
     for name, x in (("q", q), ("k", k)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 4:
             raise ValueError(f"{name} must be a CUDA [B, H, L, d] tensor")
-    B, H, Lq, d = q.shape
-    Hkv, Lk = k.shape[1], k.shape[2]
+    (B, H, Lq, d), (_, Hkv, Lk, _) = q.shape, k.shape
     if H and (Hkv < 1 or H % Hkv):
         raise ValueError(f"query heads ({H}) must be a multiple of the key heads ({Hkv})")
-    for name, x, shape in (("q", q, q.shape), ("tq", tq, q.shape), ("k", k, (B, Hkv, Lk, d)),
-                           ("v", v, (B, Hkv, Lk, d)), ("tk", tk, (B, Hkv, Lk, d)), ("tv", tv, (B, Hkv, Lk, d))):
-        _tensor(name, x, shape, torch.bfloat16, q.device)
+    _tensors(("q", "tq"), (q, tq), q.shape, _BF16, q.device)
+    _tensors(("k", "v", "tk", "tv"), (k, v, tk, tv), (B, Hkv, Lk, d), _BF16, q.device)
     return B, H, Hkv, Lq, Lk, d
 
 
 def _score_args(slopes, key_begin, key_end, softcap, scale, sizes, device):
     B, H, _, Lq, _, d = sizes
     if slopes is not None:
-        _tensor("slopes", slopes, (H,), torch.float32, device)
+        _tensor("slopes", slopes, (H,), _F32, device)
     for name, x in (("key_begin", key_begin), ("key_end", key_end)):
         if x is not None:  # (one dimension: the same for every sequence of the batch)
-            _tensor(name, x, (Lq,) if isinstance(x, torch.Tensor) and x.dim() == 1 else (B, Lq), torch.int32, device)
+            _tensor(name, x, (Lq,) if isinstance(x, torch.Tensor) and x.dim() == 1 else (B, Lq), _I32, device)
     return float(softcap or 0.0), float(d ** -0.5 if scale is None else scale)
 
 
@@ -79,22 +90,23 @@ def _fwd(entry, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end,
     softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
     for name, x in (("o", o), ("to", to)):
         if x is not None:
-            _tensor(name, x, q.shape, torch.bfloat16, dev)
+            _tensor(name, x, q.shape, _BF16, dev)
     for name, x in (("lse", lse), ("mu", mu)):
         if x is not None:
-            _tensor(name, x, (B, H, Lq), torch.float32, dev)
+            _tensor(name, x, (B, H, Lq), _F32, dev)
     scope, handle = _launch_scope(stream, dev)
     with scope:
         o = torch.empty_like(q) if o is None else o
         to = torch.empty_like(q) if to is None else to
-        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev) if lse is None and want_lse else lse
-        mu = torch.empty((B, H, Lq), dtype=torch.float32, device=dev) if mu is None and want_mu else mu
+        lse = q.new_empty((B, H, Lq), dtype=_F32) if lse is None and want_lse else lse
+        mu = q.new_empty((B, H, Lq), dtype=_F32) if mu is None and want_mu else mu
         key_begin, key_end = _per_sequence(key_begin, B), _per_sequence(key_end, B)
-        rows = (_ptr(o), _ptr(to), _ptr(lse)) + ((_ptr(mu),) if want_mu else ())
-        rc = getattr(load_library(), entry)(_ptr(q), _ptr(k), _ptr(v), _ptr(tq), _ptr(tk), _ptr(tv), *rows,
-                                            _ptr(slopes), _ptr(key_begin), _ptr(key_end), *sizes, scale, softcap,
-                                            handle)
-    _check(rc, entry)
+        rows = (o.data_ptr(), to.data_ptr(), _ptr(lse)) + ((mu.data_ptr(),) if want_mu else ())
+        rc = getattr(load_library(), entry)(q.data_ptr(), k.data_ptr(), v.data_ptr(), tq.data_ptr(), tk.data_ptr(),
+                                            tv.data_ptr(), *rows, _ptr(slopes), _ptr(key_begin), _ptr(key_end), *sizes,
+                                            scale, softcap, handle)
+    if rc:
+        _check(rc, entry)
     return o, to, lse, mu
 
 
@@ -138,15 +150,13 @@ def attn_jvp_bwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout, scale=
     B, H, _, Lq, _, _ = sizes
     dev = q.device
     softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
-    for name, x in (("o", o), ("to", to), ("dout", dout), ("dtout", dtout)):
-        _tensor(name, x, q.shape, torch.bfloat16, dev)
-    for name, x in (("lse", lse), ("mu", mu)):
-        _tensor(name, x, (B, H, Lq), torch.float32, dev)
+    _tensors(("o", "to", "dout", "dtout"), (o, to, dout, dtout), q.shape, _BF16, dev)
+    _tensors(("lse", "mu"), (lse, mu), (B, H, Lq), _F32, dev)
     grads = dict(grads or {})
     like = {n: q if n in ("dq", "dtq") else k for n in GRAD_NAMES}
     for n in GRAD_NAMES:
         if grads.get(n) is not None:
-            _tensor(n, grads[n], like[n].shape, torch.bfloat16, dev)
+            _tensor(n, grads[n], like[n].shape, _BF16, dev)
     if workspace is not None:
         _tensor("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
     scope, handle = _launch_scope(stream, dev)
