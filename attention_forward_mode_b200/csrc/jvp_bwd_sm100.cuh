@@ -998,35 +998,30 @@ __device__ __forceinline__ void bwd_body(const Params &p, const unsigned cta) {
             hv += u0 / ntv;
             tv = u0 % ntv;
         }
+        // key side: bounds and slope of the next tile, read a tile ahead
+        int2 cb_next = make_int2(0, 0);
+        float slope_next = 0.f;
+        auto read_next = [&]() {
+            cb_next = row_bounds(p.score, sb, (jt0 + tv) * BN + (int)col0 + lane, Lcol_s, Lrow_s);
+            if (kBias) slope_next = p.score.slopes[hv];
+        };
+        if (kScored && VAR != V_Q && nt > 0) read_next();
         for (int j = 0; j < nt; ++j) {
             const int b = j % C::kNB, s = j % C::kLS;
             int tile = jt0 + j;
             int2 cb = make_int2(0, 0);  // scored key side: the visible keys of this lane's streamed query
             if constexpr (kScored) {
                 tile = jt0 + tv;
-                if (VAR != V_Q) {
-                    cb = row_bounds(p.score, sb, tile * BN + (int)col0 + lane, Lcol_s, Lrow_s);
-                    if (kBias) slope2 = p.score.slopes[hv] * 1.4426950408889634f;
-                }
+                cb = cb_next;
+                if (VAR != V_Q && kBias) slope2 = slope_next * 1.4426950408889634f;
                 if (++tv == ntv) {
                     tv = 0;
                     ++hv;
                 }
+                if (VAR != V_Q && j + 1 < nt) read_next();
             }
-            // V_Q, V_K: Z and W first (complete well before X and Y)
-            const int g1bar = C::kSingle ? (int)B_ZW_DONE : (int)B_G1_DONE + b;
-            if (!failed) failed = !ew_wait(BAR(g1bar), (j / C::kNB) & 1, abort_flag, bound);
-            // the statistics came with the long-ring stage (bulk copy): observe its barrier too
-            if (C::kStatsRing && !failed)
-                failed = !ew_wait(BAR(B_ST_FULL + (j & 1)), (j >> 1) & 1, abort_flag, bound);
-            else if (C::kColStats && !failed)
-                failed = !ew_wait(BAR(B_L_FULL + s), (j / C::kLS) & 1, abort_flag, bound);
-            if (failed) continue;
-            tc_fence_after();
-            // this group's columns lo .. hi - 1 are inside the tensor and visible
             const int y0 = tile * BN + (int)col0;  // the group's first streamed item
-            int lo = 0, hi = Lcol_s - y0;
-            // scored: does every row of this warp see all 32 columns (one choice per warp),
+            // scored (while the products run): does every row of this warp see all 32 columns (one choice per warp),
             // and if not, which columns this row sees
             bool full = false;
             uint32_t vis = 0xffffffffu;
@@ -1048,6 +1043,18 @@ __device__ __forceinline__ void bwd_body(const Params &p, const unsigned cta) {
                     }
                 }
             }
+            // V_Q, V_K: Z and W first (complete well before X and Y)
+            const int g1bar = C::kSingle ? (int)B_ZW_DONE : (int)B_G1_DONE + b;
+            if (!failed) failed = !ew_wait(BAR(g1bar), (j / C::kNB) & 1, abort_flag, bound);
+            // the statistics came with the long-ring stage (bulk copy): observe its barrier too
+            if (C::kStatsRing && !failed)
+                failed = !ew_wait(BAR(B_ST_FULL + (j & 1)), (j >> 1) & 1, abort_flag, bound);
+            else if (C::kColStats && !failed)
+                failed = !ew_wait(BAR(B_L_FULL + s), (j / C::kLS) & 1, abort_flag, bound);
+            if (failed) continue;
+            tc_fence_after();
+            // this group's columns lo .. hi - 1 are inside the tensor and visible
+            int lo = 0, hi = Lcol_s - y0;
             if (kCausal) {
                 if (VAR == V_Q)
                     hi = min(hi, r0 + row + koff - y0 + 1);  // keys <= query + (Lk - Lq)
