@@ -45,10 +45,11 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
     [n_pos, 64], a row per position) the keys are rotated on the way: channels
     (i, i + 64) by angle i, or (2i, 2i + 1) with ``interleaved``; and ``q``, ``tq``
     (bf16 [H, total, 128], the same rows) are rotated into ``q_out``, ``tq_out``
-    (allocated when omitted).  A page's scale is the smallest power of two
-    that holds its largest value, over the tokens appended to it so far; a
-    page whose first token is among the new ones starts afresh.  Pages that
-    take new tokens must belong to one sequence.  Returns (q_out, tq_out)."""
+    (allocated when omitted; they may be ``q``, ``tq`` themselves).  A page's
+    scale is the smallest power of two that holds its largest value, over the
+    tokens appended to it so far; a page whose first token is among the new
+    ones starts afresh.  Pages that take new tokens must belong to one
+    sequence.  Returns (q_out, tq_out)."""
     n_seq, Hkv, pages, page, width, d, dev = _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a [Hkv, total, d] tensor")
@@ -119,12 +120,13 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
             raise ValueError(f"q is of {q.shape[0]} sequences, the cache of {n_seq}")
     else:
         H, total = q.shape[0], q.shape[1]
-        n, strides = total if max_seqlen is None else int(max_seqlen), (0, *q.stride()[:2])
+        n, strides = total if max_seqlen is None else min(int(max_seqlen), total), (0, *q.stride()[:2])
         _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), _I32, dev)
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"query heads ({H}) must be a multiple of the key heads ({Hkv})")
-    if tq is not None and (not isinstance(tq, torch.Tensor) or tq.shape != q.shape or tq.stride() != q.stride()
-                           or tq.dtype != q.dtype or tq.device != dev):
+    if tq is not None and (not isinstance(tq, torch.Tensor) or tq.shape != q.shape or tq.dtype != q.dtype
+                           or tq.device != dev or tq.stride() != q.stride()
+                           and any(m > 1 and s != t for m, s, t in zip(q.shape, q.stride(), tq.stride()))):
         raise ValueError("tq must have q's shape, strides, type and device")
     if slopes is not None:
         _tensor("slopes", slopes, (H,), _F32, dev)

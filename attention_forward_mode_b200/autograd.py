@@ -44,7 +44,8 @@ class AttnJvpFunction(torch.autograd.Function):
 
 
 class AttnJvpScoredFunction(torch.autograd.Function):
-    """The same with modified scores and shared key heads; slopes and bounds are constants."""
+    """The same with modified scores and shared key heads; slopes and bounds are
+    constants, and the gradients are not differentiable themselves."""
 
     @staticmethod
     def forward(ctx, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end):
@@ -56,6 +57,7 @@ class AttnJvpScoredFunction(torch.autograd.Function):
         return o, to
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout, dtout):
         q, k, v, tq, tk, tv, o, to, lse, mu, slopes, key_begin, key_end = ctx.saved_tensors
         dout = torch.zeros_like(o) if dout is None else dout.to(o.dtype).contiguous()
@@ -71,7 +73,9 @@ def attn_jvp_autograd(q, k, v, tq, tk, tv, scale=None, causal=False, softcap=0.0
     key j visible to query row i iff j <= i + (Lk - Lq).  ``softcap``, ``slopes``,
     ``key_begin`` and ``key_end`` as in ``attn_jvp_fwd_scored`` (constants; bounds and
     ``causal`` exclude each other: ``key_bounds`` combines masks); k, v, tk, tv may
-    have fewer heads, of which q's are a multiple."""
+    have fewer heads, of which q's are a multiple.  To capture forward and
+    backward into a CUDA graph, give leaves that no live eager graph refers to
+    (detached copies): autograd would run their accumulation on the eager stream."""
     if scale is None:
         scale = q.shape[-1] ** -0.5
     bounds = key_begin is not None or key_end is not None

@@ -139,7 +139,7 @@ __device__ __forceinline__ void cap2(const Score &sc, float2 x, float2 &t, float
         cap2(x, sc.cap_in, t, df);
 }
 
-// every score that the warp holds is inside the polynomial's range (false for NaN)
+// every score that the warp holds is inside the polynomial's range (a NaN stays one in either form)
 template <int N>
 __device__ __forceinline__ bool cap_all_small(const Score &sc, const uint32_t (&x)[N]) {
     float m[2] = {0.f, 0.f};
@@ -152,9 +152,10 @@ __device__ __forceinline__ bool cap_all_small(const Score &sc, const uint32_t (&
 }
 
 // [B][n_ktiles] query rows (first, end) that see a key of each 128-key tile,
-// for the key-side kernels; one block per tile.
+// for the key-side kernels; one block per sequence and tile.
 static __global__ void __launch_bounds__(256) query_range_kernel(Score sc, int Lq, int Lk, int2 *out) {
-    const int k0 = (int)blockIdx.x * 128, b = (int)blockIdx.y;
+    const int n_ktiles = (Lk + 127) / 128, b = (int)blockIdx.x / n_ktiles;
+    const int k0 = ((int)blockIdx.x - b * n_ktiles) * 128;
     const int k1 = min(k0 + 128, Lk);
     int first = INT_MAX, end = 0;
     for (int q = (int)threadIdx.x; q < Lq; q += 256) {
@@ -177,7 +178,7 @@ static __global__ void __launch_bounds__(256) query_range_kernel(Score sc, int L
             first = min(first, s_first[w]);
             end = max(end, s_end[w]);
         }
-        out[(size_t)b * gridDim.x + blockIdx.x] = end > 0 ? make_int2(first, end) : make_int2(0, 0);
+        out[blockIdx.x] = end > 0 ? make_int2(first, end) : make_int2(0, 0);
     }
 }
 

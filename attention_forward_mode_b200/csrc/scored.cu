@@ -351,8 +351,7 @@ int attn_jvp_bwd_scored(const void *q, const void *k, const void *v, const void 
     Score score = make_score(z, scale, softcap, slopes, key_begin, key_end);
     if (key_begin || key_end) {
         int2 *const out = reinterpret_cast<int2 *>(ws + stats);
-        query_range_kernel<<<dim3((unsigned)((Lk + 127) / 128), (unsigned)B), 256, 0, st>>>(score, (int)Lq, (int)Lk,
-                                                                                            out);
+        query_range_kernel<<<(unsigned)((Lk + 127) / 128 * B), 256, 0, st>>>(score, (int)Lq, (int)Lk, out);
         if ((e = cudaGetLastError()) != cudaSuccess) return host::fail(e);
         score.qrange = out;
     }

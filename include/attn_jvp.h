@@ -451,8 +451,9 @@ AJVP_API int attn_jvp_fwd_scored_stats(const void *q, const void *k, const void 
  *
  * Two kernels on `stream` (one more with bounds, and one when the key side is
  * split), no atomics.  Gradients of rows that see no key and of keys that no
- * row sees are zero; Lq == 0 writes zeros to dk, dv, dtk, dtv.  Other rules
- * and errors as attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
+ * row sees are zero (all inputs of such rows must be finite, too); Lq == 0
+ * writes zeros to dk, dv, dtk, dtv.  Other rules and errors as
+ * attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
  */
 AJVP_API int attn_jvp_bwd_scored(const void *q, const void *k, const void *v,
                  const void *tq, const void *tk, const void *tv,
@@ -477,7 +478,8 @@ AJVP_API uint64_t attn_jvp_bwd_scored_workspace_bytes(int64_t B, int64_t H, int6
  *                     at positions cache_lens[b], cache_lens[b] + 1, ...
  *   q, tq           : __nv_bfloat16 [H][total][d] queries and their tangents
  *                     of the same tokens, or NULL (tq needs q); rotated into
- *                     q_out, tq_out, same layout (NULL with their input)
+ *                     q_out, tq_out, same layout (NULL with their input; they
+ *                     may be q, tq themselves)
  *   k_cache, v_cache: e4m3 codes [n_pages][Hkv][page][d] (updated)
  *   k_scale, v_scale: float [n_pages][Hkv] (updated); value = code x scale
  *   block_table     : DEVICE int32 [n_seq][table_width]: the page of each run

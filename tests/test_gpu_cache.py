@@ -341,3 +341,43 @@ def test_two_streams_share_a_cache():
     for pair in got:
         for out in pair:
             assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+def test_queries_rotated_in_place():
+    H, Hkv, page = 6, 2, 16
+    g = torch.Generator(device="cuda").manual_seed(31)
+    cos, sin = angles(64)
+    table, pages = tables(3, 4, 1, seed=3)
+    cu = torch.tensor([0, 20, 20, 27], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([5, 9, 30], dtype=torch.int32, device="cuda")
+    q, tq = (torch.randn((H, 30, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn((Hkv, 30, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    for inter in (False, True):
+        two = []
+        for place in (False, True):
+            cache = empty_cache(pages, Hkv, page, seed=2)
+            for t in cache[2:]:
+                t.fill_(1.0)
+            a, b = q.clone(), tq.clone()
+            kw = dict(q_out=a, tq_out=b) if place else dict(q_out=q.clone(), tq_out=tq.clone())
+            two.append(ajvp.attn_jvp_cache_append(k, v, *cache, table.cuda(), lens, cu, q=a, tq=b, cos=cos, sin=sin,
+                                                  interleaved=inter, **kw))
+        assert all(torch.equal(x, y) for x, y in zip(*two))
+        assert torch.equal(two[1][0][:, 27:], q[:, 27:])  # behind the last sequence
+
+
+def test_tangents_of_other_strides_and_a_generous_max_seqlen():
+    """One token per sequence: strides of axes of one element do not matter.  The
+    most tokens of a sequence may be overestimated past all rows."""
+    lens = [40, 7, 100]
+    cache, table, g = filled(3, 2, 16, lens, seed=5)
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q, tq = (torch.randn((3, 1, 4, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    want = ajvp.attn_jvp_fwd_cache(q.transpose(1, 2).contiguous(), tq.transpose(1, 2).contiguous(), *cache, table, lens_d)
+    got = ajvp.attn_jvp_fwd_cache(q.transpose(1, 2), tq.transpose(1, 2).contiguous(), *cache, table, lens_d)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    rows = [x.squeeze(1).transpose(0, 1).contiguous() for x in (q, tq)]  # [H, total, 128]
+    packed = ajvp.attn_jvp_fwd_cache(*rows, *cache, table, lens_d, cu_seqlens=cu, max_seqlen=64)
+    for x, y in zip(packed[:2], want[:2]):
+        assert torch.equal(x, y.squeeze(2).transpose(0, 1))

@@ -295,3 +295,27 @@ def test_larger_shapes_by_the_norm(shape):
         pairs += [(g[n][:, hs if n in ("dq", "dtq") else hk], rg[n]) for n in rg]
         for got, want in pairs:
             assert (got.double() - want).norm() <= ref.U * want.norm()
+
+
+def test_more_sequences_than_a_grid_is_high():
+    """70000 sequences of three rows and three keys, a bound each: as the same rows in batches of 7000."""
+    B, n = 70000, 3
+    inp, cot = make(B, 1, 1, n, n, seed=23)
+    g = torch.Generator().manual_seed(24)
+    end = torch.randint(0, n + 1, (B, n), generator=g).int().cuda()
+    out, grads = run(inp, cot, dict(softcap=10.0, key_end=end))
+    for b in range(0, B, 7000):
+        s = slice(b, b + 7000)
+        part = [{k: x[s].contiguous() for k, x in d.items()} for d in (inp, cot)]
+        o2, g2 = run(*part, dict(softcap=10.0, key_end=end[s].contiguous()))
+        assert all(torch.equal(x[s], y) for x, y in zip(out, o2))
+        assert all(torch.equal(grads[k][s], g2[k]) for k in grads)
+
+
+def test_second_derivatives_are_refused():
+    inp, _ = make(1, 2, 1, 20, 20, seed=25)
+    x = [inp[k].requires_grad_() for k in NAMES]
+    o, to = ajvp.attn_jvp_autograd(*x, softcap=20.0)
+    (dq,) = torch.autograd.grad((o.float().square() + to.float()).sum(), x[:1], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dq.float().sum().backward()
