@@ -55,7 +55,7 @@ from ._binding import (  # noqa: F401
     version,
 )
 
-from ._cache import attn_jvp_cache_append, attn_jvp_fwd_cache  # noqa: E402,F401
+from ._cache import attn_jvp_cache_append, attn_jvp_fwd_cache, fwd_cache_workspace_bytes  # noqa: E402,F401
 from ._scored import (  # noqa: E402,F401
     attn_jvp_bwd_scored,
     attn_jvp_fwd_scored,
@@ -76,5 +76,5 @@ __all__ = [
     "DEFAULT_PERSISTENT_KEY_TILES",
     "set_wait_bound_ns", "strerror", "version", "AttnJvpError",
     "attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored", "bwd_scored_workspace_bytes",
-    "key_bounds", "attn_jvp_cache_append", "attn_jvp_fwd_cache",
+    "key_bounds", "attn_jvp_cache_append", "attn_jvp_fwd_cache", "fwd_cache_workspace_bytes",
 ]

@@ -40,6 +40,7 @@ EXPORTED = (
     "attn_jvp_selftest_wait_timeout",
     "attn_jvp_version", "attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored",
     "attn_jvp_bwd_scored_workspace_bytes", "attn_jvp_cache_append", "attn_jvp_fwd_cache",
+    "attn_jvp_fwd_cache_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -132,8 +133,10 @@ def load_library(path: str = LIB_PATH):
         lib.attn_jvp_bwd_scored_workspace_bytes.restype = ctypes.c_uint64
         lib.attn_jvp_cache_append.argtypes = [vp] * 15 + [i64] * 9 + [ctypes.c_int, vp]
         lib.attn_jvp_cache_append.restype = ctypes.c_int
-        lib.attn_jvp_fwd_cache.argtypes = [vp] * 13 + [i64] * 12 + [f32, f32, ctypes.c_int, vp]
+        lib.attn_jvp_fwd_cache.argtypes = [vp] * 13 + [i64] * 12 + [f32, f32, ctypes.c_int, vp, ctypes.c_uint64, vp]
         lib.attn_jvp_fwd_cache.restype = ctypes.c_int
+        lib.attn_jvp_fwd_cache_workspace_bytes.argtypes = [i64] * 6 + [ctypes.c_int]
+        lib.attn_jvp_fwd_cache_workspace_bytes.restype = ctypes.c_uint64
         lib.attn_jvp_version.argtypes = []
         lib.attn_jvp_version.restype = ctypes.c_int
         _lib = lib

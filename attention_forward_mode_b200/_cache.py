@@ -11,12 +11,14 @@ page of each run of ``page`` tokens of a sequence; nothing needs to be
 initialised before a page's first token is appended."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from ._binding import _check, _ptr, load_library
 from ._scored import _BF16, _F32, _I32, _launch_scope, _tensor, _tensors
 
-__all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache"]
+__all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache", "fwd_cache_workspace_bytes"]
 
 
 def _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens):
@@ -91,9 +93,23 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
     return q_out, tq_out
 
 
+def fwd_cache_workspace_bytes(n_seq: int, H: int, Hkv: int, n: int, page: int, table_width: int,
+                              tangent: bool = True) -> int:
+    """Device workspace with which ``attn_jvp_fwd_cache`` may spread a sequence over
+    more of the current device than a cluster of CTAs (0: it would not)."""
+    return int(load_library().attn_jvp_fwd_cache_workspace_bytes(int(n_seq), int(H), int(Hkv), int(n), int(page),
+                                                                 int(table_width), int(bool(tangent))))
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(n_seq, H, Hkv, n, page, width, tangent, device):
+    """The same, with ``device`` current (part of the key: the size depends on it)."""
+    return fwd_cache_workspace_bytes(n_seq, H, Hkv, n, page, width, tangent)
+
+
 def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_seqlens=None,
                        max_seqlen=None, scale=None, softcap=0.0, slopes=None, causal=True, o=None, to=None, lse=None,
-                       stream=None, want_lse=True):
+                       stream=None, want_lse=True, workspace=None):
     """O, tO, lse of the last query tokens of each sequence over its cached
     keys and values, which carry no tangent: tO is the derivative of O along
     ``tq`` (None: plain attention, and ``to`` is None).
@@ -106,7 +122,10 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
     included: token t of n stands at position cache_lens - n + t and sees the
     keys up to its own (``causal``; rows at negative positions see nothing), or
     every cached key.  ``softcap`` and ``slopes`` modify the scores as in
-    ``attn_jvp_fwd_scored``.  Returns (o, to, lse), contiguous, shaped like q."""
+    ``attn_jvp_fwd_scored``.  ``workspace``: a CUDA uint8 tensor of
+    ``fwd_cache_workspace_bytes`` bytes, through which few long contexts are spread
+    over the whole GPU (allocated per call when omitted; an empty one: do without).
+    Returns (o, to, lse), contiguous, shaped like q."""
     n_seq, Hkv, pages, page, width, d, dev = _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens)
     if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.device != dev \
             or q.dim() != (4 if cu_seqlens is None else 3) or q.shape[-1] != d or q.stride(-1) != 1:
@@ -138,8 +157,13 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
             _tensor(name, x, shape, _BF16, dev)
     if lse is not None:
         _tensor("lse", lse, shape[:-1], _F32, dev)
+    if workspace is not None:
+        _tensor("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
     scope, handle = _launch_scope(stream, dev)
     with scope:
+        if workspace is None:
+            size = _workspace_bytes(n_seq, H, Hkv, n, page, width, tq is not None, dev.index)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
         o = q.new_empty(shape) if o is None else o
         to = q.new_empty(shape) if to is None and tq is not None else to
         lse = q.new_empty(shape[:-1], dtype=_F32) if lse is None and want_lse else lse
@@ -148,7 +172,8 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
             k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(), _ptr(cu_seqlens),
             _ptr(slopes), n_seq, H, Hkv, n,
             total, *strides, pages, page, width, d, float(d ** -0.5 if scale is None else scale),
-            float(softcap or 0.0), int(bool(causal)), handle)
+            float(softcap or 0.0), int(bool(causal)), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            handle)
     if rc:
         _check(rc, "attn_jvp_fwd_cache")
     return o, to, lse

@@ -66,8 +66,24 @@ struct Plan {
     int nt;      // column tiles of a row tile: 4 nt rows with tangents, 8 nt without
     int warps;   // per CTA
     int splits;  // CTAs per unit
+    bool parts;  // they leave their sums in the workspace (else they are one cluster)
 };
 
+uint64_t plan_bytes(const Plan &p, int64_t n_seq, int64_t Hkv) {
+    return p.parts ? (uint64_t)(n_seq * Hkv) * (uint64_t)p.tiles * (uint64_t)p.splits * cache::part_floats(p.nt) * 4u : 0u;
+}
+
+// Time of a plan in microseconds, within about 15 % over 18 shapes on a 148-SM B200:
+// a fixed part, and the runs of 32 tokens of a warp at the latency of one, or those
+// of an SM at its rate.
+double plan_time(const Plan &p, int64_t units, int64_t runs, int sm_count) {
+    const double ctas = (double)((units * p.splits + sm_count - 1) / sm_count);  // of an SM
+    const double of_warp = (double)runs / (p.splits * p.warps);
+    const double latency = p.nt == 1 ? 1.25 : 1.5, rate = p.nt == 1 ? 0.17 : 0.24;
+    return (p.parts ? 8.5 : 7.0) + of_warp * std::max(latency, ctas * p.warps * rate);
+}
+
+// Without a workspace, or where it does not pay, the CTAs of a unit are a cluster.
 // Measured over 18 shapes of 1 .. 64 sequences of 16 .. 32760 tokens, within 10 % of
 // the best of all (nt, warps, splits) on a 148-SM B200 wherever the table is as long
 // as the sequences:
@@ -76,25 +92,54 @@ struct Plan {
 //   8 rows with tangents: 18 against 22 us; 16 sequences of 8 key heads, 5 rows: 92
 //   against 62), so from 64 units on.
 // splits: as many as keep every CTA resident at once (three of four warps per SM, two
-//   of nt 2, a tenth left free for clusters that do not fill their place), while each
-//   warp keeps two runs of 32 tokens (8 sequences of 2048, 12 heads: 1, 2, 4, 8 parts
-//   take 21, 15.5, 13, 21 us).
+//   of nt 2, a tenth left free for clusters that do not fill their place, a quarter by
+//   clusters of 16), while each warp keeps two runs of 32 tokens (8 sequences of 2048,
+//   12 heads: 1, 2, 4, 8 parts take 21, 15.5, 13, 21 us).
 // warps 8: up to an SM's worth of CTAs, where only more warps per SM hide the
 //   latency of a run (one sequence of 4096, 12 heads: 10.5 against 11.8 us); clusters of
 //   them fill no more than some 120 SMs.
-Plan make_plan(int64_t n_seq, int64_t Hkv, int64_t rows, bool tangent, int64_t tokens, int sm_count) {
-    const int64_t one = tangent ? 4 : 8;
-    Plan p;
-    const int64_t wide = n_seq * Hkv * ((rows + 2 * one - 1) / (2 * one));
-    p.nt = rows > one && wide >= 64 ? 2 : 1;
-    p.tiles = (int)((rows + p.nt * one - 1) / (p.nt * one));
-    const int64_t units = n_seq * Hkv * p.tiles, runs = (tokens + 31) / 32;
-    const int64_t most8 = sm_count * 13 / 16;
-    p.warps = p.nt == 1 && units * 8 <= most8 ? 8 : 4;
-    const int64_t most = p.warps == 8 ? most8 : sm_count * (p.nt == 1 ? 3 : 2) * 9 / 10;
+//
+// With a workspace the CTAs of a unit may be any number anywhere.  Long contexts of
+// few sequences then fill the GPU (one sequence of 32760 tokens, 40 heads on 8 key
+// heads, with tangents: 24 against 34 us; 12 heads without: 21 against 29; of 200000
+// tokens, one head: 36 against 73), while short ones gain a microsecond or two of
+// kernel time and lose as much to the second launch, so from a modelled gain of
+// an eighth on.
+Plan make_plan(int64_t n_seq, int64_t Hkv, int64_t rows, bool tangent, int64_t tokens, int sm_count, bool workspace) {
+    const int64_t one = tangent ? 4 : 8, runs = (tokens + 31) / 32;
     const int64_t least = 8;  // runs of a CTA: one per warp of eight, two per warp of four
+    const auto units_of = [&](int nt) -> int64_t { return n_seq * Hkv * ((rows + nt * one - 1) / (nt * one)); };
+    Plan p;
+    p.nt = rows > one && units_of(2) >= 64 ? 2 : 1;
+    const int64_t units = units_of(p.nt);
+    const int64_t most8 = sm_count * 13 / 16, slots = sm_count * (p.nt == 1 ? 3 : 2);
+    p.warps = p.nt == 1 && units * 8 <= most8 ? 8 : 4;
     p.splits = 1;
-    while (p.splits < 16 && units * p.splits * 2 <= most && runs >= least * p.splits * 2) p.splits *= 2;
+    p.parts = false;
+    const auto fits = [&](int64_t splits) -> bool {
+        const int64_t most = p.warps == 8 ? most8 : splits < 16 ? slots * 9 / 10 : slots * 3 / 4;
+        return units * splits <= most && runs >= least * splits;
+    };
+    while (p.splits < 16 && fits(p.splits * 2)) p.splits *= 2;
+    if (workspace) {
+        double best = plan_time(p, units, runs, sm_count) * 0.875;
+        for (int nt = 1; nt <= (rows > one ? 2 : 1); ++nt)
+            for (int ctas = 1; ctas <= (nt == 1 ? 3 : 2); ++ctas) {  // of an SM
+                Plan c;
+                c.nt = nt;
+                c.warps = 4;
+                c.parts = true;
+                const int64_t n = units_of(nt);
+                c.splits = (int)std::min<int64_t>({ctas * sm_count / n, runs / least, cache::MOST_PARTS});
+                if (c.splits < 2) continue;
+                const double t = plan_time(c, n, runs, sm_count);
+                if (t < best) {
+                    best = t;
+                    p = c;
+                }
+            }
+    }
+    p.tiles = (int)(units_of(p.nt) / (n_seq * Hkv));
     return p;
 }
 
@@ -182,12 +227,22 @@ int attn_jvp_cache_append(const void *k, const void *v, const void *q, const voi
     return e == cudaSuccess ? AJVP_OK : host::fail(e);
 }
 
+uint64_t attn_jvp_fwd_cache_workspace_bytes(int64_t n_seq, int64_t H, int64_t Hkv, int64_t n, int64_t page,
+                                            int64_t table_width, int tangent) {
+    if (check_cache(n_seq, H, Hkv, 1, page, table_width, cache::HD) != AJVP_OK || n < 1 || n_seq < 1 || H < 1) return 0;
+    if (n >= kMaxInt || H / Hkv * n >= kMaxInt || n_seq * Hkv >= kMaxInt) return 0;
+    int dev = 0;
+    if (host::device(&dev) != AJVP_OK) return 0;
+    return plan_bytes(make_plan(n_seq, Hkv, H / Hkv * n, tangent != 0, table_width * page, host::sm_count(dev), true),
+                      n_seq, Hkv);
+}
+
 int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *lse, const void *k_cache,
                        const void *v_cache, const float *k_scale, const float *v_scale, const int32_t *block_table,
                        const int32_t *cache_lens, const int32_t *cu_seqlens, const float *slopes, int64_t n_seq,
                        int64_t H, int64_t Hkv, int64_t n, int64_t total, int64_t stride_b, int64_t stride_h,
                        int64_t stride_t, int64_t n_pages, int64_t page, int64_t table_width, int64_t d, float scale,
-                       float softcap, int causal, void *stream) {
+                       float softcap, int causal, void *workspace, uint64_t workspace_bytes, void *stream) {
     int rc = check_cache(n_seq, H, Hkv, n_pages, page, table_width, d);
     if (rc != AJVP_OK) return rc;
     if (n < 0 || total < 0 || !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f)
@@ -208,6 +263,7 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     for (const void *p : {(const void *)k_scale, (const void *)v_scale, (const void *)block_table,
                           (const void *)cache_lens, (const void *)cu_seqlens, (const void *)slopes})
         if (!host::aligned(p, 4)) return AJVP_ERR_MISALIGNED;
+    if (!host::aligned(workspace, 256)) return AJVP_ERR_WORKSPACE;
     const int64_t group = H / Hkv;
     if (group * n >= kMaxInt || n_seq * Hkv >= kMaxInt) return AJVP_ERR_TOO_LARGE;
     if (n_pages < 1) return AJVP_ERR_INVALID_ARG;
@@ -253,7 +309,10 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     if ((rc = host::encode_codes(&p.tm_k, k_cache, n_pages * Hkv * page, 16)) != AJVP_OK) return rc;
     if ((rc = host::encode_codes(&p.tm_v, v_cache, n_pages * Hkv * page, 16)) != AJVP_OK) return rc;
     p.page_magic = page == 16 ? 0u : (unsigned)(((uint64_t(1) << 32) + page / 16 - 1) / (page / 16));
-    const Plan plan = make_plan(n_seq, Hkv, group * n, tq != nullptr, table_width * page, host::sm_count(dev));
+    Plan plan = make_plan(n_seq, Hkv, group * n, tq != nullptr, table_width * page, host::sm_count(dev), true);
+    if (plan.parts && (!workspace || workspace_bytes < plan_bytes(plan, n_seq, Hkv)))
+        plan = make_plan(n_seq, Hkv, group * n, tq != nullptr, table_width * page, host::sm_count(dev), false);
+    p.partial = plan.parts ? static_cast<float *>(workspace) : nullptr;
     p.tiles = plan.tiles;
     p.splits = plan.splits;
 
@@ -265,7 +324,7 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    attr[0].val.clusterDim.x = plan.parts ? 1u : (unsigned)p.splits;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -276,7 +335,18 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
                              : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 1, 4, 2>, p))
                        : (tq ? cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<true, 2, 4, 2>, p)
                              : cudaLaunchKernelEx(&cfg, cache::cache_attn_kernel<false, 2, 4, 2>, p));
-    return e == cudaSuccess ? AJVP_OK : host::fail(e);
+    if (e != cudaSuccess) return host::fail(e);
+    if (!plan.parts) return AJVP_OK;
+    cfg.gridDim = dim3((unsigned)(n_seq * Hkv * plan.tiles * plan.nt * (tq ? 4 : 8)));
+    cfg.blockDim = dim3(32 * cache::JOIN_WARPS);
+    cfg.dynamicSmemBytes = 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const cudaError_t e1 = plan.nt == 1 ? (tq ? cudaLaunchKernelEx(&cfg, cache::cache_join_kernel<true, 1>, p)
+                                              : cudaLaunchKernelEx(&cfg, cache::cache_join_kernel<false, 1>, p))
+                                        : (tq ? cudaLaunchKernelEx(&cfg, cache::cache_join_kernel<true, 2>, p)
+                                              : cudaLaunchKernelEx(&cfg, cache::cache_join_kernel<false, 2>, p));
+    return e1 == cudaSuccess ? AJVP_OK : host::fail(e1);
 }
 
 }  // extern "C"

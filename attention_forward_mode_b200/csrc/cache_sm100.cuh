@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) cache_append_kernel(const _
 // mma.sync rather than tcgen05: 128-row accumulators in tensor memory would be
 // nearly empty, and the products are not what bounds the kernel.  Splits of a
 // sequence are the CTAs of one cluster, which join their sums through distributed
-// shared memory: no workspace, one launch, and a fixed order of additions.
+// shared memory in one launch; or, for long contexts of few sequences, any number of
+// CTAs that leave them in a workspace for a second kernel (make_plan in cache.cu says
+// when).  Either way the order of additions is fixed.
 //
 // Operand ranges: queries and tangents are scaled by a power of two per row so
 // that the largest lies in [1, 2) (bf16 channels are then exact but for those
@@ -343,7 +345,8 @@ struct AttnParams {
     int B, H, Hkv, group, n_pages, page, table_width, causal;
     int n;                        // query tokens per sequence (packed: of the longest)
     int tiles;                    // row tiles per (sequence, key head)
-    int splits;                   // CTAs per cluster
+    int splits;                   // CTAs per unit
+    float *partial;               // NULL: the CTAs of a unit are one cluster; else their sums, for cache_join_kernel
     CUtensorMap tm_k, tm_v;       // codes [rows][128], boxes of 16 rows
     unsigned long long bound_ns;
     unsigned page_magic;          // ceil(2^32 / (page / 16)): x / (page / 16) = umulhi(x, magic); 0 for pages of 16
@@ -362,6 +365,9 @@ __host__ __device__ constexpr int attn_smem(int warps, int stages) {
     return stats_off(warps, stages) + (warps + 1) * ST_FLOATS * 4;
 }
 static_assert(16 * HD * 4 <= STAGE_BYTES, "the sums of a warp fit a stage");
+// a CTA's statistics and sums in a workspace: a unit has 8 nt columns
+__host__ __device__ constexpr int part_floats(int nt) { return ST_FLOATS + 8 * nt * HD; }
+constexpr int MOST_PARTS = 64;
 
 // 2-D tiled load global -> shared, completion counted on `bar` (bytes)
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y) {
@@ -444,6 +450,23 @@ __device__ __forceinline__ int binary_exponent(float x) {
 }
 __device__ __forceinline__ float pow2_or_0(int e) { return e >= -126 ? pow2(e) : 0.f; }
 
+// O, tO and lse of a row, channels 4 d4 .. 4 d4 + 3, from its sums: T is in units
+// of 2^E, and like g relative to r and in units of the tangent row's scaling
+template <bool kTan>
+__device__ __forceinline__ void write_row(const AttnParams &p, size_t out, int d4, float4 so, float4 sT, float lt, float gt,
+                                          float top, int E, float unit) {
+    const float inv = lt > 0.f ? 1.f / lt : 0.f;  // a row that sees no key: zeros, lse = -infinity
+    const float4 ov = make_float4(so.x * inv, so.y * inv, so.z * inv, so.w * inv);
+    *reinterpret_cast<uint2 *>(p.o + out * HD + 4 * d4) = make_uint2(pack_bf16x2(ov.x, ov.y), pack_bf16x2(ov.z, ov.w));
+    if constexpr (kTan) {
+        const float mu = gt * inv, in = pow2(E) * inv;
+        *reinterpret_cast<uint2 *>(p.to + out * HD + 4 * d4) =
+            make_uint2(pack_bf16x2(unit * fmaf(-mu, ov.x, sT.x * in), unit * fmaf(-mu, ov.y, sT.y * in)),
+                       pack_bf16x2(unit * fmaf(-mu, ov.z, sT.z * in), unit * fmaf(-mu, ov.w, sT.w * in)));
+    }
+    if (d4 == 0 && p.lse) p.lse[out] = lt > 0.f ? (top + __log2f(lt)) * 0.69314718055994531f : -INFINITY;
+}
+
 // NT column tiles of 8: with a tangent 4 NT query rows and their tangents, else 8 NT query rows.
 // WARPS x STAGES: 4 x 2 (three CTAs per SM for one column tile, two for two), or
 // 8 x 3 for launches of at most one CTA per SM, where a warp's own copies have to
@@ -454,6 +477,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     constexpr int R = kTan ? 1 : 2;            // query rows per thread and column tile
     constexpr int THREADS = 32 * WARPS, STATS_OFF = stats_off(WARPS, STAGES);
     constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // per warp
+    if (p.partial) asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks wait for this grid's end
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -876,7 +900,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     // each warp's sums into its ring, [columns][128]; its statistics beside them
     float *const mine = reinterpret_cast<float *>(smem + warp * RING_BYTES);
     float *const stats = reinterpret_cast<float *>(smem + STATS_OFF) + warp * ST_FLOATS;
-    float *const cst = reinterpret_cast<float *>(smem + STATS_OFF) + WARPS * ST_FLOATS;  // the CTA's
+    // the CTA's, in shared memory or the workspace
+    float *const part_of = p.partial ? p.partial + (size_t)blockIdx.x * part_floats(NT) : nullptr;
+    float *const cst = part_of ? part_of : reinterpret_cast<float *>(smem + STATS_OFF) + WARPS * ST_FLOATS;
+    float *const csum = part_of ? part_of + ST_FLOATS : reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -904,7 +931,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         }
     }
     __syncthreads();
-    // the CTA's sums, in warp order, into warp 0's ring; its statistics into cst.
+    // the CTA's sums, in warp order, into warp 0's ring (or the workspace); its statistics into cst.
     // T and g of different r: sum p (dS - R) V = sum p (dS - r) V + (r - R) sum p V
     const float *const st = reinterpret_cast<const float *>(smem + STATS_OFF);
     for (int x = threadIdx.x; x < ROWS * HD / 4; x += THREADS) {
@@ -942,8 +969,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             }
         }
         // (each place of warp 0's ring is read and written by this thread alone)
-        *reinterpret_cast<float4 *>(smem + oc * 4) = so;
-        if constexpr (kTan) *reinterpret_cast<float4 *>(smem + (oc + HD) * 4) = sT;
+        *reinterpret_cast<float4 *>(csum + oc) = so;
+        if constexpr (kTan) *reinterpret_cast<float4 *>(csum + oc + HD) = sT;
         if (d4 == 0) {
             cst[ST_M + row] = top;
             cst[ST_L + row] = lt;
@@ -954,6 +981,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             }
         }
     }
+    if (part_of) return;  // cache_join_kernel goes on
     auto cluster_sync = [&]() {
         if (p.splits > 1)
             asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1009,22 +1037,98 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                 axpy(sT, f * (dr * pow2(-Et)), o4);
             }
         }
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;  // a row that sees no key: zeros, lse = -infinity
-        const float4 ov = make_float4(so.x * inv, so.y * inv, so.z * inv, so.w * inv);
         const int h = hk * p.group + r / n, t = r % n;
-        const size_t out = (size_t)(p.o_b * b + p.o_h * h + first + t);
-        *reinterpret_cast<uint2 *>(p.o + out * HD + 4 * d4) = make_uint2(pack_bf16x2(ov.x, ov.y), pack_bf16x2(ov.z, ov.w));
-        if constexpr (kTan) {
-            // T is in units of 2^E, and like g relative to r and in the tangent row's units
-            const float mu = gt * inv, in = pow2(Et) * inv, unit = cst[ST_UNIT + row];
-            *reinterpret_cast<uint2 *>(p.to + out * HD + 4 * d4) =
-                make_uint2(pack_bf16x2(unit * fmaf(-mu, ov.x, sT.x * in), unit * fmaf(-mu, ov.y, sT.y * in)),
-                           pack_bf16x2(unit * fmaf(-mu, ov.z, sT.z * in), unit * fmaf(-mu, ov.w, sT.w * in)));
-        }
-        if (d4 == 0 && p.lse)
-            p.lse[out] = lt > 0.f ? (top + __log2f(lt)) * 0.69314718055994531f : -INFINITY;
+        write_row<kTan>(p, (size_t)(p.o_b * b + p.o_h * h + first + t), d4, so, sT, lt, gt, top, Et,
+                        kTan ? cst[ST_UNIT + row] : 0.f);
     }
     cluster_sync();  // no CTA leaves while another still reads its sums
+}
+
+// Joins the parts that the CTAs of a unit left in the workspace: a block per
+// query row, a lane per four channels, a warp per eighth of the parts; added up
+// in a fixed order.  Launched beside the attention kernel, whose end it waits for.
+constexpr int JOIN_WARPS = 8;
+template <bool kTan, int NT>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) cache_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int ROWS = (kTan ? 4 : 8) * NT, PART = part_floats(NT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = (int)blockIdx.x % ROWS, unit = (int)blockIdx.x / ROWS;
+    const int tile = unit % p.tiles, bh = unit / p.tiles;
+    const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+    int n = p.n, first = 0;
+    if (p.cu) {
+        first = min(max(p.cu[b], 0), p.total);
+        n = min(max(min(max(p.cu[b + 1], 0), p.total) - first, 0), p.n);
+    }
+    const int r = tile * ROWS + row;
+    if (r >= p.group * n) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float *const parts = p.partial + (size_t)unit * p.splits * PART;
+    float top = -INFINITY, Rt = 0.f;
+    float ms[MOST_PARTS / 32], rs[MOST_PARTS / 32];
+    int es[MOST_PARTS / 32], Et = EW_MIN;
+#pragma unroll
+    for (int i = 0; i < MOST_PARTS / 32; ++i) {
+        const int s = 32 * i + lane;
+        const float *const a = parts + (size_t)s * PART;
+        ms[i] = s < p.splits ? a[ST_M + row] : -INFINITY;
+        rs[i] = kTan && s < p.splits ? a[ST_R + row] : 0.f;
+        es[i] = kTan && s < p.splits ? __float_as_int(a[ST_E + row]) : EW_MIN;
+    }
+#pragma unroll
+    for (int i = 0; i < MOST_PARTS / 32; ++i) {  // the largest reference, and r of the first part that has it
+        float m = ms[i];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (m > top) {
+            top = m;
+            Rt = __shfl_sync(0xffffffffu, rs[i], __ffs(__ballot_sync(0xffffffffu, ms[i] == m)) - 1);
+        }
+    }
+    if constexpr (kTan) {
+#pragma unroll
+        for (int i = 0; i < MOST_PARTS / 32; ++i)
+            Et = max(Et, __reduce_max_sync(0xffffffffu, 32 * i + lane < p.splits
+                                                            ? max(es[i], binary_exponent(rs[i] - Rt)) : EW_MIN));
+    }
+    float4 so = make_float4(0.f, 0.f, 0.f, 0.f), sT = so;
+    float lt = 0.f, gt = 0.f;
+#pragma unroll 4
+    for (int s = warp; s < p.splits; s += JOIN_WARPS) {
+        const float *const a = parts + (size_t)s * PART;
+        const float *const v = a + ST_FLOATS + (kTan ? 2 * row : row) * HD + 4 * lane;
+        const float4 o4 = *reinterpret_cast<const float4 *>(v);
+        const float f = ref_weight(a[ST_M + row], top);
+        lt = fmaf(f, a[ST_L + row], lt);
+        axpy(so, f, o4);
+        if constexpr (kTan) {
+            const float4 t4 = *reinterpret_cast<const float4 *>(v + HD);
+            const float dr = a[ST_R + row] - Rt;
+            gt = fmaf(f, fmaf(dr, a[ST_L + row], a[ST_G + row]), gt);
+            axpy(sT, f * pow2_or_0(__float_as_int(a[ST_E + row]) - Et), t4);
+            axpy(sT, f * (dr * pow2(-Et)), o4);
+        }
+    }
+    __shared__ float4 s_o[JOIN_WARPS][32], s_t[JOIN_WARPS][32];
+    __shared__ float s_l[JOIN_WARPS], s_g[JOIN_WARPS];
+    s_o[warp][lane] = so;
+    if constexpr (kTan) s_t[warp][lane] = sT;
+    if (lane == 0) {
+        s_l[warp] = lt;
+        s_g[warp] = gt;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < JOIN_WARPS; ++w) {
+        axpy(so, 1.f, s_o[w][lane]);
+        if constexpr (kTan) axpy(sT, 1.f, s_t[w][lane]);
+        lt += s_l[w];
+        gt += s_g[w];
+    }
+    const int h = hk * p.group + r / n, t = r % n;
+    write_row<kTan>(p, (size_t)(p.o_b * b + p.o_h * h + first + t), lane, so, sT, lt, gt, top, Et,
+                    kTan ? parts[ST_UNIT + row] : 0.f);
 }
 
 }  // namespace cache

@@ -543,15 +543,26 @@ AJVP_API int attn_jvp_cache_append(const void *k, const void *v, const void *q, 
  * Meant for decoding: query heads sharing a key head and their tokens are taken
  * eight (with tangents) or sixteen rows at a time, and every such tile reads the
  * sequence's codes again.  Supported: d == 128, sizes as attn_jvp_cache_append,
- * strides multiples of 8 elements; one kernel, no workspace, deterministic.
- * Errors as attn_jvp_fwd.
+ * strides multiples of 8 elements.  With `workspace` (DEVICE memory, 256-byte
+ * aligned) of attn_jvp_fwd_cache_workspace_bytes(...) bytes, long contexts of few
+ * sequences may be spread over the whole GPU and joined by a second kernel;
+ * with less (NULL, 0: none) one kernel spreads a sequence over one cluster of CTAs.
+ * Deterministic for a given choice; errors as attn_jvp_fwd, plus
+ * AJVP_ERR_WORKSPACE (a misaligned workspace).
  */
 AJVP_API int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *lse,
                  const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
                  const int32_t *block_table, const int32_t *cache_lens, const int32_t *cu_seqlens,
                  const float *slopes, int64_t n_seq, int64_t H, int64_t Hkv, int64_t n, int64_t total,
                  int64_t stride_b, int64_t stride_h, int64_t stride_t, int64_t n_pages, int64_t page,
-                 int64_t table_width, int64_t d, float scale, float softcap, int causal, void *stream);
+                 int64_t table_width, int64_t d, float scale, float softcap, int causal,
+                 void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Device workspace, in bytes, with which attn_jvp_fwd_cache may spread its
+ * sequences further on the current device (0: it would not, or invalid sizes, or
+ * no usable device).  tangent: whether tq is given. */
+AJVP_API uint64_t attn_jvp_fwd_cache_workspace_bytes(int64_t n_seq, int64_t H, int64_t Hkv, int64_t n, int64_t page,
+                                                     int64_t table_width, int tangent);
 
 /*
  * attn_jvp_bwd_host -- attn_jvp_bwd on HOST buffers: every tensor argument

@@ -137,9 +137,13 @@ def test_attention_over_the_cache(case):
                                          causal=causal)
     want = ref.attention(list(q), list(tq) if tangent else None, *cache, table, lens, 128 ** -0.5, cap, slopes, causal)
     torch.cuda.synchronize()
+    check_rows(o, to, lse, want)
+
+
+def check_rows(o, to, lse, want):
     for b, (ro, rto, rlse, bo, bto) in enumerate(want):
         assert ((o[b].double() - ro).abs() <= bo).all(), (b, ((o[b].double() - ro).abs() / bo).max())
-        if tangent:
+        if to is not None:
             assert ((to[b].double() - rto).abs() <= bto).all(), (b, ((to[b].double() - rto).abs() / bto).max())
         rlse = rlse.cuda()
         empty = torch.isinf(rlse)
@@ -147,6 +151,44 @@ def test_attention_over_the_cache(case):
         # fp32 scores of 128 products (2^-17 absolute here), the cap's tanh c 2^-21
         tol = 2.0 ** -15 * (1.0 + rlse[~empty].abs())
         assert ((lse[b][~empty].double() - rlse[~empty]).abs() <= tol).all()
+
+
+LONG = [  # as ATTN; spread over the GPU through a workspace
+    (1, 1, 1, 64, [32760], 30.0, True, True, True),
+    (10, 2, 3, 32, [32000, 77, 0], 0.0, True, True, True),
+    (16, 1, 1, 48, [30001, 4], 20.0, False, False, False),
+    (40, 8, 1, 64, [17001], 0.0, False, True, True),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_long_contexts_through_a_workspace(case):
+    H, Hkv, n, page, lens, cap, bias, tangent, causal = case
+    cache, table, g = filled(len(lens), Hkv, page, lens, seed=sum(lens))
+    q, tq = (torch.randn((len(lens), H, n, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    slopes = torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], device="cuda") if bias else None
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    size = ajvp.fwd_cache_workspace_bytes(len(lens), H, Hkv, n, page, table.shape[1], tangent)
+    assert size > 0
+    ws = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
+    kw = dict(softcap=cap, slopes=slopes, causal=causal)
+    call = lambda w: ajvp.attn_jvp_fwd_cache(q, tq if tangent else None, *cache, table, lens_d, workspace=w, **kw)  # noqa: E731
+    want = ref.attention(list(q), list(tq) if tangent else None, *cache, table, lens, 128 ** -0.5, cap, slopes, causal)
+    first = call(ws)
+    torch.cuda.synchronize()
+    assert (ws[size:] == 255).all()  # nothing behind it is written
+    check_rows(*first, want)
+    check_rows(*call(ws[: size // 2 // 256 * 256]), want)  # too small to be of use
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        again = call(None)
+    for _ in range(3):
+        for x in again:
+            if x is not None:
+                x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(x is y is None or torch.equal(x, y) for x, y in zip(first, again))
 
 
 def test_pages_that_do_not_exist_and_ends_inside_tiles():

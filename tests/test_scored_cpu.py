@@ -166,14 +166,18 @@ def test_cache_refusals(lib):
     assert append(ptr=None, total=0) == B.AJVP_OK and append(ptr=None, n_seq=0) == B.AJVP_OK
 
     def attn(ptr=p, tq=None, to=None, cu=None, n_seq=1, H=2, Hkv=2, n=1, total=0, sb=256, sh=128, st=128, page=16, cap=0.0,
-             pages=4, scale=0.1):
+             pages=4, scale=0.1, ws=None):
         return lib.attn_jvp_fwd_cache(ptr, tq, ptr, to, None, ptr, ptr, ptr, ptr, ptr, ptr, cu, None, n_seq, H, Hkv, n,
-                                      total, sb, sh, st, pages, page, 2, 128, scale, cap, 1, None)
+                                      total, sb, sh, st, pages, page, 2, 128, scale, cap, 1, ws, 0, None)
 
     assert attn(tq=p) == inv and attn(to=p) == inv and attn(cu=p, n=4, total=3) == inv and attn(n=-1) == inv
     assert attn(cap=-1.0) == inv and attn(scale=float("nan")) == inv and attn(H=3) == inv and attn(pages=0) == inv
     assert attn(sh=100) == B.AJVP_ERR_MISALIGNED and attn(ptr=ctypes.c_void_p(24)) == B.AJVP_ERR_MISALIGNED
     assert attn(n=1 << 31) == big and attn(ptr=None) == inv
+    assert attn(ws=ctypes.c_void_p(64)) == B.AJVP_ERR_WORKSPACE
+    size = lib.attn_jvp_fwd_cache_workspace_bytes
+    assert size(1, 3, 2, 1, 16, 9, 1) == 0 and size(1, 2, 2, 1, 24, 9, 1) == 0 and size(-1, 2, 2, 1, 16, 9, 0) == 0
+    assert size(0, 2, 2, 1, 16, 9, 1) == 0 and size(1, 2, 2, 0, 16, 9, 1) == 0
     assert attn(ptr=None, n=0) == B.AJVP_OK and attn(ptr=None, n_seq=0) == B.AJVP_OK
 
 
