@@ -136,16 +136,14 @@ struct Params {
 };
 
 // {lse log2(e), mu, a, D} per query row; one warp per row, 4 features per lane.
-static __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const __nv_bfloat16 *__restrict__ o,
-                                                           const __nv_bfloat16 *__restrict__ to,
-                                                           const __nv_bfloat16 *__restrict__ dout,
-                                                           const __nv_bfloat16 *__restrict__ dtout,
-                                                           const float *__restrict__ lse,
-                                                           const float *__restrict__ mu, float4 *__restrict__ stats,
-                                                           long long rows) {
+__device__ __forceinline__ void bwd_rowstats(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ to,
+                                             const __nv_bfloat16 *__restrict__ dout,
+                                             const __nv_bfloat16 *__restrict__ dtout, const float *__restrict__ lse,
+                                             const float *__restrict__ mu, float4 *__restrict__ stats, long long rows,
+                                             unsigned block, unsigned blocks) {
     const int lane = threadIdx.x & 31;
-    const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
-    for (long long r = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
+    const long long warps = (long long)blocks * (blockDim.x >> 5);
+    for (long long r = (long long)block * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
         const size_t off = (size_t)r * HD + 4 * lane;
         const uint2 uo = *reinterpret_cast<const uint2 *>(o + off);
         const uint2 ut = *reinterpret_cast<const uint2 *>(to + off);
@@ -172,6 +170,32 @@ static __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const __nv_bfl
             stats[r] = make_float4(lse[r] * 1.4426950408889634f, m, a, b - a * m);
         }
     }
+}
+static __global__ void __launch_bounds__(256) bwd_rowstats_kernel(const __nv_bfloat16 *__restrict__ o,
+                                                           const __nv_bfloat16 *__restrict__ to,
+                                                           const __nv_bfloat16 *__restrict__ dout,
+                                                           const __nv_bfloat16 *__restrict__ dtout,
+                                                           const float *__restrict__ lse,
+                                                           const float *__restrict__ mu, float4 *__restrict__ stats,
+                                                           long long rows) {
+    bwd_rowstats(o, to, dout, dtout, lse, mu, stats, rows, blockIdx.x, gridDim.x);
+}
+// Scored: the same, and the query ranges of the key tiles, in one launch (the
+// first n_ranges blocks take a key tile each, the others rows; in two launches
+// the whole pass over 12 heads of 1999 takes 212 instead of 210 us, with cold caches
+// 231 instead of 227).  The gradient kernel as a programmatic dependent of this
+// one measured 225 us, and 1 % faster only without bounds.
+static __global__ void __launch_bounds__(256) scored_prep_kernel(const __nv_bfloat16 *__restrict__ o,
+                                                          const __nv_bfloat16 *__restrict__ to,
+                                                          const __nv_bfloat16 *__restrict__ dout,
+                                                          const __nv_bfloat16 *__restrict__ dtout,
+                                                          const float *__restrict__ lse, const float *__restrict__ mu,
+                                                          float4 *__restrict__ stats, long long rows, unsigned n_ranges,
+                                                          Score sc, int Lq, int Lk, int2 *ranges) {
+    if (blockIdx.x < n_ranges)
+        query_range(sc, Lq, Lk, ranges, (int)blockIdx.x);
+    else
+        bwd_rowstats(o, to, dout, dtout, lse, mu, stats, rows, blockIdx.x - n_ranges, gridDim.x - n_ranges);
 }
 
 // Sum of the split parts' fp32 partial sums, in part order, times the

@@ -152,18 +152,22 @@ __device__ __forceinline__ bool cap_all_small(const Score &sc, const uint32_t (&
 }
 
 // [B][n_ktiles] query rows (first, end) that see a key of each 128-key tile,
-// for the key-side kernels; one block per sequence and tile.
-static __global__ void __launch_bounds__(256) query_range_kernel(Score sc, int Lq, int Lk, int2 *out) {
-    const int n_ktiles = (Lk + 127) / 128, b = (int)blockIdx.x / n_ktiles;
-    const int k0 = ((int)blockIdx.x - b * n_ktiles) * 128;
+// for the key-side kernels; a block of 256 threads calls it per sequence and tile (`index`).
+__device__ __forceinline__ void query_range(const Score &sc, int Lq, int Lk, int2 *out, int index) {
+    const int n_ktiles = (Lk + 127) / 128, b = index / n_ktiles;
+    const int k0 = (index - b * n_ktiles) * 128;
     const int k1 = min(k0 + 128, Lk);
     int first = INT_MAX, end = 0;
-    for (int q = (int)threadIdx.x; q < Lq; q += 256) {
-        const int2 r = row_bounds(sc, b, q, Lq, Lk);
-        if (max(r.x, k0) < min(r.y, k1)) {
-            first = min(first, q);
-            end = q + 1;
-        }
+    for (int q = (int)threadIdx.x; q < Lq; q += 256 * 8) {  // eight rows' loads under way at once
+        int2 r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = row_bounds(sc, b, q + 256 * i, Lq, Lk);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (max(r[i].x, k0) < min(r[i].y, k1)) {
+                first = min(first, q + 256 * i);
+                end = q + 256 * i + 1;
+            }
     }
     __shared__ int s_first[8], s_end[8];
     first = __reduce_min_sync(0xffffffffu, first);
@@ -178,7 +182,7 @@ static __global__ void __launch_bounds__(256) query_range_kernel(Score sc, int L
             first = min(first, s_first[w]);
             end = max(end, s_end[w]);
         }
-        out[blockIdx.x] = end > 0 ? make_int2(first, end) : make_int2(0, 0);
+        out[index] = end > 0 ? make_int2(first, end) : make_int2(0, 0);
     }
 }
 

@@ -342,19 +342,12 @@ int attn_jvp_bwd_scored(const void *q, const void *k, const void *v, const void 
     float *const partial_v = reinterpret_cast<float *>(ws + stats + ranges + part_bytes);
 
     const long long rows = (long long)(BH * Lq);
-    bwd::bwd_rowstats_kernel<<<(unsigned)std::min<long long>((rows + 7) / 8, 148LL * 16), 256, 0, st>>>(
-        static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(to),
-        static_cast<const __nv_bfloat16 *>(dout), static_cast<const __nv_bfloat16 *>(dtout), lse, mu,
-        static_cast<float4 *>(workspace), rows);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return host::fail(e);
-    Score score = make_score(z, scale, softcap, slopes, key_begin, key_end);
-    if (key_begin || key_end) {
-        int2 *const out = reinterpret_cast<int2 *>(ws + stats);
-        query_range_kernel<<<(unsigned)((Lk + 127) / 128 * B), 256, 0, st>>>(score, (int)Lq, (int)Lk, out);
-        if ((e = cudaGetLastError()) != cudaSuccess) return host::fail(e);
-        score.qrange = out;
-    }
+    const unsigned n_stats = (unsigned)std::min<long long>((rows + 7) / 8, 148LL * 16);
+    const int64_t n_ranges = key_begin || key_end ? (Lk + 127) / 128 * B : 0;
+    const Score bounds = make_score(z, scale, softcap, slopes, key_begin, key_end);
+    Score score = bounds;
+    int2 *const range_out = reinterpret_cast<int2 *>(ws + stats);
+    if (n_ranges > 0) score.qrange = range_out;
     bwd::ParamsAll p;
     if ((rc = bwd_params(&p.k, {k, tk, v, tv}, {q, tq}, {dtout, dout}, dk, dtk, scale, score, workspace, BHk, BH, Lk, Lq,
                          Lq, scale, parts, partial_k)) != AJVP_OK)
@@ -369,6 +362,19 @@ int attn_jvp_bwd_scored(const void *q, const void *k, const void *v, const void 
     if (2 * n_key + n_query >= (int64_t(1) << 31)) return AJVP_ERR_TOO_LARGE;
     p.n_k = (unsigned)n_key;
     p.n_q = (unsigned)n_query;
+    const auto *const ob = static_cast<const __nv_bfloat16 *>(o), *const tob = static_cast<const __nv_bfloat16 *>(to);
+    const auto *const db = static_cast<const __nv_bfloat16 *>(dout);
+    const auto *const dtb = static_cast<const __nv_bfloat16 *>(dtout);
+    if (n_ranges > 0)
+        bwd::scored_prep_kernel<<<n_stats + (unsigned)n_ranges, 256, 0, st>>>(ob, tob, db, dtb, lse, mu,
+                                                                              static_cast<float4 *>(workspace), rows,
+                                                                              (unsigned)n_ranges, bounds, (int)Lq,
+                                                                              (int)Lk, range_out);
+    else
+        bwd::bwd_rowstats_kernel<<<n_stats, 256, 0, st>>>(ob, tob, db, dtb, lse, mu, static_cast<float4 *>(workspace),
+                                                          rows);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host::fail(e);
     rc = with_mask(mask_bits(softcap, slopes), [&](auto mask) -> int {
         constexpr int M = decltype(mask)::value;
         const dim3 grid((unsigned)(2 * n_key + n_query));

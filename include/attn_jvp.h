@@ -449,8 +449,7 @@ AJVP_API int attn_jvp_fwd_scored_stats(const void *q, const void *k, const void 
  *                         8 B ceil(Lk / 128) bytes, each rounded up to a
  *                         multiple of 256, run it unsplit.
  *
- * Two kernels on `stream` (one more with bounds, and one when the key side is
- * split), no atomics.  Gradients of rows that see no key and of keys that no
+ * Two kernels on `stream` (three when the key side is split), no atomics.  Gradients of rows that see no key and of keys that no
  * row sees are zero (all inputs of such rows must be finite, too); Lq == 0
  * writes zeros to dk, dv, dtk, dtv.  Other rules and errors as
  * attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
