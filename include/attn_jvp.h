@@ -20,7 +20,11 @@
  * (cross-attention); attn_jvp_fwd_causal and attn_jvp_fwd_varlen add a
  * causal mask and packed variable-length sequences, attn_jvp_bwd the
  * backward pass (attn_jvp_bwd_causal and attn_jvp_bwd_varlen those of the
- * masked forwards).  s is a constant (no derivative with respect to it).
+ * masked forwards).  attn_jvp_fwd_scored and attn_jvp_bwd_scored modify the
+ * scores (tanh cap, distance bias), mask by an interval of keys per row and
+ * share key heads; attn_jvp_cache_append and attn_jvp_fwd_cache keep keys and
+ * values in a paged 8-bit cache and attend over it.  s is a constant (no
+ * derivative with respect to it).
  *
  * Layout: every tensor is a contiguous row-major [B][H][L][d] array (the
  * layout of a PyTorch [B, H, L, d] tensor); the tangents tQ, tK, tV share the
@@ -34,7 +38,7 @@
  * are stream-ordered and asynchronous: they return
  * after enqueueing work on `stream` (a cudaStream_t; NULL = legacy default
  * stream) and do not synchronise.  The device-buffer calls enqueue kernels
- * only (attn_jvp_bwd with Lq == 0: memsets), so after one eager call on a
+ * only (attn_jvp_bwd and attn_jvp_bwd_scored with Lq == 0: memsets), so after one eager call on a
  * device (which does its one-time set-up) they can be captured into a CUDA
  * graph.  Calls are thread-safe.  Inputs must not alias outputs.  Non-finite
  * inputs give unspecified (but memory-safe) results.
