@@ -42,7 +42,7 @@
 // values the other still has to read.  They are the A operands of the
 // second MMA pair: 16 keys = 8 TMEM columns per K-step.
 //
-// Persistent form (kPersist, unmasked bf16 only; chosen for short key
+// Persistent form (kPersist, unmasked bf16; chosen for short key
 // sequences such as cross-attention to a few hundred text tokens, where a CTA
 // runs only a handful of key tiles): one CTA per SM walks the units
 // (query tile, batch*head) blockIdx.x, blockIdx.x + gridDim.x, ..., and every
@@ -55,6 +55,20 @@
 // epilogue; the producer loads unit n+1's first V tiles once the stores have
 // read the staging (B_STG_FREE), and the next unit's first P.V waits for the
 // epilogue to have read O / T (B_OT_FREE).
+//
+// Scored form (MASK_SCORED, always persistent): units differ several times in
+// key tiles, so each role counts units and tiles as it goes, and a warp of its
+// own (warp 3) prepares the next unit: near the end of each it asks the hardware's
+// launch control for a CTA that has not started, reads that unit's bounds and
+// leaves a descriptor {query tile, head, first key, key tiles} that every role
+// waits for.  So a unit's bounds, first copies and first score products run
+// under the previous unit's last products and epilogue.  O and tO are staged in
+// the two V-side stages, O in the one of the next unit's first V tile, and stored by
+// warp 2.  As one CTA per unit a unit of 15 tiles spent a third of its time on its
+// two ends (8 of 24 us); against that form (cold caches, 148 SMs): 2 x 12 heads of 4096
+// in documents 153 -> 140 us, 12 heads of 8190 under a frame mask with cap and bias
+// 574 -> 558, 12 heads of 2501 under a prefix mask 72.7 -> 70.7; a call of a few tiles
+// takes 0.8 us longer.
 #pragma once
 
 #include <type_traits>
@@ -99,6 +113,39 @@ constexpr uint32_t SM_BAR_P = SM_VT + VSTAGES_P * VT_STAGE;
 constexpr uint32_t SM_XCH_P = SM_BAR_P + 256;
 constexpr uint32_t SMEM_BYTES_P = SM_XCH_P + 2 * 2 * 128 * 4;
 static_assert(SMEM_BYTES_P <= 232448, "dynamic shared memory above the sm_100 per-CTA limit");
+
+// Scored form (persistent, units handed out by the hardware): barriers, the
+// launch control's answer, two descriptors {qt, bh, first key, key tiles} of the
+// units in hand and their rows' bounds, in place of the staging slots
+constexpr uint32_t OFF_CLC = 0;          // the answer has arrived
+constexpr uint32_t OFF_ASK = 8;          // the producer is near the end of its unit
+constexpr uint32_t OFF_UNIT_FULL = 16;   // + 8 slot: descriptor written
+constexpr uint32_t OFF_UNIT_FREE = 32;   // + 8 slot: read by every role
+constexpr uint32_t OFF_STG_TO = 48;      // tO staged (O: B_STG_FULL)
+constexpr uint32_t OFF_ANSWER = 64;
+constexpr uint32_t OFF_UNIT = 96;        // + 16 slot
+constexpr uint32_t OFF_BOUNDS = 1024;    // + 1024 slot: int2 per row
+constexpr uint32_t UNIT_READERS = 3 + SOFTMAX_THREADS / 32;  // producer, MMA issuer, storer, softmax warps
+
+// Asks for a CTA that has not started, to run its unit in this one: the answer
+// (16 bytes) arrives at `addr`, counted on `bar`.
+__device__ __forceinline__ void clc_try_cancel(uint32_t addr, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(addr),
+                 "r"(bar)
+                 : "memory");
+}
+// its index, or -1: every CTA has started
+__device__ __forceinline__ int clc_answer(uint32_t addr) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\tld.shared.b128 a, [%1];\n\tmov.b32 %0, -1;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+        : "=r"(x)
+        : "r"(addr)
+        : "memory");
+    return x;
+}
 
 // barrier slots (8 bytes each).  Two MMA commits per key tile:
 //   B_SD_FULL[j % 2]  S_j / dS'_j complete: the softmax may read them, and
@@ -181,7 +228,7 @@ __device__ __forceinline__ void store_rows_32x32(uint32_t slot, const uint32_t (
 // [H][total][128] and sequence b owns rows cu_q[b] .. cu_q[b+1]-1 (queries)
 // and cu_k[b] .. cu_k[b+1]-1 (keys).  Rows with no visible key give zeros and
 // lse = -inf.  MASK_SCORED (score_sm100.cuh): the score modifications, shared
-// key heads, and an interval of visible keys per query row; a CTA streams the
+// key heads, and an interval of visible keys per query row; a unit streams the
 // key tiles between its rows' smallest and largest visible key.
 constexpr int MASK_CAUSAL = 1, MASK_PACKED = 2;
 
@@ -200,21 +247,24 @@ constexpr int MASK_CAUSAL = 1, MASK_PACKED = 2;
 //                 fold and in the epilogue.
 template <bool kSplit, int MASK = 0, bool kPersist = false>
 __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_constant__ Params p) {
-    static_assert(!kPersist || (!kSplit && MASK == 0), "the persistent form is the unmasked bf16 kernel");
     constexpr bool kCausal = (MASK & MASK_CAUSAL) != 0, kPacked = (MASK & MASK_PACKED) != 0;
     constexpr bool kScored = (MASK & MASK_SCORED) != 0, kCap = (MASK & MASK_CAP) != 0, kBias = (MASK & MASK_BIAS) != 0;
     static_assert(!kScored || (!kSplit && !kCausal && !kPacked), "the scored form is a dense bf16 kernel");
     constexpr bool kFixed = (MASK & MASK_FIXED) != 0;
     static_assert(kScored || (!kCap && !kBias), "caps and biases belong to the scored form");
     static_assert(!kFixed || kCap, "a fixed reference needs bounded scores");
+    // the scored form is persistent, too, but its units differ in key tiles: each role
+    // counts units and tiles as it goes, and a warp of its own fetches the next unit
+    static_assert(kPersist ? !kSplit && (MASK == 0 || kScored) : !kScored, "forms that are not built");
+    constexpr bool kEven = kPersist && !kScored;  // every unit has nk key tiles
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     // V-side ring depth, barrier area and exchange area of this form
-    constexpr int VST = kPersist ? VSTAGES_P : STAGES;
-    constexpr uint32_t kBar = kPersist ? SM_BAR_P : SM_BAR, kXch = kPersist ? SM_XCH_P : SM_XCH;
-    if (kPersist && base != raw) {  // its layout leaves no alignment slack
+    constexpr int VST = kEven ? VSTAGES_P : STAGES;
+    constexpr uint32_t kBar = kEven ? SM_BAR_P : SM_BAR, kXch = kEven ? SM_XCH_P : SM_XCH;
+    if (kEven && base != raw) {  // its layout leaves no alignment slack
         if (threadIdx.x == 0) atomicOr(&g_status_word, 2);
         return;
     }
@@ -278,13 +328,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         yk0 = k0;
         Lk_s = k1 - k0;
     } else if (kScored) {
-        // groups of heads whose keys fit the L2 together; in a group the late query tiles of
-        // all heads first, the heavy ones under prefix and frame-causal masks
-        const int g = (int)blockIdx.x / (p.n_qtiles * p.score.slabs);
-        const int in = (int)blockIdx.x - g * p.n_qtiles * p.score.slabs;
-        const int n = min(p.score.slabs, p.BH - g * p.score.slabs);
-        bh = g * p.score.slabs + in % n;
-        qt = p.n_qtiles - 1 - in / n;
+        qt = bh = 0;  // (each role learns its units from the descriptors)
     } else if (kCausal) {
         bh = blockIdx.x % p.BH;
         qt = p.n_qtiles - 1 - blockIdx.x / p.BH;  // heavy (late) query tiles first
@@ -292,32 +336,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         qt = blockIdx.x % p.n_qtiles;
         bh = blockIdx.x / p.n_qtiles;
     }
-    const int q0 = qt * BR;
-    const int yq = yq0 + q0;
+    int q0 = qt * BR;
+    int yq = yq0 + q0;
     if (kPacked && q0 >= Lq_s) return;  // past the end of this sequence (uniform for the CTA)
     const int koff = Lk_s - Lq_s;        // causal offset of the diagonal
     int kend = Lk_s;                     // keys any row of this tile may see
     if (kCausal) kend = max(0, min(Lk_s, q0 + BR + koff));
     int kbase = 0;    // scored: the first streamed key, a multiple of the tile
     int bh_kv = bh;   // outer index of the key-side tensors
-    if constexpr (kScored) {
-        const int b = bh / p.score.H;
-        bh_kv = b * p.score.Hkv + (bh - b * p.score.H) / p.score.group;
-        const int2 seen = tile_key_range(p.score, b, q0, Lq_s, Lk_s,
-                                         reinterpret_cast<int *>(gbase + kBar + OFF_SCRATCH));
-        kend = seen.y;
-        kbase = seen.x / BC * BC;
-        yk0 = kbase;
-    }
-    const int nk = (kend - kbase + BC - 1) / BC;
+    int nk = (kend - kbase + BC - 1) / BC;
     // the t-th key tile that the CTA visits.  Biased scores: from the tile at the last row's
     // position down to the first, then the tiles behind it, so that the largest bias comes
     // first and the reference hardly ever rises (visited in order, steep slopes would
     // rescale the accumulators at every tile: 1051 instead of 921 us per call at 12 heads of
     // 8190 keys)
-    const int diag = min(max((q0 + BR - 1 + koff - kbase) / BC, 0), nk - 1);
+    int diag = 0;
     auto key_tile = [&](int t) -> int { return kBias && !kFixed && t <= diag ? diag - t : t; };
-    if (MASK != 0 && nk == 0) {
+    if (MASK != 0 && !kScored && nk == 0) {
         // no row of the tile sees a key: zeros and lse = -inf, no pipeline at all
         for (int r = threadIdx.x; r < BR && q0 + r < Lq_s; r += blockDim.x) {
             const size_t row = (size_t)bh * (size_t)p.Lq + (size_t)(yq + r);
@@ -331,6 +366,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         }
         return;
     }
+    // scored: this role's copy of the descriptor in slot i % 2 (after its barrier)
+    const uint32_t dyn = base + SM_STG;
+    auto take = [&](int i, int &qt_n, int &bh_n) {
+        if constexpr (kScored) {
+            const uint4 d = ld_shared_u4(dyn + OFF_UNIT + 16u * (uint32_t)(i & 1));
+            qt_n = (int)d.x;
+            bh_n = (int)d.y;
+            kbase = yk0 = (int)d.z;
+            nk = (int)d.w;
+            q0 = yq = qt_n * BR;
+            const int b = bh_n / p.score.H;
+            bh_kv = b * p.score.Hkv + (bh_n - b * p.score.H) / p.score.group;
+            diag = min(max((q0 + BR - 1 + koff - kbase) / BC, 0), nk - 1);
+        }
+    };
+    auto unit_full = [&](int i) -> uint32_t { return dyn + OFF_UNIT_FULL + 8u * (uint32_t)(i & 1); };
+    auto unit_free = [&](int i) -> uint32_t { return dyn + OFF_UNIT_FREE + 8u * (uint32_t)(i & 1); };
     const uint64_t bound = p.bound_ns;
     // persistent (nk >= 3): unit n's staged O goes to the V-side stage of unit n + 1's
     // second key tile (G = (n + 1) * nk + 1), tO to that of its third; unit n's last
@@ -369,6 +421,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         mbar_init(BAR(B_STG_FULL), SOFTMAX_THREADS / 32);
         mbar_init(BAR(B_STG_FREE), 1);
         mbar_init(BAR(B_STG_FREE + 1), 1);
+        if (kScored) {
+            mbar_init(dyn + OFF_CLC, 1);
+            mbar_init(dyn + OFF_ASK, 1);
+            mbar_init(dyn + OFF_STG_TO, SOFTMAX_THREADS / 32);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(unit_full(i), 1);
+                mbar_init(unit_free(i), UNIT_READERS);
+            }
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -396,21 +457,34 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             int kt_last[STAGES], vt_last[VST], q_last = -1;
             for (int s = 0; s < STAGES; ++s) kt_last[s] = -1;
             for (int s = 0; s < VST; ++s) vt_last[s] = -1;
-            int n = 0, qt_n = qt, bh_n = bh;
-            do {
-                const int G0 = n * nk;  // CTA-wide index of this unit's first key tile
+            int n = 0, qt_n = qt, bh_n = bh, tiles = 0;
+            for (int i = 0;; ++i) {
+                if constexpr (kScored) {
+                    ok = mbar_wait(unit_full(i), (i >> 1) & 1, abort_flag, bound);
+                    if (!ok) break;
+                    take(i, qt_n, bh_n);
+                    mbar_arrive(unit_free(i));
+                    if (nk < 0) break;
+                    if (nk <= 2) mbar_arrive(dyn + OFF_ASK);
+                    if (nk == 0) continue;
+                }
+                const int G0 = kScored ? tiles : n * nk;  // CTA-wide index of this unit's first key tile
                 const int yq_n = yq0 + qt_n * BR;
+                auto load_q = [&]() {
+                    mbar_arrive_expect_tx(BAR(B_Q_FULL), 4 * CHUNK_Q);
+                    tma_load_3d(base + SM_Q, &p.tm_q, BAR(B_Q_FULL), 0, yq_n, bh_n);
+                    tma_load_3d(base + SM_Q + CHUNK_Q, &p.tm_q, BAR(B_Q_FULL), 64, yq_n, bh_n);
+                    tma_load_3d(base + SM_TQ, &p.tm_tq, BAR(B_Q_FULL), 0, yq_n, bh_n);
+                    tma_load_3d(base + SM_TQ + CHUNK_Q, &p.tm_tq, BAR(B_Q_FULL), 64, yq_n, bh_n);
+                    q_last = n;
+                };
                 // Q / tQ are free once every S / dS' product of the previous unit is complete
-                if (n > 0 && !mbar_wait(BAR(B_SD_FULL + ((G0 - 1) & 1)), ((G0 - 1) >> 1) & 1, abort_flag, bound)) {
+                // (scored: the unit's first key tile goes ahead of them)
+                if (!kScored && n > 0 && !mbar_wait(BAR(B_SD_FULL + ((G0 - 1) & 1)), ((G0 - 1) >> 1) & 1, abort_flag, bound)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(BAR(B_Q_FULL), 4 * CHUNK_Q);
-                tma_load_3d(base + SM_Q, &p.tm_q, BAR(B_Q_FULL), 0, yq_n, bh_n);
-                tma_load_3d(base + SM_Q + CHUNK_Q, &p.tm_q, BAR(B_Q_FULL), 64, yq_n, bh_n);
-                tma_load_3d(base + SM_TQ, &p.tm_tq, BAR(B_Q_FULL), 0, yq_n, bh_n);
-                tma_load_3d(base + SM_TQ + CHUNK_Q, &p.tm_tq, BAR(B_Q_FULL), 64, yq_n, bh_n);
-                q_last = n;
+                if (!kScored) load_q();
                 // order of use by the MMA warp: KT_0, KT_1, VT_0, KT_2, VT_1, ...
                 for (int t = 0; t <= nk && ok; ++t) {
                     if (t < nk) {
@@ -431,6 +505,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         tma_load_3d(st + 2 * CHUNK_K, &p.tm_k, fb, 64, y, kScored ? bh_kv : bh_n);
                         tma_load_3d(st + 3 * CHUNK_K, &p.tm_tk, fb, 64, y, kScored ? bh_kv : bh_n);
                         kt_last[s] = G;
+                        if (kScored && t == 0) {
+                            if (n > 0 && !mbar_wait(BAR(B_SD_FULL + ((G0 - 1) & 1)), ((G0 - 1) >> 1) & 1, abort_flag, bound)) {
+                                ok = false;
+                                break;
+                            }
+                            load_q();
+                        }
+                        if (kScored && nk > 2 && t == nk - 2) mbar_arrive(dyn + OFF_ASK);
                     }
                     if (t >= 1) {
                         const int i = G0 + t - 1;
@@ -443,7 +525,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         // unit's second V tile (stored first), tO in that of its third; the
                         // first V tile has a stage of its own and loads as soon as the ring
                         // frees it, ahead of the previous unit's epilogue
-                        if (kPersist && n > 0 && (t == 2 || t == 3) &&
+                        // (scored: O in the stage of this unit's first V tile, tO in the other,
+                        // which a unit of one tile stages its own O in)
+                        if (kScored && n > 0 && (t == 1 || t == 2)) {
+                            ok = mbar_wait(BAR(B_STG_FREE + (t - 1)), (n - 1) & 1, abort_flag, bound);
+                            if (ok && nk == 1) ok = mbar_wait(BAR(B_STG_FREE + 1), (n - 1) & 1, abort_flag, bound);
+                            if (!ok) break;
+                        }
+                        if (kEven && n > 0 && (t == 2 || t == 3) &&
                             !mbar_wait(BAR(B_STG_FREE + (t - 2)), (n - 1) & 1, abort_flag, bound)) {
                             ok = false;
                             break;
@@ -460,7 +549,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         vt_last[s] = i;
                     }
                 }
-            } while (kPersist && ok && next_unit(++n, qt_n, bh_n));
+                tiles += nk;
+                if (!ok || !kPersist) break;
+                ++n;
+                if (kEven && !next_unit(n, qt_n, bh_n)) break;
+            }
             // let every copy already issued land before shared memory is released
             if (q_last >= 0) mbar_wait_drain(BAR(B_Q_FULL), q_last & 1, bound);
             for (int s = 0; s < STAGES; ++s)
@@ -483,10 +576,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             const uint64_t dk0 = smem_desc_sw128(base + SM_KT, 16, 1024);
             const uint64_t dv0 = smem_desc_sw128(base + SM_VT, CHUNK_K, 1024);
             bool ok = true;
-            // G: CTA-wide key-tile index (ring stage, buffer and phase)
-            auto issue_sd = [&](int G) -> bool {
-                const int s = G % STAGES;
-                const int b = G & 1;
+            // G: CTA-wide key-tile index (ring stage, buffer b = G % 2 and phase)
+            auto issue_sd = [&](int G, int b) -> bool {
+                const int s = b;
                 if (!mbar_wait(BAR(B_KT_FULL + s), (G / STAGES) & 1, abort_flag, bound)) return false;
                 tc_fence_after();
                 const uint64_t dk = desc_add(dk0, s * KT_STAGE);
@@ -507,9 +599,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 return true;
             };
             // first: the unit's first tile (overwrites O / T); n: the unit
-            auto issue_pv = [&](int G, bool first, int n) -> bool {
-                const int s = G % VST;  // V-side stage
-                const int b = G & 1;
+            auto issue_pv = [&](int G, int b, bool first, int n) -> bool {
+                const int s = kEven ? G % VST : b;  // V-side stage
                 if (!mbar_wait(BAR(B_P_FULL + b), (G >> 1) & 1, abort_flag, bound)) return false;
                 if (!mbar_wait(BAR(B_VT_FULL + s), (G / VST) & 1, abort_flag, bound)) return false;
                 // the previous unit's epilogue must have read O / T before they are overwritten
@@ -547,26 +638,146 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             // key tile t of a unit starts O / T afresh: the unit's first tile and,
             // with kSplit, each tile whose accumulators were just folded out
             auto restarts = [](int t) { return t == 0 || (kSplit && t % SPLIT_FOLD_TILES == 0); };
-            int n = 0, qt_n = qt, bh_n = bh;
-            do {
-                const int G0 = n * nk;
-                ok = mbar_wait(BAR(B_Q_FULL), n & 1, abort_flag, bound);
-                if (ok) ok = issue_sd(G0);
-                for (int j = 1; j < nk && ok; ++j) {
-                    ok = issue_sd(G0 + j);
-                    if (ok) ok = issue_pv(G0 + j - 1, restarts(j - 1), n);
+            int n = 0, qt_n = qt, bh_n = bh, tiles = 0;
+            for (int i = 0;; ++i) {
+                if constexpr (kScored) {
+                    ok = mbar_wait(unit_full(i), (i >> 1) & 1, abort_flag, bound);
+                    if (!ok) break;
+                    take(i, qt_n, bh_n);
+                    mbar_arrive(unit_free(i));
+                    if (nk < 0) break;
+                    if (nk == 0) continue;
                 }
-                if (ok) ok = issue_pv(G0 + nk - 1, restarts(nk - 1), n);
+                const int G0 = kScored ? tiles : n * nk;
+                ok = mbar_wait(BAR(B_Q_FULL), n & 1, abort_flag, bound);
+                if constexpr (kScored) {
+                    // units start at any G; stages and buffers are compile-time constants all
+                    // the same, so that the products' descriptors need no arithmetic
+                    auto unit = [&](auto parity) {
+                        constexpr int P = decltype(parity)::value;
+                        if (ok) ok = issue_sd(G0, P);
+                        for (int j = 1; j < nk && ok; j += 2) {
+                            ok = issue_sd(G0 + j, P ^ 1) && issue_pv(G0 + j - 1, P, j == 1, n);
+                            if (ok && j + 1 < nk) ok = issue_sd(G0 + j + 1, P) && issue_pv(G0 + j, P ^ 1, false, n);
+                        }
+                        if (ok) ok = (nk & 1) ? issue_pv(G0 + nk - 1, P, nk == 1, n) : issue_pv(G0 + nk - 1, P ^ 1, false, n);
+                    };
+                    if (G0 & 1)
+                        unit(std::integral_constant<int, 1>());
+                    else
+                        unit(std::integral_constant<int, 0>());
+                } else {
+                    if (ok) ok = issue_sd(G0, G0 & 1);
+                    for (int j = 1; j < nk && ok; ++j) {
+                        ok = issue_sd(G0 + j, (G0 + j) & 1);
+                        if (ok) ok = issue_pv(G0 + j - 1, (G0 + j - 1) & 1, restarts(j - 1), n);
+                    }
+                    if (ok) ok = issue_pv(G0 + nk - 1, (G0 + nk - 1) & 1, restarts(nk - 1), n);
+                }
                 // O and T are final once everything issued so far completes (a barrier
                 // of its own: a parity wait on a per-tile barrier could be ambiguous here)
                 if (ok) mma_commit(BAR(B_O_FULL));
-            } while (kPersist && ok && next_unit(++n, qt_n, bh_n));
+                tiles += nk;
+                if (!ok || !kPersist) break;
+                ++n;
+                if (kEven && !next_unit(n, qt_n, bh_n)) break;
+            }
             // every MMA issued must finish before tensor memory is released
             mma_commit(BAR(B_MMA_DRAIN));
             mbar_wait_drain(BAR(B_MMA_DRAIN), 0, bound);
         }
         __syncwarp();
-    } else if (kPersist && warp == 3) {
+    } else if (kScored && warp == 2) {
+        // ------------------------------------------ scored: output tensor stores
+        // each unit's O and tO, staged by the softmax warps in the V-side stages, go out
+        // through the tensor-store unit; O takes the stage of the next unit's first V
+        // tile, which may land as soon as the store has read it
+        if (lane == 0) {
+            int n = 0, qt_n = 0, bh_n = 0, tiles = 0;
+            for (int i = 0;; ++i) {
+                if (!mbar_wait(unit_full(i), (i >> 1) & 1, abort_flag, bound)) break;
+                take(i, qt_n, bh_n);
+                mbar_arrive(unit_free(i));
+                if (nk < 0) break;
+                if (nk == 0) continue;
+                tiles += nk;
+                const uint32_t so = base + SM_VT + (uint32_t)(tiles & 1) * VT_STAGE;
+                const uint32_t st = base + SM_VT + (uint32_t)((tiles & 1) ^ 1) * VT_STAGE;
+                if (!mbar_wait(BAR(B_STG_FULL), n & 1, abort_flag, bound) || *abort_flag != 0) break;
+                tma_store_3d(&p.tm_o, so, 0, yq, bh_n);
+                tma_store_3d(&p.tm_o, so + CHUNK_Q, 64, yq, bh_n);
+                tma_store_commit();
+                if (!mbar_wait(dyn + OFF_STG_TO, n & 1, abort_flag, bound) || *abort_flag != 0) break;
+                tma_store_3d(&p.tm_to, st, 0, yq, bh_n);
+                tma_store_3d(&p.tm_to, st + CHUNK_Q, 64, yq, bh_n);
+                tma_store_commit();
+                tma_store_wait_read_1();
+                mbar_arrive(BAR(B_STG_FREE));
+                tma_store_wait_read_all();
+                mbar_arrive(BAR(B_STG_FREE + 1));
+                ++n;
+            }
+            tma_store_wait_all();  // the last stores complete before the CTA exits
+        }
+        __syncwarp();
+    } else if (kScored && warp == 3) {
+        // --------------------------------------------- scored: the units to come
+        // Unit 0 is this CTA's own; near the end of each the hardware is asked for a CTA
+        // that has not started, whose unit comes next (units differ several times
+        // in length, and asking late leaves the last ones to whichever CTA is free first).
+        // Grid order: groups of heads whose keys fit the L2 together; in a group the
+        // late query tiles of all heads first, the heavy ones under prefix and frame-causal masks
+        int u = (int)blockIdx.x;
+        for (int i = 0;; ++i) {
+            const uint32_t slot = (uint32_t)(i & 1);
+            if (i >= 2 && !mbar_wait_warp(unit_free(i), ((i >> 1) & 1) ^ 1, abort_flag, bound)) break;
+            int t = 0, h = 0, first = 0, tiles = -1;
+            if (u >= 0) {
+                const int g = u / (p.n_qtiles * p.score.slabs), in = u - g * p.n_qtiles * p.score.slabs;
+                const int n = min(p.score.slabs, p.BH - g * p.score.slabs);
+                h = g * p.score.slabs + in % n;
+                t = p.n_qtiles - 1 - in / n;
+                // the rows' bounds, and the smallest interval of key tiles that holds them
+                int2 r[BR / 32];
+#pragma unroll
+                for (int k = 0; k < BR / 32; ++k)
+                    r[k] = row_bounds(p.score, h / p.score.H, t * BR + 32 * k + lane, Lq_s, Lk_s);
+                int lo = INT_MAX, hi = 0;
+#pragma unroll
+                for (int k = 0; k < BR / 32; ++k) {
+                    if (r[k].x < r[k].y) {
+                        lo = min(lo, r[k].x);
+                        hi = max(hi, r[k].y);
+                    }
+                    *reinterpret_cast<int2 *>(gbase + SM_STG + OFF_BOUNDS + slot * 1024u + 8u * (uint32_t)(32 * k + lane)) = r[k];
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                first = hi > 0 ? lo / BC * BC : 0;
+                tiles = hi > 0 ? (hi - first + BC - 1) / BC : 0;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                st_shared_v4(dyn + OFF_UNIT + 16u * slot, (uint32_t)t, (uint32_t)h, (uint32_t)first, (uint32_t)tiles);
+                mbar_arrive(unit_full(i));
+            }
+            if (u < 0) break;
+            bool ok = lane != 0 || mbar_wait_idle(dyn + OFF_ASK, i & 1, abort_flag, bound);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            if (lane == 0) {
+                fence_proxy_async_smem();  // the last answer has been read
+                mbar_arrive_expect_tx(dyn + OFF_CLC, 16);
+                clc_try_cancel(dyn + OFF_ANSWER, dyn + OFF_CLC);
+            }
+            if (!mbar_wait_warp(dyn + OFF_CLC, i & 1, abort_flag, bound)) {
+                if (lane == 0) mbar_wait_drain(dyn + OFF_CLC, i & 1, bound);
+                break;
+            }
+            u = clc_answer(dyn + OFF_ANSWER);
+            __syncwarp();
+        }
+        __syncwarp();
+    } else if (kEven && warp == 3) {
         // ------------------------------------- persistent: output tensor stores
         // each unit's O and tO, staged by the softmax warps in the V-side ring, go out
         // through the tensor-store unit; once the stores have read the staging the
@@ -604,17 +815,43 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
         const float2 s2 = make_float2(p.scale, p.scale);
         // bias: does the maximum take raw scores and biases separately (else the values
         // become the log2-unit scores before it)
-        float slope2 = 0.f;  // slope in log2 units
-        if constexpr (kBias) slope2 = p.score.slopes[bh % p.score.H] * 1.4426950408889634f;
-        const bool raw_max = kBias && !kCap && fabsf(slope2) * (float)(BC - 1) <= STEEP_LOG2;
+        float slope2 = 0.f;  // the unit's slope in log2 units
+        bool raw_max = false;
         // row max of c*S is c * max(S) (min(S) for c < 0)
-        const bool up = (kBias && !raw_max) || c >= 0.f;
-        const float sentinel = up ? -INFINITY : INFINITY;
+        bool up = c >= 0.f;
+        float sentinel = up ? -INFINITY : INFINITY;
         float *xch = reinterpret_cast<float *>(gbase + kXch);
         bool failed = false;
-        int n = 0, qt_n = qt, bh_n = bh;
-        do {
-            const int G0 = n * nk;  // CTA-wide index of this unit's first key tile
+        int n = 0, qt_n = qt, bh_n = bh, tiles = 0;
+        for (int i = 0;; ++i) {
+            int2 seen = make_int2(0, 0);  // scored: this row's keys, relative to kbase
+            if constexpr (kScored) {
+                // (every softmax thread goes on or leaves together)
+                if (named_bar_or(NB_EPI, SOFTMAX_THREADS, !mbar_wait_warp(unit_full(i), (i >> 1) & 1, abort_flag, bound)))
+                    break;
+                take(i, qt_n, bh_n);
+                seen = *reinterpret_cast<const int2 *>(gbase + SM_STG + OFF_BOUNDS + 1024u * (uint32_t)(i & 1) + 8u * (uint32_t)row);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(unit_free(i));
+                if (nk < 0) break;
+                if (nk == 0) {  // no row sees a key: zeros and lse = -inf
+                    if (q0 + row < Lq_s) {
+                        const size_t at = (size_t)bh_n * (size_t)p.Lq + (size_t)(q0 + row);
+                        uint4 *const out = reinterpret_cast<uint4 *>((grp == 0 ? p.o_bf : p.to_bf) + at * HD);
+                        for (int k = 0; k < HD / 8; ++k) out[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (grp == 0 && p.lse) p.lse[at] = -INFINITY;
+                        if (grp == 1 && p.mu) p.mu[at] = 0.f;
+                    }
+                    continue;
+                }
+                if constexpr (kBias) {
+                    slope2 = __ldg(p.score.slopes + bh_n % p.score.H) * 1.4426950408889634f;
+                    raw_max = !kCap && fabsf(slope2) * (float)(BC - 1) <= STEEP_LOG2;
+                    up = !raw_max || c >= 0.f;
+                    sentinel = up ? -INFINITY : INFINITY;
+                }
+            }
+            const int G0 = kScored ? tiles : n * nk;  // CTA-wide index of this unit's first key tile
             const int q0_n = qt_n * BR, yq_n = yq0 + q0_n;
             float m_ref = -INFINITY, l = 0.f, g = 0.f;
             // kSplit: the folded sums in this row's fp32 output columns 64*grp.. of O and
@@ -627,11 +864,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             };
             // keys this row sees (a prefix of the sequence's keys; may be <= 0 when causal)
             const int kcount = kCausal ? min(Lk_s, q0_n + row + koff + 1) : Lk_s;
-            int2 seen = make_int2(0, 0);  // scored: this row's keys, relative to kbase
-            float dist0 = 0.f;            // bias: distance to this group's first streamed key
+            float dist0 = 0.f;  // bias: distance to this group's first streamed key
             if constexpr (kScored) {
-                const int sb = bh / p.score.H;
-                seen = row_bounds(p.score, sb, q0 + row, Lq_s, Lk_s);
                 seen.x -= kbase;
                 seen.y -= kbase;
                 if (kBias) dist0 = (float)(q0 + row + koff - kbase - (int)col0);
@@ -909,7 +1143,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
             if (!failed) failed = !mbar_wait_warp(BAR(B_O_FULL), n & 1, abort_flag, bound);
             // [l, g][group][row]; the persistent form reuses the per-tile maxima area, whose
             // last reads (the unit's last tile) precede every P arrival and so O_FULL
-            float *lg = kPersist ? xch : xch + 2 * 2 * 128;
+            float *lg = kEven ? xch : xch + 2 * 2 * 128;
             if (!failed) {
                 lg[(0 * 2 + grp) * 128 + row] = l;
                 lg[(1 * 2 + grp) * 128 + row] = g;
@@ -921,7 +1155,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 const float gt = g + lg[(1 * 2 + (grp ^ 1)) * 128 + row];
                 // persistent: every thread has read the other group's l, g before the next
                 // unit's first tile writes its maxima over them
-                if (kPersist) named_bar_sync(NB_EPI, SOFTMAX_THREADS);
+                if (kEven) named_bar_sync(NB_EPI, SOFTMAX_THREADS);
                 // a row that saw no key (masks only) has lt = 0: zeros, lse = -inf
                 const float inv_l = (MASK != 0 && !(lt > 0.f)) ? 0.f : 1.f / lt;
                 const float mu = gt * inv_l;
@@ -979,8 +1213,49 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 // bf16 outputs: O into the Q tile's shared memory, tO into tQ's, in
                 // the 128-byte-swizzled layout of the store tensor maps (packed rows and
                 // the persistent form: plain stores from registers)
+                if constexpr (kScored) {  // O, then tO (which takes O again)
+                    const uint32_t first = (uint32_t)((tiles + nk) & 1);
+                    const uint32_t row_off = base + SM_VT + (uint32_t)grp * CHUNK_Q + (uint32_t)row * 128u;
+                    auto stage = [&](uint32_t slot, int h, const uint32_t (&w)[16]) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            st_shared_v4(row_off + slot * VT_STAGE + ((4u * (uint32_t)h + (uint32_t)u) ^ (uint32_t)(row & 7)) * 16u,
+                                         w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                    };
 #pragma unroll 1
-                for (int h = 0; h < (kSplit ? 0 : 2); ++h) {
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t ro[32], w[16];
+                        tmem_ld32(tbase + lane_off + TM_O + 32u * (2 * grp + h), ro);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_bf16x2(__uint_as_float(ro[2 * i]) * inv_l, __uint_as_float(ro[2 * i + 1]) * inv_l);
+                        stage(first, h, w);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(B_STG_FULL));
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t ro[32], rt[32], w[16];
+                        tmem_ld32(tbase + lane_off + TM_O + 32u * (2 * grp + h), ro);
+                        tmem_ld32(tbase + lane_off + TM_T + 32u * (2 * grp + h), rt);
+                        tmem_wait_ld();
+                        if (h == 1)  // O / T read: the next unit may overwrite them
+                            warp_arrive_after_tc(BAR(B_OT_FREE));
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_bf16x2(
+                                fmaf(-mu, __uint_as_float(ro[2 * i]) * inv_l, __uint_as_float(rt[2 * i]) * inv_l),
+                                fmaf(-mu, __uint_as_float(ro[2 * i + 1]) * inv_l, __uint_as_float(rt[2 * i + 1]) * inv_l));
+                        stage(first ^ 1u, h, w);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dyn + OFF_STG_TO);
+                }
+#pragma unroll 1
+                for (int h = 0; h < (kSplit || kScored ? 0 : 2); ++h) {
                     const int pc = 2 * grp + h;
                     uint32_t ro[32], rt[32];
                     tmem_ld32(tbase + lane_off + TM_O + 32u * pc, ro);
@@ -1031,7 +1306,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 if (grp == 1 && p.mu != nullptr && q0_n + row < Lq_s)
                     p.mu[(size_t)bh_n * (size_t)p.Lq + (size_t)(yq_n + row)] = mu;
             }
-            if (kPersist) {
+            if (kScored) {
+            } else if (kPersist) {
                 // staging complete: one arrival per warp for the storing warp
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1048,8 +1324,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                     tma_store_wait_all();
                 }
             }
-            if (any_failed) break;  // uniform: an OR over every softmax thread
-        } while (kPersist && next_unit(++n, qt_n, bh_n));
+            if (any_failed || !kPersist) break;  // uniform: an OR over every softmax thread
+            tiles += nk;
+            ++n;
+            if (kEven && !next_unit(n, qt_n, bh_n)) break;
+        }
         __syncwarp();
     }
 

@@ -78,6 +78,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The same for a wait that is long and not urgent: sleeps between polls, which
+// would take issue slots from the warps that work meanwhile.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                               uint64_t bound_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        __nanosleep(200);
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > bound_ns) {
+            *abort_flag = 1;
+            atomicOr(&g_status_word, 1);
+            return false;
+        }
+    }
+}
+
 // Warp-wide bounded wait: lane 0 polls, the outcome is broadcast.  Must be
 // called by all 32 lanes.  After it returns true the caller's tcgen05 loads
 // are ordered by tcgen05.fence::after_thread_sync as usual.

@@ -33,7 +33,7 @@ Setup g_setup[host::kMaxDevices];
 
 template <int MASK>
 cudaError_t set_fwd() {
-    return cudaFuncSetAttribute(sm100::attn_jvp_fwd_kernel<false, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(sm100::attn_jvp_fwd_kernel<false, MASK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sm100::SMEM_BYTES);
 }
 template <int MASK, bool kSplitK>
@@ -174,10 +174,10 @@ int fwd_scored(const void *q, const void *k, const void *v, const void *tq, cons
         constexpr int M = decltype(mask)::value;
         const dim3 grid((unsigned)(p.n_qtiles * BH));
         if ((M & MASK_CAP) != 0 && p.score.cap_out <= FIXED_CAP)
-            sm100::attn_jvp_fwd_kernel<false, (M & MASK_CAP) != 0 ? M | MASK_FIXED : M>
+            sm100::attn_jvp_fwd_kernel<false, (M & MASK_CAP) != 0 ? M | MASK_FIXED : M, true>
                 <<<grid, sm100::NTHREADS, sm100::SMEM_BYTES, (cudaStream_t)stream>>>(p);
         else
-            sm100::attn_jvp_fwd_kernel<false, M>
+            sm100::attn_jvp_fwd_kernel<false, M, true>
                 <<<grid, sm100::NTHREADS, sm100::SMEM_BYTES, (cudaStream_t)stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? AJVP_OK : host::fail(e);
