@@ -319,3 +319,30 @@ def test_second_derivatives_are_refused():
     (dq,) = torch.autograd.grad((o.float().square() + to.float()).sum(), x[:1], create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         dq.float().sum().backward()
+
+
+@pytest.mark.parametrize("opt", [{}, dict(softcap=30.0), dict(bias=True), dict(softcap=30.0, bias=True),
+                                 dict(softcap=200.0, bias=True)], ids=lambda o: "-".join(o) + str(o.get("softcap", "")))
+def test_many_units_of_different_lengths(opt):
+    """40 sequences of 4 row tiles and 4 heads, every tile with an interval of its own of 0 to 9 key tiles (some
+    without any): bit for bit as each sequence alone, whose few tiles are a CTA each."""
+    B, H, Lq, Lk = 40, 4, 500, 555
+    inp, _ = make(B, H, 2, Lq, Lk, seed=26)
+    g = torch.Generator().manual_seed(27)
+    begin = torch.randint(0, Lk, (B, 4), generator=g)
+    length = torch.randint(0, 4, (B, 4), generator=g) * torch.randint(0, 190, (B, 4), generator=g)
+    rows = lambda x: x.repeat_interleave(128, 1)[:, :Lq].int().contiguous().cuda()  # noqa: E731
+    kw = dict(key_begin=rows(begin), key_end=rows(begin + length))
+    if "softcap" in opt:
+        kw["softcap"] = opt["softcap"]
+    if "bias" in opt:
+        kw["slopes"] = slopes_of(H)
+    x = [inp[n] for n in NAMES]
+    for _ in range(3):
+        out = ajvp.attn_jvp_fwd_scored_stats(*x, **kw)
+        for b in range(B):
+            s = slice(b, b + 1)
+            alone = ajvp.attn_jvp_fwd_scored_stats(*(t[s] for t in x), **{n: v[s] if n.startswith("key") else v
+                                                                          for n, v in kw.items()})
+            assert all(torch.equal(y[s], z) for y, z in zip(out, alone))
+    assert ajvp.check_device_status() == ajvp.AJVP_OK
