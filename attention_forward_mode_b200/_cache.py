@@ -16,7 +16,7 @@ import functools
 import torch
 
 from ._binding import _check, _ptr, load_library
-from ._scored import _BF16, _F32, _I32, _launch_scope, _tensor, _tensors
+from ._scored import _BF16, _F32, _I32, _empty, _launch_scope, _tensor, _tensors
 
 __all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache", "fwd_cache_workspace_bytes"]
 
@@ -81,8 +81,8 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
         raise ValueError("tq goes with q, and an output with its input")
     scope, handle = _launch_scope(stream, dev)
     with scope:
-        q_out = torch.empty_like(q) if q is not None and q_out is None else q_out
-        tq_out = torch.empty_like(tq) if tq is not None and tq_out is None else tq_out
+        q_out = _empty((H, total, d), _BF16, dev) if q is not None and q_out is None else q_out
+        tq_out = _empty((H, total, d), _BF16, dev) if tq is not None and tq_out is None else tq_out
         rc = load_library().attn_jvp_cache_append(
             k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(tq), _ptr(q_out), _ptr(tq_out), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
@@ -164,11 +164,11 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
         if workspace is None:
             size = _workspace_bytes(n_seq, H, Hkv, n, page, width, tq is not None, dev.index)
             workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-        # (empty_like takes half as long as new_empty, but keeps the strides)
-        new = torch.empty_like if q.is_contiguous() else lambda x: x.new_empty(shape)
-        o = new(q) if o is None else o
-        to = new(q) if to is None and tq is not None else to
-        lse = q.new_empty(shape[:-1], dtype=_F32) if lse is None and want_lse else lse
+        shape = tuple(shape)
+        o = _empty(shape, _BF16, dev) if o is None else o
+        to = _empty(shape, _BF16, dev) if to is None and tq is not None else to
+        if lse is None and want_lse:  # (packed: [H, total])
+            lse = _empty(shape[:3], _F32, dev) if len(shape) == 4 else torch.empty(shape[:2], dtype=_F32, device=dev)
         rc = load_library().attn_jvp_fwd_cache(
             q.data_ptr(), _ptr(tq), o.data_ptr(), _ptr(to), _ptr(lse), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(), _ptr(cu_seqlens),

@@ -6,6 +6,7 @@ Argument marshalling only, as in ``_binding``."""
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -18,10 +19,33 @@ __all__ = ["attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_sco
 _HERE = contextlib.nullcontext()
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # (a tensor is on a GPU already)
+try:  # an allocation without its argument parsing: 0.8 instead of 1.8 us, of which a call makes three or more
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+
+
+def _empty(shape, dtype, device):
+    """A contiguous tensor of one, three or four dimensions on ``device``, which is current."""
+    if len(shape) == 1:
+        strides = (1,)
+    elif len(shape) == 4:
+        B, H, L, d = shape
+        strides = (H * L * d, L * d, d, 1)
+    else:
+        H, L, d = shape
+        strides = (L * d, d, 1)
+    if _empty_strided_cuda is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    return _empty_strided_cuda(shape, strides, dtype)
 
 
 def _tensor(name, x, shape, dtype, device=None):
     """x is a contiguous CUDA tensor of this shape and type (on this device)."""
+    if device is not None and type(x) is torch.Tensor and x.dtype is dtype and x.shape == shape \
+            and x.get_device() == device.index and x.is_contiguous():
+        return x
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype or x.shape != shape \
             or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
@@ -33,11 +57,9 @@ def _tensor(name, x, shape, dtype, device=None):
 def _tensors(names, xs, shape, dtype, device):
     """Every x is such a tensor of one shape and type.  (The calls are short: what
     a check costs counts, so the common case is one pass.)"""
-    for x in xs:
-        if type(x) is not torch.Tensor or x.dtype is not dtype or x.shape != shape or x.device != device \
-                or not x.is_contiguous():
-            for name, y in zip(names, xs):
-                _tensor(name, y, shape, dtype, device)
+    if not _all_right(xs, (shape,) * len(xs), dtype, device.index):
+        for name, y in zip(names, xs):
+            _tensor(name, y, shape, dtype, device)
 
 
 def _launch_scope(stream, device):
@@ -46,7 +68,7 @@ def _launch_scope(stream, device):
     current stream of the device, or ``stream``), so that nothing allocated
     for the call is handed out again, or was last used, on another one."""
     if stream is None:
-        here = torch.cuda.current_device() == device.index
+        here = _current_device() == device.index
         handle = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
         return _HERE if here else torch.cuda.device(device), handle
     if not isinstance(stream, torch.cuda.Stream):
@@ -56,7 +78,21 @@ def _launch_scope(stream, device):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
+def _all_right(xs, shapes, dtype, index):
+    for x, shape in zip(xs, shapes):
+        if type(x) is not torch.Tensor or x.dtype is not dtype or x.shape != shape or x.get_device() != index \
+                or not x.is_contiguous():
+            return False
+    return True
+
+
 def _sizes(q, k, v, tq, tk, tv):
+    if type(q) is torch.Tensor and type(k) is torch.Tensor:  # the common case in one pass
+        qs, ks = q.shape, k.shape
+        if len(qs) == len(ks) == 4 and ks[1] and not qs[1] % ks[1] and ks[0] == qs[0] and ks[3] == qs[3]:
+            index = q.get_device()
+            if index >= 0 and _all_right((q, tq, k, v, tk, tv), (qs, qs, ks, ks, ks, ks), _BF16, index):
+                return qs[0], qs[1], ks[1], qs[2], ks[2], qs[3]
     for name, x in (("q", q), ("k", k)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 4:
             raise ValueError(f"{name} must be a CUDA [B, H, L, d] tensor")
@@ -79,7 +115,7 @@ def _score_args(slopes, key_begin, key_end, softcap, scale, sizes, device):
 
 
 def _per_sequence(x, B):
-    return x.expand(B, x.shape[0]).contiguous() if x is not None and x.dim() == 1 else x
+    return x.expand(B, x.shape[0]).contiguous() if x.dim() == 1 else x
 
 
 def _fwd(entry, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end, o, to, lse, mu, stream, want_lse,
@@ -88,19 +124,24 @@ def _fwd(entry, q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end,
     B, H, _, Lq, _, _ = sizes
     dev = q.device
     softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
-    for name, x in (("o", o), ("to", to)):
-        if x is not None:
-            _tensor(name, x, q.shape, _BF16, dev)
-    for name, x in (("lse", lse), ("mu", mu)):
-        if x is not None:
-            _tensor(name, x, (B, H, Lq), _F32, dev)
+    if not (o is to is lse is mu is None):
+        for name, x in (("o", o), ("to", to)):
+            if x is not None:
+                _tensor(name, x, q.shape, _BF16, dev)
+        for name, x in (("lse", lse), ("mu", mu)):
+            if x is not None:
+                _tensor(name, x, (B, H, Lq), _F32, dev)
     scope, handle = _launch_scope(stream, dev)
     with scope:
-        o = torch.empty_like(q) if o is None else o
-        to = torch.empty_like(q) if to is None else to
-        lse = q.new_empty((B, H, Lq), dtype=_F32) if lse is None and want_lse else lse
-        mu = q.new_empty((B, H, Lq), dtype=_F32) if mu is None and want_mu else mu
-        key_begin, key_end = _per_sequence(key_begin, B), _per_sequence(key_end, B)
+        shape = (B, H, Lq, sizes[5])
+        o = _empty(shape, _BF16, dev) if o is None else o
+        to = _empty(shape, _BF16, dev) if to is None else to
+        lse = _empty(shape[:3], _F32, dev) if lse is None and want_lse else lse
+        mu = _empty(shape[:3], _F32, dev) if mu is None and want_mu else mu
+        if key_begin is not None:
+            key_begin = _per_sequence(key_begin, B)
+        if key_end is not None:
+            key_end = _per_sequence(key_end, B)
         rows = (o.data_ptr(), to.data_ptr(), _ptr(lse)) + ((mu.data_ptr(),) if want_mu else ())
         rc = getattr(load_library(), entry)(q.data_ptr(), k.data_ptr(), v.data_ptr(), tq.data_ptr(), tk.data_ptr(),
                                             tv.data_ptr(), *rows, _ptr(slopes), _ptr(key_begin), _ptr(key_end), *sizes,
@@ -138,6 +179,12 @@ def bwd_scored_workspace_bytes(B: int, H: int, Hkv: int, Lq: int, Lk: int) -> in
     return int(load_library().attn_jvp_bwd_scored_workspace_bytes(int(B), int(H), int(Hkv), int(Lq), int(Lk)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(B, H, Hkv, Lq, Lk, device):
+    """The same (at least 1), with ``device`` current (part of the key: the size depends on it)."""
+    return max(1, bwd_scored_workspace_bytes(B, H, Hkv, Lq, Lk))
+
+
 def attn_jvp_bwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout, scale=None, softcap=0.0, slopes=None,
                         key_begin=None, key_end=None, grads=None, workspace=None, stream=None):
     """Gradients of <dout, O> + <dtout, tO> of ``attn_jvp_fwd_scored`` with
@@ -147,26 +194,29 @@ def attn_jvp_bwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout, scale=
     of ``bwd_scored_workspace_bytes`` bytes (allocated per call when omitted).
     Returns a dict dq, dk, dv, dtq, dtk, dtv shaped like the inputs."""
     sizes = _sizes(q, k, v, tq, tk, tv)
-    B, H, _, Lq, _, _ = sizes
+    B, H, Hkv, Lq, Lk, d = sizes
     dev = q.device
     softcap, scale = _score_args(slopes, key_begin, key_end, softcap, scale, sizes, dev)
     _tensors(("o", "to", "dout", "dtout"), (o, to, dout, dtout), q.shape, _BF16, dev)
     _tensors(("lse", "mu"), (lse, mu), (B, H, Lq), _F32, dev)
+    shapes = dict.fromkeys(GRAD_NAMES, (B, Hkv, Lk, d)) | {"dq": (B, H, Lq, d), "dtq": (B, H, Lq, d)}
     grads = dict(grads or {})
-    like = {n: q if n in ("dq", "dtq") else k for n in GRAD_NAMES}
-    for n in GRAD_NAMES:
-        if grads.get(n) is not None:
-            _tensor(n, grads[n], like[n].shape, _BF16, dev)
+    for n, x in grads.items():
+        if n in shapes and x is not None:
+            _tensor(n, x, shapes[n], _BF16, dev)
     if workspace is not None:
         _tensor("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
     scope, handle = _launch_scope(stream, dev)
     with scope:
         for n in GRAD_NAMES:
             if grads.get(n) is None:
-                grads[n] = torch.empty_like(like[n])
+                grads[n] = _empty(shapes[n], _BF16, dev)
         if workspace is None:
-            workspace = torch.empty(max(1, bwd_scored_workspace_bytes(*sizes[:5])), dtype=torch.uint8, device=dev)
-        key_begin, key_end = _per_sequence(key_begin, B), _per_sequence(key_end, B)
+            workspace = _empty((_workspace_bytes(*sizes[:5], dev.index),), torch.uint8, dev)
+        if key_begin is not None:
+            key_begin = _per_sequence(key_begin, B)
+        if key_end is not None:
+            key_end = _per_sequence(key_end, B)
         rc = load_library().attn_jvp_bwd_scored(
             _ptr(q), _ptr(k), _ptr(v), _ptr(tq), _ptr(tk), _ptr(tv), _ptr(o), _ptr(to), _ptr(lse), _ptr(mu),
             _ptr(dout), _ptr(dtout), *(_ptr(grads[n]) for n in GRAD_NAMES), _ptr(slopes), _ptr(key_begin),

@@ -346,3 +346,15 @@ def test_many_units_of_different_lengths(opt):
                                                                           for n, v in kw.items()})
             assert all(torch.equal(y[s], z) for y, z in zip(out, alone))
     assert ajvp.check_device_status() == ajvp.AJVP_OK
+
+
+def test_outputs_allocated_either_way(monkeypatch):
+    """The allocation without argument parsing is torch's own business; without it the results are the same."""
+    from attention_forward_mode_b200 import _scored
+    inp, cot = make(2, 4, 2, 65, 90, seed=28)
+    kw = dict(softcap=20.0, key_end=torch.randint(0, 91, (2, 65), dtype=torch.int32, device="cuda"))
+    out, g = run(inp, cot, kw)
+    monkeypatch.setattr(_scored, "_empty_strided_cuda", None)
+    out2, g2 = run(inp, cot, kw)
+    for a, b in list(zip(out, out2)) + [(g[n], g2[n]) for n in g]:
+        assert a.stride() == b.stride() and a.dtype == b.dtype and torch.equal(a, b)
