@@ -16,12 +16,21 @@ import functools
 import torch
 
 from ._binding import _check, _ptr, load_library
-from ._scored import _BF16, _F32, _I32, _empty, _launch_scope, _tensor, _tensors
+from ._scored import _BF16, _F32, _I32, _all_right, _empty, _launch_scope, _tensor, _tensors
 
 __all__ = ["attn_jvp_cache_append", "attn_jvp_fwd_cache", "fwd_cache_workspace_bytes"]
 
 
 def _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens):
+    if type(k_cache) is torch.Tensor and type(block_table) is torch.Tensor:  # the common case in one pass
+        shape, table, index = k_cache.shape, block_table.shape, k_cache.get_device()
+        if len(shape) == 4 and len(table) == 2 and index >= 0:
+            pages, Hkv, page, d = shape
+            of_scale = (pages, Hkv)
+            if _all_right((k_cache, v_cache), (shape, shape), torch.float8_e4m3fn, index) \
+                    and _all_right((k_scale, v_scale), (of_scale, of_scale), _F32, index) \
+                    and _all_right((block_table, cache_lens), (table, table[:1]), _I32, index):
+                return table[0], Hkv, pages, page, table[1], d, k_cache.device
     if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda or k_cache.dim() != 4:
         raise ValueError("k_cache must be a CUDA [pages, Hkv, page, d] tensor")
     shape, dev = k_cache.shape, k_cache.device
@@ -73,10 +82,11 @@ def attn_jvp_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table,
         H = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
         if H < 1 or H % Hkv:
             raise ValueError(f"q must be [H, total, d] with H a multiple of the key heads ({Hkv})")
-        _tensor("q", q, (H, total, d), _BF16, dev)
-        for name, x in (("tq", tq), ("q_out", q_out), ("tq_out", tq_out)):
-            if x is not None:
-                _tensor(name, x, q.shape, _BF16, dev)
+        _tensors(("q", "tq"), (q,) if tq is None else (q, tq), (H, total, d), _BF16, dev)
+        if q_out is not None or tq_out is not None:
+            for name, x in (("q_out", q_out), ("tq_out", tq_out)):
+                if x is not None:
+                    _tensor(name, x, q.shape, _BF16, dev)
     if (q is None and (tq is not None or q_out is not None)) or (tq is None and tq_out is not None):
         raise ValueError("tq goes with q, and an output with its input")
     scope, handle = _launch_scope(stream, dev)
@@ -127,7 +137,7 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
     over the whole GPU (allocated per call when omitted; an empty one: do without).
     Returns (o, to, lse), contiguous, shaped like q."""
     n_seq, Hkv, pages, page, width, d, dev = _cache_sizes(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens)
-    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.device != dev \
+    if not isinstance(q, torch.Tensor) or q.dtype is not _BF16 or q.get_device() != dev.index \
             or q.dim() != (4 if cu_seqlens is None else 3) or q.shape[-1] != d or q.stride(-1) != 1:
         raise ValueError("q must be a bf16 [n_seq, H, n, d] tensor (packed: [H, total, d]) on the cache's device with "
                          "its channels together")
@@ -143,8 +153,8 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
         _tensor("cu_seqlens", cu_seqlens, (n_seq + 1,), _I32, dev)
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"query heads ({H}) must be a multiple of the key heads ({Hkv})")
-    if tq is not None and (not isinstance(tq, torch.Tensor) or tq.shape != q.shape or tq.dtype != q.dtype
-                           or tq.device != dev or tq.stride() != q.stride()
+    if tq is not None and (not isinstance(tq, torch.Tensor) or tq.shape != q.shape or tq.dtype is not _BF16
+                           or tq.get_device() != dev.index or tq.stride() != q.stride()
                            and any(m > 1 and s != t for m, s, t in zip(q.shape, q.stride(), tq.stride()))):
         raise ValueError("tq must have q's shape, strides, type and device")
     if slopes is not None:
@@ -152,9 +162,10 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
     shape = q.shape
     if tq is None and to is not None:
         raise ValueError("to goes with tq")
-    for name, x in (("o", o), ("to", to)):
-        if x is not None:
-            _tensor(name, x, shape, _BF16, dev)
+    if o is not None or to is not None:
+        for name, x in (("o", o), ("to", to)):
+            if x is not None:
+                _tensor(name, x, shape, _BF16, dev)
     if lse is not None:
         _tensor("lse", lse, shape[:-1], _F32, dev)
     if workspace is not None:
