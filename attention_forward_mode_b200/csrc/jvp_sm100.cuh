@@ -67,8 +67,9 @@
 // warp 2.  As one CTA per unit a unit of 15 tiles spent a third of its time on its
 // two ends (8 of 24 us); against that form (cold caches, 148 SMs): 2 x 12 heads of 4096
 // in documents 153 -> 140 us, 12 heads of 8190 under a frame mask with cap and bias
-// 574 -> 558, 12 heads of 2501 under a prefix mask 72.7 -> 70.7; a call of a few tiles
-// takes 0.8 us longer.
+// 574 -> 558, 12 heads of 2501 under a prefix mask 72.7 -> 70.7.  Where every SM has
+// one unit at most it is 1 to 3 % slower (144 units of 128 tiles 165 -> 168 us, capped
+// 174 -> 180; a few tiles 9.7 -> 10.5).
 #pragma once
 
 #include <type_traits>
