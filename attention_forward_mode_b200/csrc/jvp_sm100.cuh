@@ -128,6 +128,11 @@ constexpr uint32_t OFF_UNIT = 96;        // + 16 slot
 constexpr uint32_t OFF_BOUNDS = 1024;    // + 1024 slot: int2 per row
 constexpr uint32_t UNIT_READERS = 3 + SOFTMAX_THREADS / 32;  // producer, MMA issuer, storer, softmax warps
 
+// bound on a wait for a whole unit of `tiles` key tiles, each with waits of up to `bound`
+__device__ __forceinline__ uint64_t unit_bound(uint64_t bound, int tiles) {
+    return min(bound, uint64_t(1) << 40) * (uint64_t)(tiles + 8);
+}
+
 // Asks for a CTA that has not started, to run its unit in this one: the answer
 // (16 bytes) arrives at `addr`, counted on `bar`.
 __device__ __forceinline__ void clc_try_cancel(uint32_t addr, uint32_t bar) {
@@ -704,7 +709,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 tiles += nk;
                 const uint32_t so = base + SM_VT + (uint32_t)(tiles & 1) * VT_STAGE;
                 const uint32_t st = base + SM_VT + (uint32_t)((tiles & 1) ^ 1) * VT_STAGE;
-                if (!mbar_wait(BAR(B_STG_FULL), n & 1, abort_flag, bound) || *abort_flag != 0) break;
+                // (lasts as long as the unit, whose tiles' waits are bounded one by one)
+                if (!mbar_wait(BAR(B_STG_FULL), n & 1, abort_flag, unit_bound(bound, nk)) || *abort_flag != 0) break;
                 tma_store_3d(&p.tm_o, so, 0, yq, bh_n);
                 tma_store_3d(&p.tm_o, so + CHUNK_Q, 64, yq, bh_n);
                 tma_store_commit();
@@ -763,7 +769,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 mbar_arrive(unit_full(i));
             }
             if (u < 0) break;
-            bool ok = lane != 0 || mbar_wait_idle(dyn + OFF_ASK, i & 1, abort_flag, bound);
+            // (lasts as long as the unit, whose tiles' waits are bounded one by one)
+            bool ok = lane != 0 || mbar_wait_idle(dyn + OFF_ASK, i & 1, abort_flag, unit_bound(bound, tiles));
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             if (lane == 0) {
                 fence_proxy_async_smem();  // the last answer has been read

@@ -358,3 +358,19 @@ def test_outputs_allocated_either_way(monkeypatch):
     out2, g2 = run(inp, cot, kw)
     for a, b in list(zip(out, out2)) + [(g[n], g2[n]) for n in g]:
         assert a.stride() == b.stride() and a.dtype == b.dtype and torch.equal(a, b)
+
+
+def test_a_wait_bound_shorter_than_a_unit():
+    """The bound is on single waits: a row tile of 1094 key tiles takes some 1.4 ms in all."""
+    inp, _ = make(1, 2, 1, 100, 70000, seed=29)
+    x = [inp[n] for n in NAMES]
+    want = ajvp.attn_jvp_fwd_scored(*x, softcap=30.0)
+    torch.cuda.synchronize()
+    ajvp.set_wait_bound_ns(300_000)
+    try:
+        got = ajvp.attn_jvp_fwd_scored(*x, softcap=30.0)
+        torch.cuda.synchronize()
+    finally:
+        ajvp.set_wait_bound_ns(0)
+    assert ajvp.check_device_status() == ajvp.AJVP_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
