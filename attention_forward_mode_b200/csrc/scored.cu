@@ -169,7 +169,8 @@ int fwd_scored(const void *q, const void *k, const void *v, const void *tq, cons
     p.scale_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;
     p.bound_ns = host::wait_bound_ns();
     p.score = make_score(z, scale, softcap, slopes, key_begin, key_end);
-    p.score.slabs = (int)(z.H / z.Hkv * slabs_together(z.Lk, BHk));  // heads of a group share their keys
+    // heads of a group share their keys (and never more slabs than there are: the kernel multiplies them by its row tiles)
+    p.score.slabs = (int)std::min<int64_t>(BH, z.H / z.Hkv * slabs_together(z.Lk, BHk));
     return with_mask(mask_bits(softcap, slopes), [&](auto mask) {
         constexpr int M = decltype(mask)::value;
         const dim3 grid((unsigned)(p.n_qtiles * BH));
