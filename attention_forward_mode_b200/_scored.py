@@ -159,7 +159,8 @@ def attn_jvp_fwd_scored(q, k, v, tq, tk, tv, scale=None, softcap=0.0, slopes=Non
     ``key_end[b, i]`` of query row i (int32 [B, Lq], or [Lq] for every sequence;
     ``key_bounds`` makes them).  q, tq bf16 [B, H, Lq, 128]; k, v, tk, tv
     [B, Hkv, Lk, 128] with H a multiple of Hkv.  Rows that see nothing give
-    zeros and lse = -inf.  Asynchronous on ``stream`` (default: the current
+    zeros and lse = -inf, whatever their q and tq hold; k, v, tk and tv must be
+    finite also where they are hidden.  Asynchronous on ``stream`` (default: the current
     stream of the tensors' device)."""
     return _fwd("attn_jvp_fwd_scored", q, k, v, tq, tk, tv, scale, softcap, slopes, key_begin, key_end, o, to, lse,
                 None, stream, want_lse, False)[:3]
@@ -189,7 +190,8 @@ def attn_jvp_bwd_scored(q, k, v, tq, tk, tv, o, to, lse, mu, dout, dtout, scale=
                         key_begin=None, key_end=None, grads=None, workspace=None, stream=None):
     """Gradients of <dout, O> + <dtout, tO> of ``attn_jvp_fwd_scored`` with
     respect to q, k, v, tq, tk, tv (slopes and cap are constants); o, to, lse,
-    mu from ``attn_jvp_fwd_scored_stats`` with the same options.  ``grads``: an
+    mu from ``attn_jvp_fwd_scored_stats`` with the same options.  All inputs must be
+    finite, those of rows that see nothing too.  ``grads``: an
     optional dict of preallocated outputs; ``workspace``: a CUDA uint8 tensor
     of ``bwd_scored_workspace_bytes`` bytes (allocated per call when omitted).
     Returns a dict dq, dk, dv, dtq, dtk, dtv shaped like the inputs."""

@@ -1166,7 +1166,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                 if (kEven) named_bar_sync(NB_EPI, SOFTMAX_THREADS);
                 // a row that saw no key (masks only) has lt = 0: zeros, lse = -inf
                 const float inv_l = (MASK != 0 && !(lt > 0.f)) ? 0.f : 1.f / lt;
-                const float mu = gt * inv_l;
+                // (scored: whatever such a row's q and tq hold; 0 times the NaN of a padding row would be one.  Hidden
+                // tangents zeroed with their scores, tile by tile, measured 5 % slower for documents)
+                const float mu = kScored && !(lt > 0.f) ? 0.f : gt * inv_l;
+                [[maybe_unused]] const uint32_t keep = lt > 0.f ? 0xffffffffu : 0u;
                 // group grp writes output columns 64*grp .. 64*grp+63
                 if (kSplit) {
                     // fp32 outputs straight from registers, 16 bytes per store
@@ -1255,7 +1258,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_jvp_fwd_kernel(const __grid_
                         for (int i = 0; i < 16; ++i)
                             w[i] = pack_bf16x2(
                                 fmaf(-mu, __uint_as_float(ro[2 * i]) * inv_l, __uint_as_float(rt[2 * i]) * inv_l),
-                                fmaf(-mu, __uint_as_float(ro[2 * i + 1]) * inv_l, __uint_as_float(rt[2 * i + 1]) * inv_l));
+                                fmaf(-mu, __uint_as_float(ro[2 * i + 1]) * inv_l, __uint_as_float(rt[2 * i + 1]) * inv_l)) & keep;
                         stage(first ^ 1u, h, w);
                     }
                     fence_proxy_async_smem();

@@ -412,8 +412,11 @@ AJVP_API int64_t attn_jvp_bwd_key_split_parts(int64_t B, int64_t H, int64_t Lq, 
  * Supported: d == 128, Lq, Lk < 2^24; 2 s log2(e) / c finite; tensors and
  * lse 16-byte, slopes and bounds 4-byte aligned; other rules and errors as
  * attn_jvp_fwd (AJVP_ERR_INVALID_ARG also for H not a multiple of Hkv and for
- * a negative or non-finite softcap).  Values of keys that a row does not see
- * must be finite where they share a 64-key tile with keys that it sees.
+ * a negative or non-finite softcap).  Every 128-row tile of queries multiplies
+ * its weights, zeros among them, with all keys and values (k, v, tk, tv) of the
+ * 64-key tiles between its rows' smallest and largest visible key: those must
+ * be finite, also where a row does not see them.  q and tq of rows that see
+ * nothing may hold anything.
  */
 AJVP_API int attn_jvp_fwd_scored(const void *q, const void *k, const void *v,
                         const void *tq, const void *tk, const void *tv,
@@ -453,10 +456,11 @@ AJVP_API int attn_jvp_fwd_scored_stats(const void *q, const void *k, const void 
  *                         8 B ceil(Lk / 128) bytes, each rounded up to a
  *                         multiple of 256, run it unsplit.
  *
- * Two kernels on `stream` (three when the key side is split), no atomics.  Gradients of rows that see no key and of keys that no
- * row sees are zero (all inputs of such rows must be finite, too); Lq == 0
- * writes zeros to dk, dv, dtk, dtv.  Other rules and errors as
- * attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
+ * Two kernels on `stream` (three when the key side is split), no atomics.
+ * Gradients of rows that see no key and of keys that no row sees are zero; all
+ * inputs of such rows and keys must be finite here (q, tq, o, to, dout and dtout
+ * of rows that see nothing included).  Lq == 0 writes zeros to dk, dv, dtk, dtv.
+ * Other rules and errors as attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
  */
 AJVP_API int attn_jvp_bwd_scored(const void *q, const void *k, const void *v,
                  const void *tq, const void *tk, const void *tv,

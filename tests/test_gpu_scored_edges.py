@@ -5,9 +5,37 @@ import pytest
 import torch
 
 import attention_forward_mode_b200 as ajvp
-from test_gpu_scored import NAMES, against_reference, make, slopes_of
+import scored_reference as ref
+from test_gpu_scored import NAMES, against_reference, make, ref_opts, slopes_of
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0), dict(softcap=200.0), dict(bias=1.0), dict(bias=40.0),
+                                dict(softcap=30.0, bias=1.0), dict(softcap=200.0, bias=1.0)], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+def test_padding_rows_that_are_not_finite(kw, bad):
+    """Rows that see nothing give zeros whatever their q and tq hold, also inside a tile of live rows.  The other
+    rows are the definition's."""
+    kw = dict(kw)
+    if "bias" in kw:
+        kw["slopes"] = slopes_of(4) * kw.pop("bias")
+    inp, _ = make(1, 4, 2, 300, 300, seed=31)
+    begin, end = ajvp.key_bounds(300, documents=[0, 40, 170, 233])  # rows 233 .. 299 are padding
+    begin[50:60], end[50:60] = 90, 90  # and ten rows inside a document see nothing
+    dead = end <= begin
+    x = {n: t.clone() for n, t in inp.items()}
+    x["q"][:, :, dead], x["tq"][:, :, dead] = bad, -bad
+    o = ajvp.attn_jvp_fwd_scored_stats(*(x[n] for n in NAMES), key_begin=begin, key_end=end, **kw)
+    (ro, rto, rlse, _), (eo, eto) = ref.forward(*(inp[n] for n in NAMES), 128 ** -0.5, bounds=True,
+                                                **ref_opts(dict(kw, key_begin=begin, key_end=end), 1))
+    ref.check("o", o[0], ro, eo)
+    ref.check("to", o[1], rto, eto)
+    live = ~dead
+    assert ((o[2] - rlse)[:, :, live].abs() <= 2.0 ** -15 * (1.0 + rlse[:, :, live].abs())).all()
+    assert torch.isfinite(o[3]).all()
+    assert (o[0][:, :, dead] == 0).all() and (o[1][:, :, dead] == 0).all() and (o[3][:, :, dead] == 0).all()
+    assert (o[2][:, :, dead] == -float("inf")).all()
 
 
 @pytest.mark.parametrize("H,B,Lq", [(65536, 1, 1), (32768, 2, 130)])
