@@ -126,10 +126,12 @@ def attn_jvp_fwd_cache(q, tq, k_cache, v_cache, k_scale, v_scale, block_table, c
 
     q, tq: bf16 [n_seq, H, n, 128], any strides that are multiples of 8 with
     the channels together; or packed [H, total, 128] with ``cu_seqlens`` (int32
-    [n_seq + 1]) and ``max_seqlen`` (at least the most tokens of one sequence;
-    ``total`` when omitted), the layout of ``attn_jvp_cache_append``.
+    [n_seq + 1]) and ``max_seqlen`` (at least the most tokens of one sequence: a
+    sequence's tokens from there on are neither computed nor written; ``total`` when
+    omitted, for which the launch is then planned, so give it where it is
+    known), the layout of ``attn_jvp_cache_append``.
     ``cache_lens`` (int32 [n_seq]) counts the cached tokens, the query tokens' own
-    included: token t of n stands at position cache_lens - n + t and sees the
+    included: token t of a sequence's m stands at position cache_lens - m + t and sees the
     keys up to its own (``causal``; rows at negative positions see nothing), or
     every cached key.  ``softcap`` and ``slopes`` modify the scores as in
     ``attn_jvp_fwd_scored``.  ``workspace``: a CUDA uint8 tensor of

@@ -491,9 +491,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     const int tile = unit % p.tiles, bh = unit / p.tiles;
     const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
     int n = p.n, first = 0;  // this sequence's query tokens and their first row
+    int n_all = n;           // (packed: n of these are computed)
     if (p.cu) {
         first = min(max(p.cu[b], 0), p.total);
-        n = min(max(min(max(p.cu[b + 1], 0), p.total) - first, 0), p.n);
+        n_all = max(min(max(p.cu[b + 1], 0), p.total) - first, 0);
+        n = min(n_all, p.n);
     }
     const int n_rows = p.group * n;
     if (tile * ROWS >= n_rows) return;  // (the same for every CTA of the cluster)
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         for (int i = 0; i < R; ++i) {
             const int r = tile * ROWS + (kTan ? nt * 4 + c : nt * 8 + 2 * c + i);
             const bool live = r < n_rows;
-            pos[nt][i] = len - n + (live ? r % n : 0);
+            pos[nt][i] = len - n_all + (live ? r % n : 0);
             end[nt][i] = live && p.causal ? min(max(pos[nt][i] + 1, 0), len) : len;
             slope2[nt][i] = p.slopes && live ? p.slopes[hk * p.group + r / n] * 1.4426950408889634f : 0.f;
             least = min(least, end[nt][i]);

@@ -538,11 +538,16 @@ AJVP_API int attn_jvp_cache_append(const void *k, const void *v, const void *q, 
  *                     may be NULL); packed: [H][total][d], [H][total]
  *   k_cache .. block_table : as attn_jvp_cache_append wrote them
  *   cache_lens      : DEVICE int32 [n_seq] cached tokens, the query tokens' own
- *                     included: token t of n is at position cache_lens[b] - n + t
+ *                     included: token t of the sequence's m is at position
+ *                     cache_lens[b] - m + t (m: n, or packed cu_seqlens[b + 1] -
+ *                     cu_seqlens[b])
  *   cu_seqlens      : DEVICE int32 [n_seq + 1], or NULL
  *   slopes          : DEVICE float [H], or NULL; the distance is |position - j|
  *   n               : query tokens per sequence (packed: at least the most of
- *                     one sequence, at most total; further ones are not computed)
+ *                     one sequence, at most total; a sequence's tokens from the
+ *                     n'th on are neither computed nor written.  The launch is
+ *                     planned for n rows of every sequence: total in place of
+ *                     the most is right, but slower)
  *   causal          : key j visible iff j <= position; 0: every cached key
  *
  * Rows that see no key give zeros and lse = -infinity.  Pages outside

@@ -1,0 +1,52 @@
+"""The paged 8-bit cache where its attention could go wrong quietly: early
+tokens that hardly count, truncated rows, scales of zero, wide caps, values
+that are all zero, chunks of many query tokens."""
+import numpy as np
+import pytest
+import torch
+
+import attention_forward_mode_b200 as ajvp
+import cache_reference as ref
+from test_gpu_cache import check_rows, empty_cache, filled, tables
+
+pytestmark = pytest.mark.gpu
+S = 128 ** -0.5
+
+
+@pytest.mark.parametrize("tangent", [True, False])
+def test_rows_within_an_underestimated_max_seqlen(tangent):
+    """Rows past max_seqlen are not computed; the others stand where they stand, whatever max_seqlen is."""
+    counts, lens, H, most = [5, 2, 0, 9], [200, 40, 16, 333], 4, 3
+    cache, table, g = filled(4, 2, 32, lens, seed=42)
+    cu = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    q, tq = (torch.randn((H, cu[-1], 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    o, to = torch.full_like(q, 5.0), torch.full_like(q, 5.0)
+    lse = torch.full((H, cu[-1]), 5.0, device="cuda")
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ajvp.attn_jvp_fwd_cache(q, tq if tangent else None, *cache, table, dev(lens), cu_seqlens=dev(cu), max_seqlen=most,
+                            o=o, to=to if tangent else None, lse=lse)
+    some = [b for b, n in enumerate(counts) if n]  # (the reference takes sequences that have rows)
+    rows = [slice(cu[b], cu[b + 1]) for b in some]
+    want = ref.attention([q[:, r] for r in rows], [tq[:, r] for r in rows] if tangent else None, *cache, table[some],
+                         [lens[b] for b in some], S)
+    for r, (ro, rto, rlse, bo, bto) in zip(rows, want):
+        n = min(most, r.stop - r.start)
+        assert ((o[:, r][:, :n].double() - ro[:, :n]).abs() <= bo[:, :n]).all()
+        if tangent:
+            assert ((to[:, r][:, :n].double() - rto[:, :n]).abs() <= bto[:, :n]).all()
+        assert ((lse[:, r][:, :n] - rlse.cuda()[:, :n]).abs() <= 2.0 ** -15 * (1.0 + rlse.cuda()[:, :n].abs())).all()
+        assert all((x[:, r][:, n:] == 5.0).all() for x in (o, lse) + ((to,) if tangent else ()))
+
+
+@pytest.mark.parametrize("case", [(4, 2, 300, 32, [1000, 300, 17], 30.0, True), (2, 1, 1560, 64, [4680], 0.0, True),
+                                  (5, 1, 701, 16, [800, 1500], 0.0, False)],
+                         ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_chunks_of_many_query_tokens(case):
+    """Whole chunks and frames of queries over the cache; where a sequence is shorter than the chunk, its first
+    rows stand at negative positions and see nothing."""
+    H, Hkv, n, page, lens, cap, tangent = case
+    cache, table, g = filled(len(lens), Hkv, page, lens, seed=46)
+    q, tq = (torch.randn((len(lens), H, n, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, to, lse = ajvp.attn_jvp_fwd_cache(q, tq if tangent else None, *cache, table, lens_d, softcap=cap)
+    check_rows(o, to, lse, ref.attention(list(q), list(tq) if tangent else None, *cache, table, lens, S, cap))
