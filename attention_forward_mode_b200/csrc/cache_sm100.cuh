@@ -524,9 +524,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         const int id = table[page_index(2 * run + lane)];
         return (unsigned)id < (unsigned)p.n_pages ? id : -1;
     };
-    // ... and its copy; returns its {key, value} scales (0: hidden)
+    // ... and its copy; returns its {key, value} scales (key -1, which no scale is: hidden)
     auto copy = [&](int run, int id, int stage) -> float2 {
-        float2 sc = make_float2(0.f, 0.f);
+        float2 sc = make_float2(-1.f, 0.f);
         if (lane < 2 && run < run1) {
             const uint32_t bar = bars + 8u * stage, d = ring + (uint32_t)(stage * STAGE_BYTES + lane * HALF_BYTES);
             if (id >= 0) {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         for (int h = 0; h < 2; ++h) {
             kscale[h] = __shfl_sync(0xffffffffu, held[0].x, h);
             vscale[h] = __shfl_sync(0xffffffffu, held[0].y, h);
-            valid[h] = kscale[h] != 0.f;
+            valid[h] = kscale[h] != -1.f;  // (a scale of 0 counts: its keys are zero)
         }
 
         // S^T of tokens gr (elements 0, 1) and gr + 8 (2, 3) of each half; two chains of four

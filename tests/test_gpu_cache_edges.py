@@ -38,6 +38,26 @@ def test_rows_within_an_underestimated_max_seqlen(tangent):
         assert all((x[:, r][:, n:] == 5.0).all() for x in (o, lse) + ((to,) if tangent else ()))
 
 
+def test_scales_of_zero():
+    """A page whose key scale is 0 holds zero keys: its tokens score 0 and count.  A value scale of 0: zero values."""
+    lens, H, Hkv, page = [300, 33], 4, 2, 16
+    cache, table, g = filled(2, Hkv, page, lens, seed=43)
+    cache[2][table[0, 3], 0] = cache[2][table[0, 4]] = cache[2][table[1, 2], 1] = 0.0
+    cache[3][table[0, 4], 1] = cache[3][table[0, 9]] = 0.0
+    q, tq = (torch.randn((2, H, 3, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for t in (tq, None):
+        o, to, lse = ajvp.attn_jvp_fwd_cache(q, t, *cache, table, lens_d)
+        check_rows(o, to, lse, ref.attention(list(q), None if t is None else list(t), *cache, table, lens, S))
+    zero = [torch.zeros_like(t.view(torch.uint8)).view(t.dtype) if t.dim() == 4 else torch.zeros_like(t) for t in cache]
+    o, to, lse = ajvp.attn_jvp_fwd_cache(q[:, :, :1], tq[:, :, :1], *zero, table, lens_d)
+    assert (o == 0).all() and (to == 0).all()
+    want = torch.log(lens_d.double())[:, None, None]
+    # scores of 0 against a reference of some -107 in log2 units (a value scale of 0 counts as 2^-100): fp32 holds
+    # log2 of the weights' sum, up to 116, to 2^-18, and lg2.approx errs by some steps more; 2^-15 as elsewhere
+    assert ((lse.double() - want).abs() <= 2.0 ** -15).all()
+
+
 @pytest.mark.parametrize("case", [(4, 2, 300, 32, [1000, 300, 17], 30.0, True), (2, 1, 1560, 64, [4680], 0.0, True),
                                   (5, 1, 701, 16, [800, 1500], 0.0, False)],
                          ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
