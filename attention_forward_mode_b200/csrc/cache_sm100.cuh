@@ -352,6 +352,10 @@ struct AttnParams {
     unsigned page_magic;          // ceil(2^32 / (page / 16)): x / (page / 16) = umulhi(x, magic); 0 for pages of 16
 };
 
+// The least exponent of a value scale that the references follow (a page of zeros has 2^-100): 2^24 exponentials
+// of at most 2^88.75 stay below 2^113, and their products with dS below 2^128 for dS up to 2^15 units.  Under
+// smaller scales weights are at most 2^(8.75 + 80 - 100), which f16 holds to 2^-13 of the largest.
+constexpr int EV_MIN = -80;
 constexpr int EW_MIN = -120;                         // T's unit before any weight
 constexpr int HALF_BYTES = 16 * HD;                  // 16 tokens of keys, or of values
 constexpr int STAGE_BYTES = 4 * HALF_BYTES;          // 32 tokens: keys, then values
@@ -730,8 +734,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                                 if constexpr (kTan) dS[h][nt][e] = 0.f;  // (codes past the end may be NaN)
                             }
         }
-        // running references: weights 2^(y + ev - m), the largest 2^7 when set, at most 2^8.75 = 430
-        const float ev[2] = {(float)exponent_of(vscale[0]), (float)exponent_of(vscale[1])};
+        // running references: weights 2^(y + ev - m), the largest 2^7 when set, at most 2^8.75 = 430.  exp2(y - m)
+        // is 2^-ev times a weight: below EV_MIN its sums, and those of its products with dS, could pass 2^128
+        const float ev[2] = {(float)max(exponent_of(vscale[0]), EV_MIN), (float)max(exponent_of(vscale[1]), EV_MIN)};
         bool need = false;
         float top[NT][R];
 #pragma unroll

@@ -53,9 +53,26 @@ def test_scales_of_zero():
     o, to, lse = ajvp.attn_jvp_fwd_cache(q[:, :, :1], tq[:, :, :1], *zero, table, lens_d)
     assert (o == 0).all() and (to == 0).all()
     want = torch.log(lens_d.double())[:, None, None]
-    # scores of 0 against a reference of some -107 in log2 units (a value scale of 0 counts as 2^-100): fp32 holds
-    # log2 of the weights' sum, up to 116, to 2^-18, and lg2.approx errs by some steps more; 2^-15 as elsewhere
+    # scores of 0 against a reference of some -100 in log2 units (a value scale of 0 counts as a very small one):
+    # fp32 holds log2 of the weights' sum to 2^-18, and lg2.approx errs by some steps more; 2^-15 as elsewhere
     assert ((lse.double() - want).abs() <= 2.0 ** -15).all()
+
+
+def test_values_that_are_all_zero():
+    """A context of zero values, large keys and small queries: O and tO are zeros, lse is what it is."""
+    lens, H, page = [4096, 100], 2, 64
+    cache, table, g = filled(2, 1, page, lens, seed=45)
+    total = sum(lens)
+    k = (torch.randn((1, total, 128), generator=g, device="cuda") * 2.0 ** 14).bfloat16()
+    cu = torch.tensor([0, lens[0], total], dtype=torch.int32, device="cuda")
+    ajvp.attn_jvp_cache_append(k, torch.zeros_like(k), *cache, table, torch.zeros(2, dtype=torch.int32, device="cuda"), cu)
+    q = (torch.randn((2, H, 1, 128), generator=g, device="cuda") * 2.0 ** -13).bfloat16()
+    tq = torch.randn((2, H, 1, 128), generator=g, device="cuda").bfloat16()
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, to, lse = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens_d)
+    assert (o == 0).all() and (to == 0).all()
+    for b, (_, _, rlse, _, _) in enumerate(ref.attention(list(q), list(tq), *cache, table, lens, S)):
+        assert ((lse[b] - rlse).abs() <= 2.0 ** -15 * (1.0 + rlse.abs())).all()
 
 
 @pytest.mark.parametrize("case", [(4, 2, 300, 32, [1000, 300, 17], 30.0, True), (2, 1, 1560, 64, [4680], 0.0, True),
