@@ -293,7 +293,8 @@ int attn_jvp_fwd_cache(const void *q, const void *tq, void *o, void *to, float *
     p.q_t = stride_t;
     p.o_b = cu_seqlens ? 0 : H * n;
     p.o_h = cu_seqlens ? total : n;
-    p.cap_in = softcap > 0.f ? 2.f * log2e / softcap : 0.f;
+    p.cap_in = softcap > 0.f ? 2.f / softcap : 0.f;
+    p.cap_w = softcap > 0.f ? 1.f / (softcap * log2e) : 0.f;
     p.cap_out = softcap * log2e;
     p.scale = scale;
     p.B = (int)n_seq;

@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "score_sm100.cuh"
 
 namespace ajvp {
@@ -340,7 +342,8 @@ struct AttnParams {
     const float *ks, *vs;
     const int *table, *lens;
     const float *slopes;          // [H] or NULL
-    float cap_in, cap_out;        // 2 log2(e) / c (of scaled scores) and c log2(e); 0: no cap
+    float cap_in, cap_w, cap_out; // of log2-unit scores y: tanh(z / c) = 1 - 2 / (1 + 2^(cap_in y)), z / c = cap_w y; c log2(e)
+                                  // (0: no cap)
     float scale;
     int B, H, Hkv, group, n_pages, page, table_width, causal;
     int n;                        // query tokens per sequence (packed: of the longest)
@@ -691,22 +694,58 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                     if constexpr (kTan) dS[h][nt][e] = (S[h][nt][2 * e + 1] + S2[h][nt][2 * e + 1]) * kscale[h];
                 }
         }
-        if (p.cap_out > 0.f) {
+        const bool partial = (run + 1) * 32 > least || !valid[0] || !valid[1];
+        auto hide = [&](float as) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        float2 t, df;
-                        cap2(make_float2(y[h][nt][i][0], y[h][nt][i][1]), p.cap_in * 0.69314718055994531f, t, df);
-                        y[h][nt][i][0] = t.x * p.cap_out;
-                        y[h][nt][i][1] = t.y * p.cap_out;
-                        if constexpr (kTan) {
-                            dS[h][nt][0] *= df.x;
-                            dS[h][nt][1] *= df.y;
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < R; ++i)
+                            if (!valid[h] || run * 32 + 16 * h + gr + 8 * e >= end[nt][i]) {
+                                y[h][nt][i][e] = as;
+                                if constexpr (kTan) dS[h][nt][e] = 0.f;  // (codes past the end may be NaN)
+                            }
+        };
+        if (p.cap_out > 0.f) {
+            // scores well below the cap by the polynomial: the exponential's tanh is exact to 2^-23 absolute, which
+            // a wide cap multiplies.  Hidden scores, which may come from anything, have no say in the choice.
+            if (partial) hide(0.f);
+            float most = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        most = fmax3(most, fabsf(y[h][nt][i][0]), fabsf(y[h][nt][i][1]));
+            auto cap = [&](auto small) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            const float2 x = make_float2(y[h][nt][i][0], y[h][nt][i][1]);
+                            float2 t, df;
+                            if constexpr (decltype(small)::value)
+                                cap2_small(x, p.cap_w, t, df);
+                            else
+                                cap2(x, p.cap_in, t, df);
+                            y[h][nt][i][0] = t.x * p.cap_out;
+                            y[h][nt][i][1] = t.y * p.cap_out;
+                            if constexpr (kTan) {
+                                dS[h][nt][0] *= df.x;
+                                dS[h][nt][1] *= df.y;
+                            }
                         }
-                    }
+            };
+            if (__all_sync(0xffffffffu, most * p.cap_w <= CAP_SMALL))
+                cap(std::true_type{});
+            else
+                cap(std::false_type{});
         }
         if (p.slopes) {
 #pragma unroll
@@ -720,20 +759,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                         y[h][nt][i][1] = fmaf(-slope2[nt][i], fabsf(dist - 8.f), y[h][nt][i][1]);
                     }
         }
-        if ((run + 1) * 32 > least || !valid[0] || !valid[1]) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int i = 0; i < R; ++i)
-                            if (!valid[h] || run * 32 + 16 * h + gr + 8 * e >= end[nt][i]) {
-                                y[h][nt][i][e] = -INFINITY;
-                                if constexpr (kTan) dS[h][nt][e] = 0.f;  // (codes past the end may be NaN)
-                            }
-        }
+        if (partial) hide(-INFINITY);
         // running references: weights 2^(y + ev - m), the largest 2^7 when set, at most 2^8.75 = 430.  exp2(y - m)
         // is 2^-ev times a weight: below EV_MIN its sums, and those of its products with dS, could pass 2^128
         const float ev[2] = {(float)max(exponent_of(vscale[0]), EV_MIN), (float)max(exponent_of(vscale[1]), EV_MIN)};

@@ -58,6 +58,17 @@ def test_scales_of_zero():
     assert ((lse.double() - want).abs() <= 2.0 ** -15).all()
 
 
+@pytest.mark.parametrize("cap", [1e3, 1e5, 1e7, 1e20])
+def test_caps_far_above_the_scores(cap):
+    """A cap of 1e7 is no cap: the scores are as exact as without one."""
+    lens, H = [500, 70], 6
+    cache, table, g = filled(2, 2, 32, lens, seed=44)
+    q, tq = (torch.randn((2, H, 2, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, to, lse = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens_d, softcap=cap)
+    check_rows(o, to, lse, ref.attention(list(q), list(tq), *cache, table, lens, S, cap))
+
+
 def test_values_that_are_all_zero():
     """A context of zero values, large keys and small queries: O and tO are zeros, lse is what it is."""
     lens, H, page = [4096, 100], 2, 64
