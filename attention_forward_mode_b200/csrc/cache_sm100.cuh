@@ -329,8 +329,12 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) cache_append_kernel(const _
 // 2^-14 below it).  P is weighted by its page's value scale and a row's reference
 // M covers both: it is set so that the largest weight is 2^7 and moves when one
 // would pass 2^8.75, so weights 2^-21 below the row's largest start to lose bits.
-// P dS, with dS relative to the row's first run (r, so that a nearly constant dS
-// does not cancel against mu O), has a power of two of its own, kept the same way.
+// P dS is rounded with dS relative to r, a mean of dS over at least a sixteenth of
+// the weight that the warp has summed so far, so that neither a nearly constant dS
+// nor that of tokens that hardly count (far ones under a bias come first) costs
+// bits; it has a power of two of its own, kept the same way.  (An eighth in place
+// of a sixteenth: 26.2 against 25.7 us for one sequence of 32760 tokens with 40 heads
+// on 8; r of the first run alone: 24.9, but tO was lost where that run weighs little.)
 struct AttnParams {
     const __nv_bfloat16 *q, *tq;  // row (b, h, t) at q_b b + q_h h + q_t t channels; packed: cu[b] + t in place of t
     __nv_bfloat16 *o, *to;        // rows o_b b + o_h h + t (packed: + cu[b])
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
     least = __reduce_min_sync(0xffffffffu, least);
 
     float acc[NT][8][4];  // channels 16 gr + 2 j + {0, 1} (pairs of elements), columns 2 c + {0, 1}
-    float m[NT][R], l[NT][R], g[NT], r0[NT];
+    float m[NT][R], l[NT][R], g[NT], r0[NT], lr[NT];  // lr: the row's sum when r was set
     int ew[NT];  // T is in units of 2^ew
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -629,10 +633,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
             m[nt][i] = -INFINITY;
             l[nt][i] = 0.f;
         }
-        g[nt] = r0[nt] = 0.f;
+        g[nt] = r0[nt] = lr[nt] = 0.f;
         ew[nt] = EW_MIN;
     }
-    bool begun = false;
 
     int stage = 0;
     uint32_t phase = 0;
@@ -785,7 +788,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                         m[nt][i] = mx;
                     }
                     l[nt][i] *= alpha[i];
-                    if constexpr (kTan) g[nt] *= alpha[i];
+                    if constexpr (kTan) {
+                        g[nt] *= alpha[i];
+                        lr[nt] *= alpha[i];
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -805,22 +811,45 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                     for (int e = 0; e < 2; ++e) pe[h][nt][i][e] = ex2_approx(y[h][nt][i][e] - ref);
                 l[nt][i] += (pe[0][nt][i][0] + pe[0][nt][i][1]) + (pe[1][nt][i][0] + pe[1][nt][i][1]);
             }
-        if (kTan && !begun) {  // r: the first run's weighted mean of dS
+        if constexpr (kTan) {
+            // r, a mean of dS over at least a sixteenth of the row's weight so far: by the time the sum has grown
+            // sixteenfold, one of the row's eight threads holds more than twice the sum at r
+            bool grown = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w = 0.f, s = 0.f;
+            for (int nt = 0; nt < NT; ++nt) grown |= l[nt][0] > 2.f * lr[nt];
+            if (__any_sync(0xffffffffu, grown)) {
+                float dr[NT];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float s = g[nt];  // with this run's
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        w += pe[h][nt][0][e];
-                        s = fmaf(pe[h][nt][0][e], dS[h][nt][e], s);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) s = fmaf(pe[h][nt][0][e], dS[h][nt][e] - r0[nt], s);
+                    s = column_sum(s);
+                    lr[nt] = column_sum(l[nt][0]);
+                    const float r = lr[nt] > 0.f ? r0[nt] + s / lr[nt] : r0[nt];
+                    dr[nt] = r - r0[nt];
+                    r0[nt] = r;
+                }
+                if (run != run0 + warp) {  // the sums of earlier runs move to the new r
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float now = (pe[0][nt][0][0] + pe[0][nt][0][1]) + (pe[1][nt][0][0] + pe[1][nt][0][1]);
+                        g[nt] = fmaf(-dr[nt], l[nt][0] - now, g[nt]);
+                        // sum p (dS - r') V = sum p (dS - r) V - (r' - r) sum p V, whose last product stays inside
+                        // fp32 in these units with sums of up to 2^42
+                        const int e = max(ew[nt], binary_exponent(dr[nt]) - 80);
+                        const float f = pow2_or_0(ew[nt] - e), d = -dr[nt] * pow2(-e);
+                        ew[nt] = e;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            acc[nt][j][1] = fmaf(d, acc[nt][j][0], acc[nt][j][1] * f);
+                            acc[nt][j][3] = fmaf(d, acc[nt][j][2], acc[nt][j][3] * f);
+                        }
                     }
-                w = column_sum(w);
-                s = column_sum(s);
-                r0[nt] = w > 0.f ? s / w : 0.f;
+                }
             }
-            begun = true;
         }
         float wt[2][NT][2][2];  // the columns of P^T: [half][][column 2 c + i][token gr + 8 e]
 #pragma unroll

@@ -13,6 +13,60 @@ pytestmark = pytest.mark.gpu
 S = 128 ** -0.5
 
 
+def leading(low, q0, far, seed=41):
+    """One decoding token of each of 32 sequences over 1024 tokens, 8 heads (256 sequences and heads, a CTA each).
+    The first 128 tokens, whole runs of every warp, score ``low q0`` / sqrt(128) below the others and have a score
+    tangent of 8 ``far`` / sqrt(128) (``far`` a pair: its two values in turn), the others one of the order of 1."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n_seq, Hkv, L, lead, page = 32, 8, 1024, 128, 64
+    table, pages = tables(n_seq, L // page, 1, seed)
+    cache, table = empty_cache(pages, Hkv, page, seed), table.cuda()
+    k, v = (torch.randn((Hkv, n_seq, L, 128), generator=g, device="cuda") for _ in range(2))
+    k[:, :, :lead, 0] = -low
+    for i, f in enumerate(far):
+        k[:, :, i:lead:len(far), 1] = f
+    q, tq = (torch.randn((n_seq, Hkv, 1, 128), generator=g, device="cuda") * 0.05 for _ in range(2))
+    q[..., 0], q[..., 1], tq[..., 1], tq[..., 0] = q0, 0.0, 8.0, 0.0
+    cu = torch.arange(n_seq + 1, dtype=torch.int32, device="cuda") * L
+    flat = lambda x: x.flatten(1, 2).bfloat16()  # noqa: E731
+    ajvp.attn_jvp_cache_append(flat(k), flat(v), *cache, table, torch.zeros(n_seq, dtype=torch.int32, device="cuda"), cu)
+    return q.bfloat16(), tq.bfloat16(), cache, table, torch.full((n_seq,), L, dtype=torch.int32, device="cuda")
+
+
+def tangent_parts(q, tq, cache, table, L):
+    """to in 64 bits, and per row: P, dS - mu, V."""
+    k8, v8, ks, vs = cache
+    k, v = (c[table.long()].double().mul(f[table.long()].double()[..., None, None]).transpose(1, 2).flatten(2, 3)[:, :, :L]
+            for c, f in ((k8, ks), (v8, vs)))
+    P = torch.softmax(S * (q.double() @ k.mT), -1)
+    u = S * (tq.double() @ k.mT)
+    u = u - (P * u).sum(-1, keepdim=True)
+    return (P * u) @ v, P, u, v
+
+
+def independent_roundings(to, P, u, v):
+    """A row's rounding error in the mean square, [.., 1, 128]: weights P (dS - r) rounded to f16 and outputs to
+    bf16, each off by at most half a step h relative and h / sqrt(3) in the mean, independently.  The reference r
+    is a mean of dS over at least a sixteenth of the weight summed so far, so that |r - mu| <= 16 sum P |dS - mu|."""
+    h = ref.U16 * (u.abs() + 16 * (P * u.abs()).sum(-1, keepdim=True)) * P
+    return (h.square() @ v.square() + (ref.UB * to).square()) / 3
+
+
+def as_exact_as_its_roundings(args):
+    q, tq, cache, table, lens = args
+    o, to, _ = ajvp.attn_jvp_fwd_cache(q, tq, *cache, table, lens)
+    rto, P, u, v = tangent_parts(q, tq, cache, table, int(lens[0]))
+    mean_square = independent_roundings(rto, P, u, v).sum()
+    # 256 x 128 outputs, a sum of many independent errors: twice its mean in norm is far outside
+    assert (to.double() - rto).square().sum() <= 4 * mean_square
+
+
+@pytest.mark.parametrize("low,far", [(16.0, 400.0), (24.0, 6000.0)])
+def test_tangents_after_tokens_that_hardly_count(low, far):
+    """The first tokens weigh 2^-16 (2^-24) of a later one: tO is as exact as without them."""
+    as_exact_as_its_roundings(leading(low, 8.0, (far,)))
+
+
 @pytest.mark.parametrize("tangent", [True, False])
 def test_rows_within_an_underestimated_max_seqlen(tangent):
     """Rows past max_seqlen are not computed; the others stand where they stand, whatever max_seqlen is."""
