@@ -332,9 +332,10 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) cache_append_kernel(const _
 // P dS is rounded with dS relative to r, a mean of dS over at least a sixteenth of
 // the weight that the warp has summed so far, so that neither a nearly constant dS
 // nor that of tokens that hardly count (far ones under a bias come first) costs
-// bits; it has a power of two of its own, kept the same way.  (An eighth in place
-// of a sixteenth: 26.2 against 25.7 us for one sequence of 32760 tokens with 40 heads
-// on 8; r of the first run alone: 24.9, but tO was lost where that run weighs little.)
+// bits; it has a power of two of its own, which rises with it and falls with the
+// weights.  (An eighth in place of a sixteenth: 26.2 against 25.7 us for one sequence
+// of 32760 tokens with 40 heads on 8; a unit that falls: 26.1; r of the first run
+// alone: 24.9, but tO was lost where that run weighs little.)
 struct AttnParams {
     const __nv_bfloat16 *q, *tq;  // row (b, h, t) at q_b b + q_h h + q_t t channels; packed: cu[b] + t in place of t
     __nv_bfloat16 *o, *to;        // rows o_b b + o_h h + t (packed: + cu[b])
@@ -621,7 +622,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
 
     float acc[NT][8][4];  // channels 16 gr + 2 j + {0, 1} (pairs of elements), columns 2 c + {0, 1}
     float m[NT][R], l[NT][R], g[NT], r0[NT], lr[NT];  // lr: the row's sum when r was set
-    int ew[NT];  // T is in units of 2^ew
+    int ew[NT];    // T is in units of 2^ew
+    float mw[NT];  // m when the unit was set
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -635,6 +637,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
         }
         g[nt] = r0[nt] = lr[nt] = 0.f;
         ew[nt] = EW_MIN;
+        mw[nt] = -INFINITY;
     }
 
     int stage = 0;
@@ -839,9 +842,13 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                         g[nt] = fmaf(-dr[nt], l[nt][0] - now, g[nt]);
                         // sum p (dS - r') V = sum p (dS - r) V - (r' - r) sum p V, whose last product stays inside
                         // fp32 in these units with sums of up to 2^42
-                        const int e = max(ew[nt], binary_exponent(dr[nt]) - 80);
-                        const float f = pow2_or_0(ew[nt] - e), d = -dr[nt] * pow2(-e);
+                        // The unit falls as far as the weights that it was set by have since m rose (T with them, so
+                        // that it stays in range; by more than 2^126 it is nothing).
+                        const int by = (int)fminf(m[nt][0] - mw[nt], (float)(ew[nt] - EW_MIN));
+                        const int e = max(ew[nt] - by, binary_exponent(dr[nt]) - 80);
+                        const float f = ew[nt] - e > 126 ? 0.f : pow2_or_0(ew[nt] - e), d = -dr[nt] * pow2(-e);
                         ew[nt] = e;
+                        mw[nt] = m[nt][0];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             acc[nt][j][1] = fmaf(d, acc[nt][j][0], acc[nt][j][1] * f);
@@ -884,6 +891,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? (NT == 1 ? 3 : 2) : 1
                     if (e > ew[nt]) {
                         const float r = pow2_or_0(ew[nt] - e);
                         ew[nt] = e;
+                        mw[nt] = m[nt][0];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             acc[nt][j][1] *= r;

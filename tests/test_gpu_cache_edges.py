@@ -67,6 +67,11 @@ def test_tangents_after_tokens_that_hardly_count(low, far):
     as_exact_as_its_roundings(leading(low, 8.0, (far,)))
 
 
+def test_the_unit_of_tangents_follows_the_weights():
+    """First tokens of some 2^-60 of a later one's weight, whose score tangents are 2^30 times as large."""
+    as_exact_as_its_roundings(leading(2.0 ** 14, 0.029, (2.0 ** 30, -(2.0 ** 30))))
+
+
 @pytest.mark.parametrize("tangent", [True, False])
 def test_rows_within_an_underestimated_max_seqlen(tangent):
     """Rows past max_seqlen are not computed; the others stand where they stand, whatever max_seqlen is."""
