@@ -246,7 +246,7 @@ def key_bounds(Lq: int, Lk: int | None = None, *, causal: bool = False, prefix: 
         raise ValueError("prefix belongs to the causal mask")
     p = torch.arange(Lq, device=device, dtype=torch.int64) + (Lk - Lq)
     begin, end = torch.zeros_like(p), torch.full_like(p, Lk)
-    inside = (p >= 0) | torch.tensor(not (causal or frame), device=device)
+    inside = p >= 0 if causal or frame else torch.ones_like(p, dtype=torch.bool)  # (nothing is copied from the host)
     if documents is not None:
         cu = torch.as_tensor(documents, device=device, dtype=torch.int64)
         if cu.dim() != 1 or cu.numel() < 2:

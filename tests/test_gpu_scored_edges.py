@@ -38,6 +38,37 @@ def test_padding_rows_that_are_not_finite(kw, bad):
     assert (o[2][:, :, dead] == -float("inf")).all()
 
 
+def test_a_causal_mask_made_inside_a_captured_graph():
+    """attn_jvp_autograd turns causal into bounds on the device alone: nothing is copied from the host."""
+    inp, _ = make(1, 4, 2, 150, 200, seed=32)
+    x = [inp[n] for n in NAMES]
+    call = lambda: (*ajvp.attn_jvp_autograd(*x, softcap=20.0, causal=True),  # noqa: E731
+                    *ajvp.key_bounds(150, 200, causal=True, prefix=9), *ajvp.key_bounds(150, frame=40),
+                    *ajvp.key_bounds(150, causal=True, window=31))
+    want = call()
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        got = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_far_keys_under_a_bias_and_their_gradients(cap):
+    """Rows that see only the first 20 of 700 keys: biases of up to 87 (126 in log2 units), whose fp32 roundings
+    of some 2^-17 stay below those of the bf16 weights, 2^-9."""
+    B, H, L = 1, 2, 700
+    inp, cot = make(B, H, 1, L, L, seed=33)
+    end = torch.full((L,), 20, dtype=torch.int32, device="cuda")
+    kw = dict(softcap=cap, slopes=slopes_of(H) * 2.0, key_end=end)
+    x = [inp[n] for n in NAMES]
+    out = ajvp.attn_jvp_fwd_scored_stats(*x, **kw)
+    g = ajvp.attn_jvp_bwd_scored(*x, *out, cot["dout"], cot["dtout"], **kw)
+    against_reference(inp, cot, kw, out, g)
+
+
 @pytest.mark.parametrize("H,B,Lq", [(65536, 1, 1), (32768, 2, 130)])
 def test_very_many_heads_of_one_key(H, B, Lq):
     """H query heads share one key head and key, so that O = V; tO = tV and the log-sum-exp is the score."""
