@@ -237,13 +237,16 @@ def key_bounds(Lq: int, Lk: int | None = None, *, causal: bool = False, prefix: 
     or behind the last offset.  Inside its document (else the whole sequence),
     ``causal`` hides the keys behind p except the document's first ``prefix``
     ones, ``frame`` (> 0) those behind the end of p's frame of that many keys,
-    and ``window`` (> 0) all but the last ``window`` keys up to p.
+    and ``window`` (> 0) all but the last ``window`` keys up to p (with ``frame``,
+    the keys behind p that its frame shows stay; not with ``prefix``).
     """
     Lk = Lq if Lk is None else Lk
     if Lq < 0 or Lk < 1 or prefix < 0 or frame < 0 or window < 0 or (causal and frame):
         raise ValueError("sizes must not be negative, and a mask is causal by keys or by frames")
     if prefix and not causal:
         raise ValueError("prefix belongs to the causal mask")
+    if prefix and window:
+        raise ValueError("a prefix and a window are no single interval of keys")
     p = torch.arange(Lq, device=device, dtype=torch.int64) + (Lk - Lq)
     begin, end = torch.zeros_like(p), torch.full_like(p, Lk)
     inside = p >= 0 if causal or frame else torch.ones_like(p, dtype=torch.bool)  # (nothing is copied from the host)
@@ -256,8 +259,8 @@ def key_bounds(Lq: int, Lk: int | None = None, *, causal: bool = False, prefix: 
         at = at.clamp(0, cu.numel() - 2)
         begin, end = cu[at], cu[at + 1].clamp(max=Lk)
     first = begin
-    if causal:
-        end = torch.minimum(end, torch.maximum(p + 1, first + prefix))
+    if causal or (window and not frame):
+        end = torch.minimum(end, torch.maximum(p + 1, first + prefix) if prefix else p + 1)
     if frame:
         end = torch.minimum(end, first + (torch.div(p - first, frame, rounding_mode="floor") + 1) * frame)
     if window:
