@@ -31,8 +31,10 @@ mask (key j visible to query i iff j <= i + Lk - Lq) applies unchanged.
 
 ``score`` (a dict of softcap, slopes, key_begin, key_end, any of them) selects the
 scored kernels: slopes are given for all H heads and bounds for the whole
-sequences, on every rank.  k, v, tk, tv may then have fewer heads Hkv, of which
-H is a multiple; Hkv must divide by P as well.
+sequences, on every rank (``causal`` becomes bounds where none are given).  k, v,
+tk, tv may then have fewer heads Hkv, of which H is a multiple; Hkv must divide
+by P as well.  A local step of the caller's own is called as it is where no
+``score`` is given, whatever heads k, v, tk, tv have.
 """
 from __future__ import annotations
 
@@ -54,6 +56,17 @@ def _scored_local(fn, score, H, Hkv, world, group):
         r, n = dist.get_rank(group), H // world
         opts["slopes"] = opts["slopes"][r * n:(r + 1) * n].contiguous()
     return lambda *args: fn(*args, **opts)
+
+
+def _with_causal(score, causal, Lq, Lk, device):
+    """The options of a scored call, ``causal`` turned into bounds."""
+    opts = dict(score or {})
+    if causal:
+        if opts.get("key_begin") is not None or opts.get("key_end") is not None:
+            raise ValueError("causal goes into the score's bounds: key_bounds(Lq, Lk, causal=True, ...)")
+        from ._scored import key_bounds
+        opts["key_begin"], opts["key_end"] = key_bounds(Lq, Lk, causal=True, device=device)
+    return opts
 
 
 def _to_heads(x: torch.Tensor, world: int, group) -> torch.Tensor:
@@ -98,11 +111,10 @@ def ulysses_attn_jvp(q, k, v, tq, tk, tv, scale=None, group=None, local_fn=None,
         raise ValueError(f"heads ({H}) must divide by the group size ({world})")
     if scale is None:
         scale = d ** -0.5
-    if score is not None or k.shape[1] != H:
-        if causal:
-            raise ValueError("causal goes into the score's bounds")
+    if score is not None or (local_fn is None and k.shape[1] != H):
         if local_fn is None:
             from ._scored import attn_jvp_fwd_scored as local_fn
+        score = _with_causal(score, causal, Lqs * world, Lks * world, q.device)
         fn = _scored_local(local_fn, score, H, k.shape[1], world, group)
     elif local_fn is not None:
         fn = local_fn
@@ -144,11 +156,10 @@ def ulysses_attn_jvp_train(q, k, v, tq, tk, tv, scale=None, group=None, local_fw
     if scale is None:
         scale = d ** -0.5
     heads = None  # (H, Hkv) of a scored call
-    if score is not None or k.shape[1] != H:
-        if causal:
-            raise ValueError("causal goes into the score's bounds")
+    if score is not None or (local_fwd is None and k.shape[1] != H):
         from ._scored import attn_jvp_fwd_scored_stats
         heads = (H, k.shape[1])
+        score = _with_causal(score, causal, Lqs * world, k.shape[2] * world, q.device)
         fn = _scored_local(local_fwd or attn_jvp_fwd_scored_stats, score, *heads, world, group)
     else:
         fn = local_fwd if local_fwd is not None else (attn_jvp_fwd_causal_stats if causal else attn_jvp_fwd_stats)
