@@ -37,7 +37,7 @@ EXPORTED = (
     "attn_jvp_host_workspace_bytes", "attn_jvp_bwd_host", "attn_jvp_bwd_host_workspace_bytes",
     "attn_jvp_strerror", "attn_jvp_last_cuda_error", "attn_jvp_check_device_status",
     "attn_jvp_set_wait_bound_ns", "attn_jvp_set_persistent_key_tiles", "attn_jvp_set_bwd_pairs",
-    "attn_jvp_selftest_wait_timeout",
+    "attn_jvp_selftest_wait_timeout", "attn_jvp_selftest_wait_timeout_in",
     "attn_jvp_version", "attn_jvp_fwd_scored", "attn_jvp_fwd_scored_stats", "attn_jvp_bwd_scored",
     "attn_jvp_bwd_scored_workspace_bytes", "attn_jvp_cache_append", "attn_jvp_fwd_cache",
     "attn_jvp_fwd_cache_workspace_bytes",
@@ -123,6 +123,8 @@ def load_library(path: str = LIB_PATH):
         lib.attn_jvp_set_bwd_pairs.restype = ctypes.c_int
         lib.attn_jvp_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
         lib.attn_jvp_selftest_wait_timeout.restype = ctypes.c_int
+        lib.attn_jvp_selftest_wait_timeout_in.argtypes = [ctypes.c_int, ctypes.c_uint64, vp]
+        lib.attn_jvp_selftest_wait_timeout_in.restype = ctypes.c_int
         lib.attn_jvp_fwd_scored.argtypes = [vp] * 12 + [i64] * 6 + [f32, f32, vp]
         lib.attn_jvp_fwd_scored.restype = ctypes.c_int
         lib.attn_jvp_fwd_scored_stats.argtypes = [vp] * 13 + [i64] * 6 + [f32, f32, vp]
@@ -674,9 +676,11 @@ def set_bwd_pairs(on: bool) -> None:
     _check(load_library().attn_jvp_set_bwd_pairs(1 if on else 0), "attn_jvp_set_bwd_pairs")
 
 
-def selftest_wait_timeout(bound_ns: int, stream=None) -> None:
-    _check(load_library().attn_jvp_selftest_wait_timeout(int(bound_ns), _stream_handle(stream)),
-           "attn_jvp_selftest_wait_timeout")
+def selftest_wait_timeout(bound_ns: int, stream=None, unit: int = 0) -> None:
+    """A bounded wait that runs out in the kernels of ``unit`` (0: the unmodified
+    attention, 1: the scored one, 2: the cache), for ``check_device_status`` to report."""
+    _check(load_library().attn_jvp_selftest_wait_timeout_in(int(unit), int(bound_ns), _stream_handle(stream)),
+           "attn_jvp_selftest_wait_timeout_in")
 
 
 def version() -> int:

@@ -19,6 +19,7 @@
 #include "jvp_bwd_sm100.cuh"
 #include "jvp_f32.cuh"
 #include "jvp_sm100.cuh"
+#include "selftest_sm100.cuh"
 
 namespace {
 
@@ -1100,33 +1101,21 @@ int attn_jvp_version(void) { return kVersion; }
 }  // extern "C"
 
 // ------------------------------------------------------- failure self test
-namespace {
-__global__ void selftest_wait_kernel(unsigned long long bound_ns) {
-    __shared__ __align__(8) uint64_t bar;
-    __shared__ int abort_flag;
-    const uint32_t b = ajvp::smem_u32(&bar);
-    if (threadIdx.x == 0) {
-        ajvp::mbar_init(b, 1);
-        abort_flag = 0;
-        ajvp::fence_barrier_init();
-    }
-    __syncwarp();
-    // nothing ever arrives on `bar`: the bounded wait must give up
-    bool ok = ajvp::mbar_wait(b, 0, reinterpret_cast<volatile int *>(&abort_flag), bound_ns);
-    ok = __all_sync(0xffffffffu, ok);
-    (void)ok;
-}
-}  // namespace
-
-extern "C" int attn_jvp_selftest_wait_timeout(uint64_t bound_ns, void *stream) {
+extern "C" int attn_jvp_selftest_wait_timeout_in(int unit, uint64_t bound_ns, void *stream) {
     int dev = 0;
     int rc = device_setup(&dev);
     if (rc != AJVP_OK) return rc;
-    if (bound_ns == 0 || bound_ns > 10000000000ull) return AJVP_ERR_INVALID_ARG;
-    selftest_wait_kernel<<<1, 32, 0, (cudaStream_t)stream>>>((unsigned long long)bound_ns);
-    cudaError_t e = cudaGetLastError();
+    if (bound_ns == 0 || bound_ns > 10000000000ull || unit < 0 || unit > 2) return AJVP_ERR_INVALID_ARG;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = unit == 0   ? ajvp::selftest_wait(bound_ns, false, st)
+                          : unit == 1 ? ajvp::host::scored_selftest(bound_ns, st)
+                                      : ajvp::host::cache_selftest(bound_ns, st);
     if (e != cudaSuccess) return fail_cuda(e);
     return AJVP_OK;
+}
+
+extern "C" int attn_jvp_selftest_wait_timeout(uint64_t bound_ns, void *stream) {
+    return attn_jvp_selftest_wait_timeout_in(0, bound_ns, stream);
 }
 
 // ------------------------------------------- host entry on static scratch

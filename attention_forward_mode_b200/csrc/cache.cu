@@ -13,6 +13,7 @@
 #include "attn_jvp.h"
 #include "cache_sm100.cuh"
 #include "host_common.h"
+#include "selftest_sm100.cuh"
 
 using namespace ajvp;
 
@@ -147,6 +148,7 @@ Plan make_plan(int64_t n_seq, int64_t Hkv, int64_t rows, bool tangent, int64_t t
 
 namespace ajvp {
 namespace host {
+cudaError_t cache_selftest(uint64_t bound_ns, cudaStream_t stream) { return selftest_wait(bound_ns, false, stream); }
 cudaError_t cache_status(int *word) {
     int w = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&w, g_status_word, sizeof(int));

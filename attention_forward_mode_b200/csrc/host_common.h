@@ -31,6 +31,9 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 // read into *word (ORed), cleared when set
 cudaError_t scored_status(int *word);
 cudaError_t cache_status(int *word);
+// a bounded wait in them that runs out and sets that word (scored: the sleeping form)
+cudaError_t scored_selftest(uint64_t bound_ns, cudaStream_t stream);
+cudaError_t cache_selftest(uint64_t bound_ns, cudaStream_t stream);
 
 }  // namespace host
 }  // namespace ajvp

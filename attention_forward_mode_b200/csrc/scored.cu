@@ -16,6 +16,7 @@
 #include "host_common.h"
 #include "jvp_bwd_sm100.cuh"
 #include "jvp_sm100.cuh"
+#include "selftest_sm100.cuh"
 
 using namespace ajvp;
 
@@ -257,6 +258,7 @@ int bwd_params(bwd::Params *p, std::initializer_list<const void *> r, std::initi
 
 namespace ajvp {
 namespace host {
+cudaError_t scored_selftest(uint64_t bound_ns, cudaStream_t stream) { return selftest_wait(bound_ns, true, stream); }
 cudaError_t scored_status(int *word) {
     int w = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&w, g_status_word, sizeof(int));

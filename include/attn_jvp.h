@@ -763,6 +763,15 @@ AJVP_API int attn_jvp_set_bwd_pairs(int on);
  */
 AJVP_API int attn_jvp_selftest_wait_timeout(uint64_t bound_ns, void *stream);
 
+/*
+ * The same in the translation unit that holds the kernels of a part of the
+ * library, each of which keeps a status word of its own behind
+ * attn_jvp_check_device_status: 0 as above, 1 the scored attention (with its
+ * wait that sleeps between polls), 2 the cache.  Other units are rejected
+ * (AJVP_ERR_INVALID_ARG).
+ */
+AJVP_API int attn_jvp_selftest_wait_timeout_in(int unit, uint64_t bound_ns, void *stream);
+
 /* Library version, major * 10000 + minor * 100 + patch. */
 AJVP_API int attn_jvp_version(void);
 

@@ -86,3 +86,14 @@ def test_very_many_heads_of_one_key(H, B, Lq):
     err = (to.float() - tv.float()).abs()
     bound = 2.0 ** -8 * (tv.float().abs() + mu.abs()[..., None] * v.float().abs())
     assert (err <= 1.01 * bound).all()
+
+
+@pytest.mark.parametrize("unit", [0, 1, 2])
+def test_every_status_word_reports_a_wait_that_ran_out(unit):
+    """The unmodified, the scored and the cache's kernels each set a word of their own: reported once, then clear."""
+    assert ajvp.check_device_status() == ajvp.AJVP_OK
+    ajvp.selftest_wait_timeout(1_000_000, unit=unit)
+    assert ajvp.check_device_status() == ajvp.AJVP_ERR_TIMEOUT
+    assert ajvp.check_device_status() == ajvp.AJVP_OK
+    with pytest.raises(ajvp.AttnJvpError):
+        ajvp.selftest_wait_timeout(1_000_000, unit=3)
