@@ -102,8 +102,8 @@ double plan_time(const Plan &p, int64_t units, int64_t runs, int sm_count) {
 //
 // With a workspace the CTAs of a unit may be any number anywhere.  Long contexts of
 // few sequences then fill the GPU (one sequence of 32760 tokens, 40 heads on 8 key
-// heads, with tangents: 24 against 34 us; 12 heads without: 21 against 29; of 200000
-// tokens, one head: 36 against 73), while short ones gain a microsecond or two of
+// heads, with tangents: 24 against 35 us; 12 heads without: 21 against 28; of 200000
+// tokens, one head: 37 against 73), while short ones gain a microsecond or two of
 // kernel time and lose as much to the second launch, so from a modelled gain of
 // an eighth on.
 Plan make_plan(int64_t n_seq, int64_t Hkv, int64_t rows, bool tangent, int64_t tokens, int sm_count, bool workspace) {

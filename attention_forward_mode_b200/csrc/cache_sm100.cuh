@@ -317,8 +317,11 @@ __global__ void __launch_bounds__(APPEND_THREADS, 4) cache_append_kernel(const _
 // and measured slower: 174 instead of 132 us for 64 sequences of up to 8192
 // tokens).  Bytes of two tokens' value rows pair up as A fragments, and P^T is
 // turned by movmatrix.
-// mma.sync rather than tcgen05: 128-row accumulators in tensor memory would be
-// nearly empty, and the products are not what bounds the kernel.  Splits of a
+// mma.sync rather than tcgen05 is a choice for few query rows, not a limit: in this
+// orientation 128 tokens, or the 128 channels, would fill tcgen05's 128 rows, with 16
+// and more query columns, but its operands would have to be converted into shared
+// memory first.  That form is not built: chunks of many query tokens take every eight
+// columns' products, and their conversions, anew.  Splits of a
 // sequence are the CTAs of one cluster, which join their sums through distributed
 // shared memory in one launch; or, for long contexts of few sequences, any number of
 // CTAs that leave them in a workspace for a second kernel (make_plan in cache.cu says

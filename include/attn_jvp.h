@@ -536,7 +536,8 @@ AJVP_API int attn_jvp_cache_append(const void *k, const void *v, const void *q, 
  *                     tq NULL: no tangent (to NULL)
  *   o, to, lse      : __nv_bfloat16 [n_seq][H][n][d] and float [n_seq][H][n] (lse
  *                     may be NULL); packed: [H][total][d], [H][total]
- *   k_cache .. block_table : as attn_jvp_cache_append wrote them
+ *   k_cache .. block_table : as attn_jvp_cache_append wrote them (a scale of 0
+ *                     stands for zero keys or values)
  *   cache_lens      : DEVICE int32 [n_seq] cached tokens, the query tokens' own
  *                     included: token t of the sequence's m is at position
  *                     cache_lens[b] - m + t (m: n, or packed cu_seqlens[b + 1] -
@@ -553,8 +554,8 @@ AJVP_API int attn_jvp_cache_append(const void *k, const void *v, const void *q, 
  * Rows that see no key give zeros and lse = -infinity.  Pages outside
  * 0 .. n_pages - 1 count as hidden; lengths are clamped to the table's capacity.
  * Meant for decoding: query heads sharing a key head and their tokens are taken
- * eight (with tangents) or sixteen rows at a time, and every such tile reads the
- * sequence's codes again.  Supported: d == 128, sizes as attn_jvp_cache_append,
+ * four or eight (with tangents), or eight or sixteen rows at a time, and every
+ * such tile reads the sequence's codes again.  Supported: d == 128, sizes as attn_jvp_cache_append,
  * strides multiples of 8 elements.  With `workspace` (DEVICE memory, 256-byte
  * aligned) of attn_jvp_fwd_cache_workspace_bytes(...) bytes, long contexts of few
  * sequences may be spread over the whole GPU and joined by a second kernel;
