@@ -307,11 +307,11 @@ int attn_jvp_bwd_scored(const void *q, const void *k, const void *v, const void 
     const Sizes z{B, H, Hkv, Lq, Lk, d};
     int rc = check_sizes(z, scale, softcap);
     if (rc != AJVP_OK) return rc;
-    if (B == 0 || H == 0) return AJVP_OK;
+    if (B == 0 || Hkv == 0) return AJVP_OK;
     const cudaStream_t st = (cudaStream_t)stream;
     if ((rc = check_large(z)) != AJVP_OK) return rc;
     if (d != bwd::HD) return AJVP_ERR_UNSUPPORTED_DIM;
-    if (Lq == 0) {  // no query rows: the key-side gradients are zero
+    if (Lq == 0 || H == 0) {  // no query rows: the key-side gradients are zero
         void *zero[4] = {dk, dv, dtk, dtv};
         for (void *p : zero)
             if (!p) return AJVP_ERR_INVALID_ARG;

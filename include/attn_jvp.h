@@ -459,7 +459,8 @@ AJVP_API int attn_jvp_fwd_scored_stats(const void *q, const void *k, const void 
  * Two kernels on `stream` (three when the key side is split), no atomics.
  * Gradients of rows that see no key and of keys that no row sees are zero; all
  * inputs of such rows and keys must be finite here (q, tq, o, to, dout and dtout
- * of rows that see nothing included).  Lq == 0 writes zeros to dk, dv, dtk, dtv.
+ * of rows that see nothing included).  Lq == 0 or H == 0 writes zeros to dk, dv,
+ * dtk, dtv.
  * Other rules and errors as attn_jvp_fwd_scored, plus AJVP_ERR_WORKSPACE.
  */
 AJVP_API int attn_jvp_bwd_scored(const void *q, const void *k, const void *v,

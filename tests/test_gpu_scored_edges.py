@@ -97,3 +97,14 @@ def test_every_status_word_reports_a_wait_that_ran_out(unit):
     assert ajvp.check_device_status() == ajvp.AJVP_OK
     with pytest.raises(ajvp.AttnJvpError):
         ajvp.selftest_wait_timeout(1_000_000, unit=3)
+
+
+def test_no_query_heads_give_zero_key_gradients():
+    """H = 0 is a multiple of every Hkv: the keys' gradients are sums over nothing."""
+    inp, _ = make(1, 2, 2, 4, 50, seed=35)
+    e, z = torch.empty((1, 0, 4, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 0, 4), device="cuda")
+    full = {n: torch.full_like(inp["k"], 3.0) for n in ("dk", "dv", "dtk", "dtv")}
+    g = ajvp.attn_jvp_bwd_scored(e, inp["k"], inp["v"], e, inp["tk"], inp["tv"], e, e, z, z, e, e, grads=full)
+    assert g["dq"].shape == e.shape and all((g[n] == 0).all() for n in full)
+    o, to, lse = ajvp.attn_jvp_fwd_scored(e, inp["k"], inp["v"], e, inp["tk"], inp["tv"])
+    assert o.shape == to.shape == e.shape and lse.shape == z.shape
